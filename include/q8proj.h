@@ -88,6 +88,14 @@ typedef enum {
     Q8_ACT_I8X2 = 2   /* two-word ~14-bit int8 code (the lane's default) */
 } q8_act_mode;
 
+/* Element types of the K/V caches that attn_decode and kv_evict take
+ * (q8_proj_fused_kv writes Q8_KV_F32). */
+typedef enum {
+    Q8_KV_F32 = 0,
+    Q8_KV_F16 = 1,
+    Q8_KV_BF16 = 2
+} q8_kv_type;
+
 /* Largest activation row count one call accepts (decode batch or prefill chunk). */
 #define Q8_MAX_ROWS 256
 
@@ -103,7 +111,8 @@ int q8_last_cuda_error(void);
 /*
  * Synchronises `stream`, then reads and clears the device error word of the
  * current device: 0 = none, 1 = a bounded wait ran out, 2 = a KV-cache
- * position outside its cache (q8_proj_fused_kv).  *code receives it.
+ * position outside its cache (q8_proj_fused_kv, attn_decode, kv_evict), 3 = a
+ * sampling parameter outside its range (head_sample).  *code receives it.
  */
 q8_status q8_device_error(int32_t* code /* host */, void* stream);
 
@@ -285,6 +294,107 @@ q8_status head_argmax_noalloc(int mode, const int8_t* q, const uint16_t* s, int6
                               int64_t K, const void* xq, const float* xd, int64_t rows,
                               int32_t* tok, double* maxval, void* logits, void* stream);
 size_t head_argmax_noalloc_scratch_bytes(void);
+
+/*
+ * Attention of a decode step: one new token a sequence, over the caches that
+ * q8_proj_fused_kv writes, with a sliding window and first tokens ("sinks")
+ * that stay visible.  The pages describe no attention kernel; this is the
+ * step's operator between the QKV projection and Wo.
+ *   q        float, row m at q + m * ldq: [heads][head_dim] (the first
+ *            columns of the QKV projection's output: ldq = its N);
+ *            ldq >= heads * head_dim
+ *   k_cache, v_cache  [rows][n_pos][kv_heads * head_dim] of kv_type; query
+ *            head g reads K/V head g / (heads / kv_heads)
+ *   pos      int32 [rows], device memory, read by the launch: row m's newest
+ *            cache entry.  Visible are the entries i in [0, pos[m]] with
+ *            i < sinks or i > pos[m] - window; window = -1: all of them.
+ *   out[m][g] = sum_i p_i v_i, p = softmax_i(scale * q_g . k_i) over the
+ *            visible i; row m at out + m * ldo, ldo >= heads * head_dim
+ *   acc      float [rows][kv_heads][n_pos] or NULL: acc[m][h][i] += the sum
+ *            over the query heads of K/V head h of p_i (what kv_evict ranks);
+ *            entries that are not visible keep their values
+ * A row with nothing visible (pos[m] = -1, or window = 0 and sinks = 0) gives
+ * zeros and leaves acc as it was; a position outside [-1, n_pos) does the
+ * same and sets device error 2.  What an entry that is not visible holds
+ * (NaN, infinity) does not matter.  Scores, weights and sums are binary32;
+ * the result does not depend on what else runs (no atomics on values).
+ * 1 <= rows <= Q8_MAX_ROWS; heads a multiple of kv_heads, heads <= 1024;
+ * head_dim a multiple of 8, 8 <= head_dim <= 256; 1 <= n_pos <= 2^31 - 1, each
+ * cache at most 2^40 bytes; window >= -1, sinks >= 0; out overlaps no input.
+ *   workspace: attn_decode_workspace(...) bytes for the same arguments (with_acc:
+ *   acc is given), zeroed whole before the first call on it; every completed
+ *   call leaves what it counts with at zero, so that calls of any sizes may
+ *   follow one another on one workspace.  Calls sharing it must not overlap.
+ *   (0 bytes: arguments that attn_decode refuses.)
+ */
+q8_status attn_decode(const float* q, int64_t ldq, const void* k_cache, const void* v_cache,
+                      int kv_type, int64_t rows, int64_t n_pos, int64_t heads, int64_t kv_heads,
+                      int64_t head_dim, const int32_t* pos, int64_t window, int64_t sinks,
+                      float scale, float* out, int64_t ldo, float* acc, void* workspace,
+                      size_t ws_bytes, void* stream);
+size_t attn_decode_workspace(int64_t rows, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                             int64_t n_pos, int64_t window, int64_t sinks, int with_acc);
+
+/*
+ * Eviction from the K/V caches by accumulated attention weight, in place.
+ *   k_cache, v_cache, kv_type, pos  as attn_decode; row m holds pos[m] + 1
+ *            entries (pos[m] = -1: none)
+ *   acc      float [rows][kv_heads][n_pos], what attn_decode accumulated
+ * A row of more than `budget` entries keeps, in each K/V head by itself, the
+ * first `sinks`, the last `recent`, and of those between them the
+ * budget - sinks - recent with the largest acc (ties: the lowest index; NaN
+ * counts as lowest).  They move to the front in their order: K, V, and acc
+ * into new_acc, which is 0 from `budget` on; new_pos[m] = budget - 1, so that
+ * the next token's entry goes to row `budget`.  Cache rows from `budget` on
+ * keep what they held.  A row of at most `budget` entries keeps its caches;
+ * its acc and pos are copied.
+ *   new_pos  int32 [rows], may be pos itself
+ *   new_acc  float [rows][kv_heads][n_pos], may be acc itself; otherwise
+ *            neither may overlap its source (Q8_ERR_ARG)
+ *   kept     int32 [rows][kv_heads][budget] or NULL: the entry that new row j
+ *            held before; -1 behind a shorter row's last entry
+ * A position outside [-1, n_pos) leaves its row as it was (kept: -1) and sets
+ * device error 2.  1 <= budget <= n_pos, sinks + recent <= budget, other
+ * limits as attn_decode.
+ *   workspace: kv_evict_workspace(rows, kv_heads, budget) bytes, of any content.
+ */
+q8_status kv_evict(void* k_cache, void* v_cache, int kv_type, int64_t rows, int64_t n_pos,
+                   int64_t kv_heads, int64_t head_dim, const int32_t* pos, const float* acc,
+                   int64_t budget, int64_t sinks, int64_t recent, int32_t* new_pos, float* new_acc,
+                   int32_t* kept, void* workspace, size_t ws_bytes, void* stream);
+size_t kv_evict_workspace(int64_t rows, int64_t kv_heads, int64_t budget);
+
+/*
+ * Sampling of one token a row from the head's logits (q8_proj's float output,
+ * or head_argmax's in the int8 modes), beside the arg-max that head_argmax
+ * takes, from given random numbers.
+ *   logits   float, row m at logits + m * ldl, N values; ldl >= N
+ *   u        float [rows], the uniform number in [0, 1) that draws the token
+ *            (below 0 or NaN counts as 0, 1 and above as the last one)
+ *   temperature, top_k, top_p, min_p  one a row, each NULL for "off" (1, 0,
+ *            1, 0): device memory, read by the launch
+ * With M the row's maximum, w_i = exp((x_i - M) / temperature); the tokens in
+ * order of x (ties: the lowest index first) are cut to the first top_k (<= 0:
+ * all), then to the shortest beginning that holds at least top_p of the mass
+ * left (>= 1: all), then to those with w_i >= min_p; the first always stays.
+ *   tok[m]   the smallest kept i whose sum of w over the kept j <= i exceeds
+ *            u times their whole sum (u = 0: the lowest kept one)
+ *   prob     float [rows] or NULL: w over that sum, for the token
+ *   kept     int32 [rows] or NULL: how many tokens were kept
+ * temperature 0 (or below 2^-60) takes the arg-max (prob 1, kept 1).  Logits of -inf
+ * or NaN are never drawn; where there are +inf, those weigh 1 and all others
+ * 0.  A row without any other logit gives token 0, prob 0 and kept 0; so does
+ * a row whose temperature is negative or NaN, or whose top_p or min_p is NaN,
+ * which also sets device error 3.  Weights are integers in units of
+ * 2^-(62 - ceil(log2 N)) of the largest, computed to about 2^-40 of their
+ * value, and their sums are exact: a row's token depends on nothing but its
+ * own row and settings.
+ * 1 <= rows <= Q8_MAX_ROWS, 1 <= N <= 2^20, logits 16-byte aligned, the
+ * others 4-byte.  No workspace.
+ */
+q8_status head_sample(const float* logits, int64_t ldl, int64_t rows, int64_t N, const float* u,
+                      const float* temperature, const int32_t* top_k, const float* top_p,
+                      const float* min_p, int32_t* tok, float* prob, int32_t* kept, void* stream);
 
 /*
  * Debug: the per-block int32 dot products the projections fold with their

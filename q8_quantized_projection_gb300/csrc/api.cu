@@ -1,6 +1,9 @@
 // api.cu -- the C ABI of libq8proj (declared in include/q8proj.h): argument
 // validation on the host, then launches of the kernels on the caller's stream.
+#include <math.h>
+
 #include <atomic>
+#include <cfloat>
 #include <mutex>
 
 #include "common.cuh"
@@ -464,6 +467,138 @@ q8_status q8_debug_block_dots(int mode, const int8_t* q, const void* xq, int64_t
         return launched(launch_chunk_debug(mode, q, N, K, xq, rows, isum, ctx));
     }
     return launched(launch_debug_dots(mode, q, xq, N, K, rows, isum, ctx));
+}
+
+// ---------------------------------------------- the decode step's other operators
+
+// Sizes of a K/V cache [rows][n_pos][kv_heads * dim]: what attn_decode and
+// kv_evict take; *bytes receives one cache's size.
+static q8_status check_cache(int kv_type, int64_t rows, int64_t n_pos, int64_t kv_heads, int64_t dim,
+                             size_t* bytes) {
+    if (kv_type < Q8_KV_F32 || kv_type > Q8_KV_BF16) return Q8_ERR_MODE;
+    if (rows < 1 || rows > Q8_MAX_ROWS || n_pos < 1 || n_pos > INT32_MAX) return Q8_ERR_SHAPE;
+    if (kv_heads < 1 || kv_heads > kMaxHeads || dim < 8 || dim > 256 || dim % 8) return Q8_ERR_SHAPE;
+    const int64_t elt = kv_type == Q8_KV_F32 ? 4 : 2;
+    if (n_pos > (int64_t(1) << 40) / (rows * kv_heads * dim * elt)) return Q8_ERR_SHAPE;
+    *bytes = size_t(rows) * size_t(n_pos) * size_t(kv_heads * dim * elt);
+    return Q8_OK;
+}
+
+// [a, a + na) and [b, b + nb) overlap (either NULL: no)
+static bool overlaps2(const void* a, size_t na, const void* b, size_t nb) {
+    if (!a || !b) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+static q8_status check_attn(int kv_type, int64_t rows, int64_t n_pos, int64_t heads, int64_t kv_heads,
+                            int64_t dim, int64_t window, int64_t sinks, size_t* cache) {
+    const q8_status st = check_cache(kv_type, rows, n_pos, kv_heads, dim, cache);
+    if (st != Q8_OK) return st;
+    if (heads < kv_heads || heads > kMaxHeads || heads % kv_heads) return Q8_ERR_SHAPE;
+    if (window < -1 || sinks < 0) return Q8_ERR_SHAPE;
+    return Q8_OK;
+}
+
+size_t attn_decode_workspace(int64_t rows, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                             int64_t n_pos, int64_t window, int64_t sinks, int with_acc) {
+    size_t cache;
+    if (check_attn(Q8_KV_F16, rows, n_pos, heads, kv_heads, head_dim, window, sinks, &cache) != Q8_OK)
+        return 0;
+    return attn_workspace_bytes(rows, heads, kv_heads, head_dim, n_pos, window, sinks, with_acc != 0);
+}
+
+q8_status attn_decode(const float* q, int64_t ldq, const void* k_cache, const void* v_cache,
+                      int kv_type, int64_t rows, int64_t n_pos, int64_t heads, int64_t kv_heads,
+                      int64_t head_dim, const int32_t* pos, int64_t window, int64_t sinks,
+                      float scale, float* out, int64_t ldo, float* acc, void* workspace,
+                      size_t ws_bytes, void* stream) {
+    if (!q || !k_cache || !v_cache || !pos || !out) return Q8_ERR_ARG;
+    size_t cache;
+    q8_status st = check_attn(kv_type, rows, n_pos, heads, kv_heads, head_dim, window, sinks, &cache);
+    if (st != Q8_OK) return st;
+    const int64_t width = heads * head_dim, max_ld = int64_t(1) << 31;
+    if (ldq < width || ldo < width || ldq > max_ld || ldo > max_ld) return Q8_ERR_SHAPE;
+    if (!(fabsf(scale) <= FLT_MAX)) return Q8_ERR_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(pos) ||
+        !aligned16(out) || (acc && !aligned16(acc)))
+        return Q8_ERR_ALIGN;
+    const size_t qn = size_t((rows - 1) * ldq + width) * 4, on = size_t((rows - 1) * ldo + width) * 4;
+    const size_t an = size_t(rows * kv_heads) * size_t(n_pos) * 4, pn = size_t(rows) * 4;
+    if (overlaps2(out, on, q, qn) || overlaps2(out, on, k_cache, cache) ||
+        overlaps2(out, on, v_cache, cache) || overlaps2(out, on, acc, an) || overlaps2(out, on, pos, pn) ||
+        overlaps2(acc, an, q, qn) || overlaps2(acc, an, k_cache, cache) ||
+        overlaps2(acc, an, v_cache, cache) || overlaps2(acc, an, pos, pn))
+        return Q8_ERR_ARG;
+    if (!workspace ||
+        ws_bytes < attn_workspace_bytes(rows, heads, kv_heads, head_dim, n_pos, window, sinks, acc != nullptr))
+        return Q8_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return Q8_ERR_ALIGN;
+    LaunchCtx ctx;
+    if ((st = make_ctx(stream, ctx)) != Q8_OK) return st;
+    const AttnArgs a{q,   ldq,    k_cache, v_cache, kv_type, rows, n_pos, heads, kv_heads, head_dim,
+                     pos, window, sinks,   scale,   out,     ldo,  acc,   workspace};
+    return launched(launch_attn(a, ctx));
+}
+
+size_t kv_evict_workspace(int64_t rows, int64_t kv_heads, int64_t budget) {
+    if (rows < 1 || rows > Q8_MAX_ROWS || kv_heads < 1 || kv_heads > kMaxHeads || budget < 1 ||
+        budget > INT32_MAX)
+        return 0;
+    return evict_workspace_bytes(rows, kv_heads, budget);
+}
+
+q8_status kv_evict(void* k_cache, void* v_cache, int kv_type, int64_t rows, int64_t n_pos,
+                   int64_t kv_heads, int64_t head_dim, const int32_t* pos, const float* acc,
+                   int64_t budget, int64_t sinks, int64_t recent, int32_t* new_pos, float* new_acc,
+                   int32_t* kept, void* workspace, size_t ws_bytes, void* stream) {
+    if (!k_cache || !v_cache || !pos || !acc || !new_pos || !new_acc) return Q8_ERR_ARG;
+    size_t cache;
+    q8_status st = check_cache(kv_type, rows, n_pos, kv_heads, head_dim, &cache);
+    if (st != Q8_OK) return st;
+    if (budget < 1 || budget > n_pos || sinks < 0 || recent < 0 || sinks > budget ||
+        recent > budget - sinks)
+        return Q8_ERR_SHAPE;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(pos) || !aligned16(acc) ||
+        !aligned16(new_pos) || !aligned16(new_acc) || (kept && !aligned16(kept)))
+        return Q8_ERR_ALIGN;
+    const size_t an = size_t(rows * kv_heads) * size_t(n_pos) * 4, pn = size_t(rows) * 4;
+    const size_t kn = size_t(rows * kv_heads) * size_t(budget) * 4;
+    // every buffer that is written is disjoint from every other one
+    const struct { const void* p; size_t n; bool written; } b[] = {
+        {k_cache, cache, true}, {v_cache, cache, true}, {pos, pn, false},    {acc, an, false},
+        {new_pos, pn, true},    {new_acc, an, true},    {kept, kn, true}};
+    for (int i = 0; i < 7; ++i)
+        for (int j = 0; j < i; ++j) {
+            if (!b[i].written && !b[j].written) continue;
+            if ((i == 4 && j == 2 && new_pos == pos) || (i == 5 && j == 3 && new_acc == acc)) continue;
+            if (overlaps2(b[i].p, b[i].n, b[j].p, b[j].n)) return Q8_ERR_ARG;
+        }
+    if (!workspace || ws_bytes < evict_workspace_bytes(rows, kv_heads, budget)) return Q8_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return Q8_ERR_ALIGN;
+    LaunchCtx ctx;
+    if ((st = make_ctx(stream, ctx)) != Q8_OK) return st;
+    const EvictArgs a{k_cache, v_cache, kv_type, rows,    n_pos,   kv_heads, head_dim, pos,
+                      acc,     budget,  sinks,   recent,  new_pos, new_acc,  kept,     workspace};
+    return launched(launch_evict(a, ctx));
+}
+
+q8_status head_sample(const float* logits, int64_t ldl, int64_t rows, int64_t N, const float* u,
+                      const float* temperature, const int32_t* top_k, const float* top_p,
+                      const float* min_p, int32_t* tok, float* prob, int32_t* kept, void* stream) {
+    if (!logits || !u || !tok) return Q8_ERR_ARG;
+    if (rows < 1 || rows > Q8_MAX_ROWS || N < 1 || N > kSampleMaxN || ldl < N ||
+        ldl > (int64_t(1) << 31))
+        return Q8_ERR_SHAPE;
+    const void* per_row[] = {u, temperature, top_k, top_p, min_p, tok, prob, kept};
+    for (const void* p : per_row)
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return Q8_ERR_ALIGN;
+    if (!aligned16(logits)) return Q8_ERR_ALIGN;
+    LaunchCtx ctx;
+    q8_status st = make_ctx(stream, ctx);
+    if (st != Q8_OK) return st;
+    const SampleArgs a{logits, ldl, rows, N, u, temperature, top_k, top_p, min_p, tok, prob, kept};
+    return launched(launch_sample(a, ctx));
 }
 
 }  // extern "C"

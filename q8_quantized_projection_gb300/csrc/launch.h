@@ -152,4 +152,61 @@ static_assert(gemv_max_rows(0) <= kArgmaxGroupRows && gemv_max_rows(1) <= kArgma
                   gemv_max_rows(2) <= kArgmaxGroupRows,
               "the arg-max workspace holds one candidate per CTA and row of a group");
 
+// --------------------------------------------- the decode step's other operators
+
+constexpr int64_t kMaxHeads = 1024;                 // query or K/V heads of one call
+constexpr int64_t kSampleMaxN = int64_t(1) << 20;   // logits of one row
+
+// Attention of one token a sequence over its K/V cache (attn.cu).
+struct AttnArgs {
+    const float* q;
+    int64_t ldq;
+    const void* k;       // [rows][n_pos][kv_heads][dim], of type kv_type
+    const void* v;
+    int kv_type;
+    int64_t rows, n_pos, heads, kv_heads, dim;
+    const int32_t* pos;
+    int64_t window, sinks;
+    float scale;
+    float* out;
+    int64_t ldo;
+    float* acc;          // [rows][kv_heads][n_pos], or NULL
+    void* ws;
+};
+size_t attn_workspace_bytes(int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim, int64_t n_pos,
+                            int64_t window, int64_t sinks, bool acc);
+cudaError_t launch_attn(const AttnArgs& a, const LaunchCtx& ctx);
+
+// Eviction from the K/V caches by accumulated weight (evict.cu).
+struct EvictArgs {
+    void* k;
+    void* v;
+    int kv_type;
+    int64_t rows, n_pos, kv_heads, dim;
+    const int32_t* pos;
+    const float* acc;
+    int64_t budget, sinks, recent;
+    int32_t* new_pos;
+    float* new_acc;
+    int32_t* kept;       // [rows][kv_heads][budget], or NULL
+    void* ws;
+};
+size_t evict_workspace_bytes(int64_t rows, int64_t kv_heads, int64_t budget);
+cudaError_t launch_evict(const EvictArgs& a, const LaunchCtx& ctx);
+
+// Sampling from the head's logits (sample.cu).
+struct SampleArgs {
+    const float* x;
+    int64_t ldx, rows, N;
+    const float* u;
+    const float* temperature;   // these four: one a row, or NULL (off)
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    int32_t* tok;
+    float* prob;                // or NULL
+    int32_t* kept;              // or NULL
+};
+cudaError_t launch_sample(const SampleArgs& a, const LaunchCtx& ctx);
+
 }  // namespace q8

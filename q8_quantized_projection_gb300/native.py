@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(PKG, "libq8proj.so")
 
 Q8_ACT_F32, Q8_ACT_I8, Q8_ACT_I8X2 = 0, 1, 2
 MODES = {"f32": Q8_ACT_F32, "i8": Q8_ACT_I8, "i8x2": Q8_ACT_I8X2}
+Q8_KV_F32, Q8_KV_F16, Q8_KV_BF16 = 0, 1, 2
 Q8_MAX_ROWS = 256
 
 _STATUS = ["Q8_OK", "Q8_ERR_ARG", "Q8_ERR_SHAPE", "Q8_ERR_ALIGN", "Q8_ERR_MODE",
@@ -47,6 +48,13 @@ SIGNATURES = {
     "head_argmax": (_int, [_int, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _sz,
                            _vp]),
     "head_argmax_workspace": (_sz, [_i64]),
+    "attn_decode": (_int, [_vp, _i64, _vp, _vp, _int, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64,
+                           C.c_float, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "attn_decode_workspace": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64, _i64, _int]),
+    "kv_evict": (_int, [_vp, _vp, _int, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _vp,
+                        _vp, _vp, _sz, _vp]),
+    "kv_evict_workspace": (_sz, [_i64, _i64, _i64]),
+    "head_sample": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "q8_debug_block_dots": (_int, [_int, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp]),
     "q8_debug_row_geometry": (_int, [_int, _i64, _i64, _i64, _int, _int, _vp]),
     "q8_debug_row_geometry_fused": (_int, [_int, _int, _i64, _i64, _int, _int, _vp]),
@@ -228,6 +236,127 @@ def head_argmax_noalloc(mode, q, s, xq, xd, rows, tok, maxval=None, logits=None,
                                       _stream(stream)), "head_argmax_noalloc")
 
 
+def _need(what, t, dtype, shape, device, dense=True):
+    """A tensor argument that the C call reads by pointer: its type, shape,
+    device and (dense) layout.  shape: None where any size may stand."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if len(t.shape) != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, not {t.device}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _row_pitch(what, t, dtype, rows, device):
+    """The elements from one row to the next of a 2-D tensor with dense rows."""
+    _need(what, t, dtype, (rows, None), device, dense=False)
+    if t.stride(1) != 1 and t.shape[1] != 1:
+        raise ValueError(f"{what} must have dense rows")
+    return t.stride(0) if rows != 1 else t.shape[1]
+
+
+def _on_current_device(what, t):
+    """The device of a call's first tensor, which must be the current one."""
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}; calls run on the current CUDA device")
+    return t.device
+
+
+def _kv_type(what, t):
+    import torch
+    types = {torch.float32: Q8_KV_F32, torch.float16: Q8_KV_F16, torch.bfloat16: Q8_KV_BF16}
+    if t.dtype not in types:
+        raise TypeError(f"{what} must be float32, float16 or bfloat16, not {t.dtype}")
+    return types[t.dtype]
+
+
+def _kv_caches(k_cache, v_cache, kv_heads):
+    """(device, kv type, rows, n_pos, head_dim) of a pair of caches
+    [rows, n_pos, kv_heads * head_dim]."""
+    device = _on_current_device("k_cache", k_cache)
+    kv = _kv_type("k_cache", k_cache)
+    _need("k_cache", k_cache, k_cache.dtype, (None, None, None), device)
+    _need("v_cache", v_cache, k_cache.dtype, tuple(k_cache.shape), device)
+    rows, n_pos, kv_dim = k_cache.shape
+    if kv_heads < 1 or kv_dim % kv_heads:
+        raise ValueError(f"cache rows of {kv_dim} values do not hold {kv_heads} heads")
+    return device, kv, rows, n_pos, kv_dim // kv_heads
+
+
+def attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window=-1, sinks=0, acc=False) -> int:
+    return int(load().attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window, sinks,
+                                            1 if acc else 0))
+
+
+def attn_decode(q, k_cache, v_cache, pos, out, workspace, heads, kv_heads, window=-1, sinks=0,
+                scale=None, acc=None, stream=None):
+    """q, out: [rows, >= heads * head_dim] float32 with any row pitch; caches
+    [rows, n_pos, kv_heads * head_dim]; pos int32 [rows]; acc float32
+    [rows, kv_heads, n_pos] or None; scale None: 1 / sqrt(head_dim)."""
+    import torch
+    device, kv, rows, n_pos, dim = _kv_caches(k_cache, v_cache, kv_heads)
+    ldq = _row_pitch("q", q, torch.float32, rows, device)
+    ldo = _row_pitch("out", out, torch.float32, rows, device)
+    if min(q.shape[1], out.shape[1]) < heads * dim:
+        raise ValueError(f"rows of q and out must hold {heads} heads of {dim} values")
+    _need("pos", pos, torch.int32, (rows,), device)
+    if acc is not None:
+        _need("acc", acc, torch.float32, (rows, kv_heads, n_pos), device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    _check(load().attn_decode(_ptr(q), ldq, _ptr(k_cache), _ptr(v_cache), kv, rows, n_pos, heads,
+                              kv_heads, dim, _ptr(pos), window, sinks,
+                              dim ** -0.5 if scale is None else float(scale), _ptr(out), ldo, _ptr(acc),
+                              _ptr(workspace), workspace.numel() * workspace.element_size(),
+                              _stream(stream)), "attn_decode")
+
+
+def kv_evict_workspace(rows, kv_heads, budget) -> int:
+    return int(load().kv_evict_workspace(rows, kv_heads, budget))
+
+
+def kv_evict(k_cache, v_cache, pos, acc, new_pos, new_acc, workspace, kv_heads, budget, sinks=0,
+             recent=0, kept=None, stream=None):
+    """Caches and acc as attn_decode; new_pos, new_acc may be pos, acc; kept
+    int32 [rows, kv_heads, budget] or None."""
+    import torch
+    device, kv, rows, n_pos, dim = _kv_caches(k_cache, v_cache, kv_heads)
+    for what, t in (("pos", pos), ("new_pos", new_pos)):
+        _need(what, t, torch.int32, (rows,), device)
+    for what, t in (("acc", acc), ("new_acc", new_acc)):
+        _need(what, t, torch.float32, (rows, kv_heads, n_pos), device)
+    if kept is not None:
+        _need("kept", kept, torch.int32, (rows, kv_heads, budget), device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    _check(load().kv_evict(_ptr(k_cache), _ptr(v_cache), kv, rows, n_pos, kv_heads, dim, _ptr(pos),
+                           _ptr(acc), budget, sinks, recent, _ptr(new_pos), _ptr(new_acc), _ptr(kept),
+                           _ptr(workspace), workspace.numel() * workspace.element_size(),
+                           _stream(stream)), "kv_evict")
+
+
+def head_sample(logits, u, tok, temperature=None, top_k=None, top_p=None, min_p=None, prob=None,
+                kept=None, stream=None):
+    """logits float32 [rows, N] with any row pitch; u, temperature, top_p,
+    min_p, prob float32 [rows]; top_k, tok, kept int32 [rows]."""
+    import torch
+    device = _on_current_device("logits", logits)
+    rows, n = logits.shape
+    ldl = _row_pitch("logits", logits, torch.float32, rows, device)
+    for what, t, dtype in (("u", u, torch.float32), ("temperature", temperature, torch.float32),
+                           ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32),
+                           ("min_p", min_p, torch.float32), ("tok", tok, torch.int32),
+                           ("prob", prob, torch.float32), ("kept", kept, torch.int32)):
+        if t is not None:
+            _need(what, t, dtype, (rows,), device)
+    _check(load().head_sample(_ptr(logits), ldl, rows, n, _ptr(u), _ptr(temperature), _ptr(top_k),
+                              _ptr(top_p), _ptr(min_p), _ptr(tok), _ptr(prob), _ptr(kept),
+                              _stream(stream)), "head_sample")
+
+
 def q8_debug_block_dots(mode, q, xq, rows, isum, path=0, stream=None):
     n, k = q.shape
     _check(load().q8_debug_block_dots(_mode(mode), _ptr(q), _ptr(xq), n, k, rows, _ptr(isum),
@@ -291,6 +420,15 @@ def activation_buffers(mode, rows, k, device="cuda"):
     xq = torch.empty((planes, rows, k), dtype=torch.int8, device=device)
     xd = torch.empty((rows, k // 32), dtype=torch.float32, device=device)
     return (xq[0] if planes == 1 else xq), xd
+
+
+def attn_workspace(rows, heads, kv_heads, head_dim, n_pos, window=-1, sinks=0, acc=False, device="cuda"):
+    """A zeroed attn_decode workspace (its counters must start at zero)."""
+    import torch
+    nbytes = attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window, sinks, acc)
+    if nbytes == 0:
+        raise Q8Error(2, "attn_decode_workspace")
+    return torch.zeros((nbytes + 15) // 16 * 16, dtype=torch.uint8, device=device)
 
 
 def argmax_workspace(rows, device="cuda"):
