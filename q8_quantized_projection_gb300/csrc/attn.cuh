@@ -1,0 +1,592 @@
+// attn.cuh -- attention of one token a sequence over its K/V cache: the kernel
+// template and its launch (one translation unit a cache type).
+//
+// Mathematics.  With s_i = scale q.k_i (in units of log 2), one pass over K and
+// V keeps a reference r, l = sum 2^(s_i - r) and o = sum 2^(s_i - r) v_i; r
+// moves (and l, o are rescaled) only when a score exceeds it by more than 2^3,
+// which binary32 takes without loss.  States over parts of the entries join by
+// the same rule, so the entries may be split anywhere.  Scores, weights and
+// sums are binary32 throughout.
+//
+// What bounds it.  Each K and V value is read once and used in one multiply-add
+// a query head: with 4 heads a K/V head that is 1 (f32) or 2 (16-bit) FMA a
+// byte, below what the FMA pipes give at full HBM bandwidth.  So the kernel
+// streams: every warp owns a ring of stages in shared memory that it fills
+// with 16-byte cp.async and consumes alone -- no barrier between warps, about
+// 128 KB in flight an SM.
+//
+// Layout.  LPK lanes share an entry, each with DPL of its values in registers
+// (q and o of NG query heads: 64 + 64 registers at most); a warp takes 32/LPK
+// entries at a time, U times a stage.  A stage's U x NG partial scores are
+// summed over the LPK lanes by halving exchanges (each step leaves a lane half
+// the values), so that each lane ends with few scores, exponentiates those
+// only, and hands them back by shuffles.
+//
+// Split.  A unit is a row's K/V head (and block of at most 8 query heads); its
+// visible entries are tiles of 4 warps x KT (several such where the tiles would
+// not fit 32 bits), and it counts EXTRA tiles more for what it costs to begin
+// and end.  The tiles of all units in one line are cut evenly over the CTAs, so
+// ragged batches balance and one long sequence fills the GPU; lengths are read
+// on the device, so one captured graph serves every step.  Two CTAs of four
+// warps an SM: one streams while the other ends a unit.  A unit cut between CTAs leaves
+// partial states in the workspace; the CTA that finishes it last (a ticket)
+// joins them in CTA order, so results repeat bit for bit.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "q8proj.h"
+
+namespace q8 {
+
+constexpr int kAttnWarps = 4;                         // two CTAs an SM
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kAttnRing = 24 * 1024;                  // bytes a warp
+constexpr int kAttnMaxCtas = 512;
+constexpr size_t kAttnHeader = 4 * kAttnMaxCtas;      // one ticket a CTA
+
+struct AttnParams {
+    AttnArgs a;
+    int nb, gsz;          // blocks of query heads a K/V head, heads a block
+    int tile_its;         // stages a warp takes in one tile
+    int64_t cap;          // entries of a row that can be visible
+    float* part;          // [2 * CTAs][NG][D + 2]: o, r, l
+    float2* ml;           // [rows][heads]: reference and 1 / sum (acc)
+    float* scores;        // [rows][heads][cap] (acc)
+    float qscale;         // scale * log2(e)
+    int* err;
+};
+
+// The visible entries in order: entry v of nvis is cache row v + (v < ns ? 0 : gap).
+struct Visible {
+    int64_t nvis, ns, gap;
+};
+
+__device__ __forceinline__ Visible visible(int pos, int64_t n_pos, int64_t window, int64_t sinks) {
+    if (pos < -1 || pos >= n_pos) return {0, 0, 0};
+    const int64_t n = int64_t(pos) + 1;
+    if (window < 0 || window >= n) return {n, n, 0};
+    const int64_t ns = sinks < n - window ? sinks : n - window;
+    return {ns + window, ns, n - window - ns};
+}
+
+typedef unsigned long long f32x2;   // two binary32 values
+
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {   // within 2^-22 of 2^x, relative
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 16 bytes from global to shared memory, or 16 zero bytes (nothing is read).
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool read) {
+    const int n = read ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The 16 bytes of a chunk as pairs of binary32 (both 16-bit types convert exactly).
+template <int KV>
+__device__ __forceinline__ void chunk_pairs(int4 c, f32x2* out) {
+    if constexpr (KV == Q8_KV_F32) {
+        out[0] = pack2(__int_as_float(c.x), __int_as_float(c.y));
+        out[1] = pack2(__int_as_float(c.z), __int_as_float(c.w));
+    } else {
+        const int w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (KV == Q8_KV_BF16) {
+                out[i] = pack2(__int_as_float(w[i] << 16), __int_as_float(w[i] & int(0xffff0000)));
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                out[i] = pack2(f.x, f.y);
+            }
+        }
+    }
+}
+
+template <int KV, int NG, int LPK>
+struct AttnShape {
+    static constexpr int ELT = KV == Q8_KV_F32 ? 4 : 2;
+    static constexpr int CD = 16 / ELT;                       // values a 16-byte chunk
+    static constexpr int DPL = NG <= 4 ? 16 : 8;              // values a lane
+    static constexpr int NC = DPL / CD;                       // chunks a lane
+    static constexpr int NP = DPL / 2;                        // pairs a lane
+    static constexpr int DMAX = DPL * LPK;
+    static constexpr int PITCH = DMAX * ELT;                  // bytes an entry in a stage
+    static constexpr int KPS = 32 / LPK;                      // entries a warp takes at a time
+    static constexpr int U = NG == 8 ? 2 : KV == Q8_KV_F32 ? 2 : 4;
+    static constexpr int KT = KPS * U;                        // entries a stage
+    static constexpr int HALF = KT * PITCH;                   // bytes of K (and of V) a stage
+    static constexpr int S0 = kAttnRing / (2 * HALF);
+    static constexpr int S = S0 > 6 ? 6 : S0;                 // stages
+    static constexpr int TK = kAttnWarps * KT;                // entries a stage of all warps
+    static constexpr int EXTRA = (48 * 1024 + kAttnWarps * 2 * HALF - 1) / (kAttnWarps * 2 * HALF);
+    static constexpr int NV = U * NG;                         // scores of an entry group a stage
+    static constexpr int R = NV > LPK ? NV / LPK : 1;         // scores a lane ends with
+    static constexpr int DUP = LPK > NV ? LPK / NV : 1;       // lanes holding the same scores
+    static constexpr int LG = LPK / NG;                       // lanes a query head
+    static_assert(S >= 2 && LG >= 1 && U % R == 0 && R * LPK >= NV, "attention tile");
+    static_assert(NG * DMAX * 4 + NG * 8 <= kAttnRing, "a warp's state fits its ring");
+};
+
+template <int KV, int NG, int LPK>
+__global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams p) {
+    using T = AttnShape<KV, NG, LPK>;
+    extern __shared__ __align__(128) unsigned char ring_all[];
+    __shared__ uint32_t s_pre[Q8_MAX_ROWS + 1];   // tiles before each row
+    __shared__ uint32_t s_warp[kAttnWarps];
+    __shared__ int s_pos[Q8_MAX_ROWS];
+    __shared__ __align__(16) float s_q[NG * T::DMAX];
+    __shared__ float s_m[kAttnWarps][NG], s_l[kAttnWarps][NG];
+    __shared__ int s_last;
+    const AttnArgs& a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int sl = lane % LPK, grp = lane / LPK, grp0 = lane - sl;
+    const int D = int(a.dim), rows = int(a.rows);
+    const uint32_t per_row = uint32_t(a.kv_heads) * p.nb;
+    const int TT = T::TK * p.tile_its;                     // entries a tile
+    unsigned char* ring = ring_all + warp * kAttnRing;
+    const uint32_t ring_s = smem_u32(ring);
+    const int gl = sl / T::LG;                             // this lane's query head of the block
+    const int u0 = (sl / T::DUP) * T::R % T::U;            // and its first of R entry steps
+    const int swz = LPK == 4 ? (grp & 1) * 4 : 0;          // rows next to each other on other banks
+
+    // values behind D are never copied; they stay zero
+    if (D < T::DMAX) {
+        for (int i = lane; i < kAttnRing / 16; i += 32) reinterpret_cast<int4*>(ring)[i] = int4{0, 0, 0, 0};
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // tiles of each row (a row with nothing visible has one, which writes its zeros)
+    {
+        constexpr int PER = (Q8_MAX_ROWS + kAttnThreads - 1) / kAttnThreads;
+        uint32_t n[PER], x = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int m = tid * PER + i;
+            if (m < rows) {
+                const int pos = a.pos[m];
+                s_pos[m] = pos;
+                if (blockIdx.x == 0 && (pos < -1 || pos >= a.n_pos)) atomicExch(p.err, Q8_DEVERR_POSITION);
+                // (up to 2^31 - 1 entries, so 32 bits hold the rounding up)
+                const uint32_t nvis = uint32_t(visible(pos, a.n_pos, a.window, a.sinks).nvis);
+                x += ((nvis ? (nvis + TT - 1) / TT : 1) + T::EXTRA) * per_row;
+            }
+            n[i] = x;
+        }
+        const uint32_t own = x;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) x += s_warp[w];
+        if (tid == 0) s_pre[0] = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) s_pre[tid * PER + i + 1] = x - own + n[i];
+        __syncthreads();
+    }
+    // CTA c has tiles [first(c), first(c + 1)): W in equal shares, the first ones
+    // one longer, none below 4 (a shorter share costs more to join than it saves)
+    const uint32_t W = s_pre[rows];
+    const uint32_t ctas = max(min(W / 4, gridDim.x), 1u), cta = blockIdx.x;
+    if (cta >= ctas) return;
+    const uint32_t share = W / ctas, longer = W % ctas;
+    const auto first = [&](uint32_t c) { return c * share + min(c, longer); };
+    const auto owner = [&](uint32_t tile) {
+        const uint32_t edge = longer * (share + 1);
+        return tile < edge ? tile / (share + 1) : longer + (tile - edge) / share;
+    };
+    const uint32_t t_begin = first(cta), t_end = first(cta + 1);
+    uint32_t t0 = t_begin;
+
+    while (t0 < t_end) {
+        // the segment: tiles [t0, t1) of unit (m, h, b)
+        int lo = 0, hi = rows - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (s_pre[mid] <= t0) lo = mid; else hi = mid - 1;
+        }
+        const int m = lo;
+        const uint32_t span = (s_pre[m + 1] - s_pre[m]) / per_row, tiles = span - T::EXTRA;
+        const uint32_t unit = (t0 - s_pre[m]) / span;
+        const uint32_t unit0 = s_pre[m] + unit * span;              // the unit's first tile
+        if (t0 >= unit0 + tiles) {                                  // in its extra ones
+            t0 = unit0 + span;
+            continue;
+        }
+        const uint32_t t1 = min(unit0 + tiles, t_end);
+        const int h = int(unit / p.nb), b = int(unit % p.nb);
+        const int group = int(uint32_t(a.heads) / uint32_t(a.kv_heads));
+        const int g0 = h * group + b * p.gsz;                       // the block's first query head
+        const int ng = min(p.gsz, group - b * p.gsz);
+        const Visible vis = visible(s_pos[m], a.n_pos, a.window, a.sinks);
+        const int64_t pitch = a.kv_heads * D * T::ELT;
+        const int64_t off = (int64_t(m) * a.n_pos * a.kv_heads + h) * D * T::ELT;
+        const unsigned char* kp = static_cast<const unsigned char*>(a.k) + off;
+        const unsigned char* vp = static_cast<const unsigned char*>(a.v) + off;
+        // this warp's entries: KT of every TK from v_begin on (at most 2^31 - 1 are visible)
+        const int64_t upto = int64_t(t1 - unit0) * TT;
+        const int v_end = int(vis.nvis < upto ? vis.nvis : upto);
+        const int64_t v_begin = int64_t(t0 - unit0) * TT + warp * T::KT;
+        const int its = v_end > v_begin ? int((v_end - v_begin + T::TK - 1) / T::TK) : 0;
+
+        float ref = -INFINITY, l = 0.0f;    // of query head gl, over this lane group's entries
+
+        int in_slot = 0, out_slot = 0;
+        const auto load = [&](int it) {
+            if (it < its) {
+                const uint32_t st = ring_s + in_slot * (2 * T::HALF);
+                in_slot = in_slot + 1 == T::S ? 0 : in_slot + 1;
+                constexpr int CPR = T::PITCH / 16;
+#pragma unroll
+                for (int i = 0; i < T::HALF / 512; ++i) {
+                    const int c = i * 32 + lane, r = c / CPR, col = c % CPR;
+                    const int64_t v = v_begin + int64_t(it) * T::TK + r;
+                    const bool in = v < v_end;
+                    const int64_t at = (in ? v + (v < vis.ns ? 0 : vis.gap) : 0) * pitch + col * 16;
+                    const uint32_t dst = st + r * T::PITCH + ((LPK == 4 ? col ^ (r & 1) * 4 : col) * 16);
+                    if (col * T::CD < D) {
+                        cp16(dst, kp + at, in);
+                        cp16(dst + T::HALF, vp + at, in);
+                    }
+                }
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < T::S - 1; ++i) load(i);
+
+        // q by way of shared memory, scaled; zero behind D and behind the block's heads
+#pragma unroll 4
+        for (int e = tid; e < NG * T::DMAX; e += kAttnThreads) {
+            const int g = e / T::DMAX, d = e % T::DMAX;
+            s_q[e] = g < ng && d < D ? a.q[m * a.ldq + int64_t(g0 + g) * D + d] * p.qscale : 0.0f;
+        }
+        __syncthreads();
+        f32x2 q[NG][T::NP], o[NG][T::NP];
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int i = 0; i < T::NP; ++i) {
+                const int d = (i / (T::CD / 2) * LPK + sl) * T::CD + i % (T::CD / 2) * 2;
+                q[g][i] = *reinterpret_cast<const f32x2*>(s_q + g * T::DMAX + d);
+                o[g][i] = 0ull;
+            }
+        for (int it = 0; it < its; ++it) {
+            cp_wait<T::S - 2>();
+            __syncwarp();
+            load(it + T::S - 1);
+            const uint32_t st = ring_s + out_slot * (2 * T::HALF);
+            out_slot = out_slot + 1 == T::S ? 0 : out_slot + 1;
+            const int64_t vb = v_begin + int64_t(it) * T::TK;
+            // partial scores over this lane's values, x[g * U + u]
+            float x[T::NV];
+#pragma unroll
+            for (int u = 0; u < T::U; ++u) {
+                f32x2 k[T::NP];
+#pragma unroll
+                for (int c = 0; c < T::NC; ++c)
+                    chunk_pairs<KV>(lds128(st + (u * T::KPS + grp) * T::PITCH + ((c * LPK + sl) ^ swz) * 16),
+                                    k + c * (T::CD / 2));
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    f32x2 s = mul2(q[g][0], k[0]);
+#pragma unroll
+                    for (int i = 1; i < T::NP; ++i) s = fma2(q[g][i], k[i], s);
+                    const float2 f = unpack2(s);
+                    x[g * T::U + u] = f.x + f.y;
+                }
+            }
+            // sum over the LPK lanes; lane sl keeps x[R * (sl / DUP) ...], R of them
+            int n = T::NV;
+#pragma unroll
+            for (int mask = LPK / 2; mask; mask >>= 1) {
+                if (n > 1) {
+                    n /= 2;
+                    const bool up = sl & mask;
+#pragma unroll
+                    for (int i = 0; i < T::NV / 2; ++i) {
+                        if (i >= n) break;
+                        const float give = up ? x[i] : x[i + n], mine = up ? x[i + n] : x[i];
+                        x[i] = mine + __shfl_xor_sync(0xffffffffu, give, mask);
+                    }
+                } else {
+                    x[0] += __shfl_xor_sync(0xffffffffu, x[0], mask);
+                }
+            }
+            bool moves = false;
+#pragma unroll
+            for (int r = 0; r < T::R; ++r) {
+                const int64_t v = vb + (u0 + r) * T::KPS + grp;
+                if (p.scores && v < v_end && gl < ng && sl % T::DUP == 0)
+                    p.scores[(int64_t(m) * a.heads + g0 + gl) * p.cap + v] = x[r];
+                x[r] = v < v_end ? x[r] : -INFINITY;
+                moves = moves || x[r] > ref + 8.0f;
+            }
+            if (__any_sync(0xffffffffu, moves)) {
+                float top = ref;
+#pragma unroll
+                for (int r = 0; r < T::R; ++r) top = fmaxf(top, x[r]);
+#pragma unroll
+                for (int mask = T::LG / 2; mask; mask >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, mask));
+                const float f = top == ref ? 1.0f : ex2(ref - top);
+                ref = top;
+                l *= f;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const float fg = __shfl_sync(0xffffffffu, f, grp0 + g * T::LG);
+#pragma unroll
+                    for (int i = 0; i < T::NP; ++i) o[g][i] = mul2(o[g][i], pack2(fg, fg));
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < T::R; ++r) {
+                x[r] = x[r] == -INFINITY ? 0.0f : ex2(x[r] - ref);
+                l += x[r];
+            }
+#pragma unroll
+            for (int u = 0; u < T::U; ++u) {
+                f32x2 v[T::NP];
+#pragma unroll
+                for (int c = 0; c < T::NC; ++c)
+                    chunk_pairs<KV>(
+                        lds128(st + T::HALF + (u * T::KPS + grp) * T::PITCH + ((c * LPK + sl) ^ swz) * 16),
+                        v + c * (T::CD / 2));
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const float w = __shfl_sync(0xffffffffu, x[u % T::R],
+                                                grp0 + (g * T::U + u) / T::R * T::DUP);
+                    const f32x2 ww = pack2(w, w);
+#pragma unroll
+                    for (int i = 0; i < T::NP; ++i) o[g][i] = fma2(ww, v[i], o[g][i]);
+                }
+            }
+        }
+        cp_wait<0>();
+        __syncwarp();
+
+        // join the warp's lane groups, then the warps
+        {
+            float top = ref;
+#pragma unroll
+            for (int mask = LPK; mask < 32; mask <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, mask));
+            const float f = ref == -INFINITY ? 0.0f : ex2(ref - top);
+            // (l stays NaN where a score was NaN before any other)
+            l = ref == -INFINITY ? l : l * f;
+            const float fo = ref == -INFINITY ? 1.0f : f;   // o is 0 or NaN there
+#pragma unroll
+            for (int mask = LPK; mask < 32; mask <<= 1) l += __shfl_xor_sync(0xffffffffu, l, mask);
+#pragma unroll
+            for (int mask = T::LG / 2; mask; mask >>= 1) l += __shfl_xor_sync(0xffffffffu, l, mask);
+            l *= 1.0f / T::DUP;
+            if (grp == 0 && sl % T::LG == 0) {
+                s_m[warp][gl] = top;
+                s_l[warp][gl] = l;
+            }
+            f32x2 z[NG * T::NP];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float fg = __shfl_sync(0xffffffffu, fo, grp0 + g * T::LG);
+#pragma unroll
+                for (int i = 0; i < T::NP; ++i) z[g * T::NP + i] = mul2(o[g][i], pack2(fg, fg));
+            }
+            constexpr int P = NG * T::NP, KEEP = P / T::KPS;
+            int n = P;
+#pragma unroll
+            for (int mask = 16; mask >= LPK; mask >>= 1) {
+                n /= 2;
+                const bool up = lane & mask;
+#pragma unroll
+                for (int i = 0; i < P / 2; ++i) {
+                    if (i >= n) break;
+                    const f32x2 give = up ? z[i] : z[i + n], mine = up ? z[i + n] : z[i];
+                    const float2 y = unpack2(__shfl_xor_sync(0xffffffffu, give, mask)), w = unpack2(mine);
+                    z[i] = pack2(w.x + y.x, w.y + y.y);
+                }
+            }
+            float* so = reinterpret_cast<float*>(ring);       // [NG][DMAX]
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i) {
+                const int at = grp * KEEP + i, g = at / T::NP, pr = at % T::NP;
+                const int d = (pr / (T::CD / 2) * LPK + sl) * T::CD + pr % (T::CD / 2) * 2;
+                *reinterpret_cast<float2*>(so + g * T::DMAX + d) = unpack2(z[i]);
+            }
+        }
+        __syncthreads();
+
+        // the CTA's state of the segment, and the whole unit's where it is all here
+        const bool whole = t0 == unit0 && t1 == unit0 + tiles;
+        const uint32_t c_first = owner(unit0), c_last = owner(unit0 + tiles - 1);
+        const size_t slot = size_t(NG) * (D + 2);
+        float* part = p.part + (2 * cta + (t_begin >= unit0 ? 0 : 1)) * slot;
+        const int D2 = D / 2;
+        for (int e = tid; e < ng * D2; e += kAttnThreads) {
+            const int g = e / D2, d = (e - g * D2) * 2;
+            float top = s_m[0][g];
+#pragma unroll
+            for (int w = 1; w < kAttnWarps; ++w) top = fmaxf(top, s_m[w][g]);
+            float sum = 0.0f, v0 = 0.0f, v1 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                const float f = s_m[w][g] == -INFINITY ? 1.0f : ex2(s_m[w][g] - top);   // l and o: 0 or NaN
+                const float2 o2 = *reinterpret_cast<const float2*>(ring_all + w * kAttnRing + (g * T::DMAX + d) * 4);
+                sum += s_l[w][g] * f;
+                v0 += o2.x * f;
+                v1 += o2.y * f;
+            }
+            if (whole) {
+                float* out = a.out + m * a.ldo + int64_t(g0 + g) * D + d;
+                out[0] = vis.nvis ? v0 / sum : 0.0f;
+                out[1] = vis.nvis ? v1 / sum : 0.0f;
+                if (d == 0 && p.ml) p.ml[int64_t(m) * a.heads + g0 + g] = make_float2(top, 1.0f / sum);
+            } else {
+                *reinterpret_cast<float2*>(part + g * (D + 2) + d) = make_float2(v0, v1);
+                if (d == 0) *reinterpret_cast<float2*>(part + g * (D + 2) + D) = make_float2(top, sum);
+            }
+        }
+        if (!whole) {
+            unsigned* ticket = static_cast<unsigned*>(a.ws) + c_first;
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const unsigned before = atomicAdd(ticket, 1u);
+                s_last = before == c_last - c_first;
+                if (s_last) *ticket = 0u;
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                // a CTA's state is in its first slot if it begins inside the unit, as
+                // every one behind c_first does
+                const float* p0 = p.part + (2 * c_first + (first(c_first) < unit0 ? 1 : 0)) * slot;
+                const float* p1 = p.part + 2 * (c_first + 1) * slot;
+                const int n = int(c_last - c_first) + 1;
+                const auto state = [&](int i, int g) {      // reference and sum of part i
+                    const float* x = (i ? p1 + (i - 1) * 2 * slot : p0) + g * (D + 2) + D;
+                    return __ldcg(reinterpret_cast<const float2*>(x));
+                };
+                float* s_f = reinterpret_cast<float*>(ring_all);   // (the states there have been read)
+                // one warp a query head: factors 2^(r_i - r), the sum and 1 / sum
+                for (int g = warp; g < ng; g += kAttnWarps) {
+                    const float2 mine = lane < n ? state(lane, g) : make_float2(-INFINITY, 0.0f);
+                    float top = mine.x, sum = 0.0f;
+                    for (int i = lane + 32; i < n; i += 32) top = fmaxf(top, state(i, g).x);
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    for (int i = lane; i < n; i += 32) {
+                        const float2 rl = i == lane ? mine : state(i, g);
+                        const float f = rl.x == -INFINITY ? 1.0f : ex2(rl.x - top);
+                        s_f[i * NG + g] = f;
+                        sum += rl.y * f;
+                    }
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                    if (lane == 0) {
+                        s_l[0][g] = sum;
+                        if (p.ml) p.ml[int64_t(m) * a.heads + g0 + g] = make_float2(top, 1.0f / sum);
+                    }
+                }
+                __syncthreads();
+                for (int e = tid; e < ng * D2; e += kAttnThreads) {
+                    const int g = e / D2, d = (e - g * D2) * 2;
+                    const float2 x0 = __ldcg(reinterpret_cast<const float2*>(p0 + g * (D + 2) + d));
+                    float v0 = x0.x * s_f[g], v1 = x0.y * s_f[g];
+                    const float* src = p1 + g * (D + 2) + d;
+#pragma unroll 8
+                    for (int i = 1; i < n; ++i, src += 2 * slot) {
+                        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+                        v0 += x.x * s_f[i * NG + g];
+                        v1 += x.y * s_f[i * NG + g];
+                    }
+                    float* out = a.out + m * a.ldo + int64_t(g0 + g) * D + d;
+                    out[0] = v0 / s_l[0][g];
+                    out[1] = v1 / s_l[0][g];
+                }
+            }
+        }
+        __syncthreads();
+        if (D < T::DMAX) {   // the states (and factors) overwrote values behind D
+            constexpr int DIRTY = NG * (T::DMAX > kAttnMaxCtas ? T::DMAX : kAttnMaxCtas);
+            static_assert(DIRTY * 4 <= kAttnRing, "states and factors fit a warp's ring");
+            for (int i = lane; i < DIRTY / 4; i += 32) reinterpret_cast<int4*>(ring)[i] = int4{0, 0, 0, 0};
+            __syncwarp();
+        }
+        t0 = t1;
+    }
+}
+
+template <int KV, int NG, int LPK>
+cudaError_t launch_attn_shape(const AttnParams& p, const LaunchCtx& ctx) {
+    static std::atomic<bool> ready[kMaxDevices];
+    const auto kern = attn_kernel<KV, NG, LPK>;
+    constexpr size_t smem = size_t(kAttnWarps) * kAttnRing;
+    const cudaError_t e = set_smem_once(kern, smem, ctx.dev, ready);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attrs[1];
+    cfg.gridDim = dim3(unsigned(2 * ctx.num_sms < kAttnMaxCtas ? 2 * ctx.num_sms : kAttnMaxCtas));
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = ctx.stream;
+    cfg.numAttrs = pdl_attrs(ctx, attrs);
+    cfg.attrs = attrs;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// LPK: the lanes that hold an entry's head_dim values, DPL each.
+template <int KV, int NG>
+cudaError_t launch_attn_heads(const AttnParams& p, const LaunchCtx& ctx) {
+    constexpr int DPL = AttnShape<KV, NG, 8>::DPL;
+    if constexpr (DPL == 16) {
+        if (p.a.dim <= 64) return launch_attn_shape<KV, NG, 4>(p, ctx);
+        if (p.a.dim <= 128) return launch_attn_shape<KV, NG, 8>(p, ctx);
+        return launch_attn_shape<KV, NG, 16>(p, ctx);
+    } else {
+        if (p.a.dim <= 64) return launch_attn_shape<KV, NG, 8>(p, ctx);
+        if (p.a.dim <= 128) return launch_attn_shape<KV, NG, 16>(p, ctx);
+        return launch_attn_shape<KV, NG, 32>(p, ctx);
+    }
+}
+
+template <int KV>
+cudaError_t launch_attn_type(const AttnParams& p, const LaunchCtx& ctx) {
+    if (p.gsz == 1) return launch_attn_heads<KV, 1>(p, ctx);
+    if (p.gsz == 2) return launch_attn_heads<KV, 2>(p, ctx);
+    if (p.gsz <= 4) return launch_attn_heads<KV, 4>(p, ctx);
+    return launch_attn_heads<KV, 8>(p, ctx);
+}
+
+}  // namespace q8
