@@ -236,54 +236,79 @@ def head_argmax_noalloc(mode, q, s, xq, xd, rows, tok, maxval=None, logits=None,
                                       _stream(stream)), "head_argmax_noalloc")
 
 
-def _need(what, t, dtype, shape, device, dense=True):
-    """A tensor argument that the C call reads by pointer: its type, shape,
-    device and (dense) layout.  shape: None where any size may stand."""
+# Arguments of the calls below are checked before their addresses are taken:
+# types, shapes, layouts and device.  The checks cost a launch-bound caller
+# host time, so each tensor that is in order passes one condition.
+
+def _need(what, t, dtype, shape, device):
+    """A dense tensor of this type, shape and device (its index)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if len(t.shape) != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, not {t.device}")
-    if dense and not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{what} must be on cuda:{device}, not {t.device}")
+    raise ValueError(f"{what} must be contiguous")
 
 
-def _row_pitch(what, t, dtype, rows, device):
-    """The elements from one row to the next of a 2-D tensor with dense rows."""
-    _need(what, t, dtype, (rows, None), device, dense=False)
-    if t.stride(1) != 1 and t.shape[1] != 1:
+def _maybe(what, t, dtype, shape, device):
+    return None if t is None else _need(what, t, dtype, shape, device)
+
+
+def _need_rows(what, t, dtype, rows, least, device):
+    """A 2-D tensor of dense rows of at least `least` values: its address and row pitch."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < least:
+        raise ValueError(f"{what} must have {rows} rows of at least {least} values, not {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on cuda:{device}, not {t.device}")
+    pitch, step = t.stride()
+    if step != 1 and t.shape[1] != 1:
         raise ValueError(f"{what} must have dense rows")
-    return t.stride(0) if rows != 1 else t.shape[1]
+    return t.data_ptr(), pitch if rows != 1 else t.shape[1]
 
 
-def _on_current_device(what, t):
-    """The device of a call's first tensor, which must be the current one."""
+def _current(what, t):
+    """(torch, the device index of a call's first tensor, which must be the current one)."""
     import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    device = t.get_device()
+    if device < 0 or device != torch.cuda.current_device():
         raise ValueError(f"{what} is on {t.device}; calls run on the current CUDA device")
-    return t.device
+    return torch, device
 
 
-def _kv_type(what, t):
-    import torch
-    types = {torch.float32: Q8_KV_F32, torch.float16: Q8_KV_F16, torch.bfloat16: Q8_KV_BF16}
-    if t.dtype not in types:
-        raise TypeError(f"{what} must be float32, float16 or bfloat16, not {t.dtype}")
-    return types[t.dtype]
+def _raw_stream(torch, device, stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream
+
+
+def _workspace(workspace, device):
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _kv_caches(k_cache, v_cache, kv_heads):
-    """(device, kv type, rows, n_pos, head_dim) of a pair of caches
+    """(torch, device, kv type, rows, n_pos, head_dim) of a pair of caches
     [rows, n_pos, kv_heads * head_dim]."""
-    device = _on_current_device("k_cache", k_cache)
-    kv = _kv_type("k_cache", k_cache)
-    _need("k_cache", k_cache, k_cache.dtype, (None, None, None), device)
-    _need("v_cache", v_cache, k_cache.dtype, tuple(k_cache.shape), device)
-    rows, n_pos, kv_dim = k_cache.shape
+    torch, device = _current("k_cache", k_cache)
+    dtype, shape = k_cache.dtype, k_cache.shape
+    kv = (Q8_KV_F32 if dtype is torch.float32 else Q8_KV_F16 if dtype is torch.float16
+          else Q8_KV_BF16 if dtype is torch.bfloat16 else -1)
+    if kv < 0:
+        raise TypeError(f"k_cache must be float32, float16 or bfloat16, not {dtype}")
+    if len(shape) != 3:
+        raise ValueError(f"k_cache must have shape (rows, n_pos, kv_dim), not {tuple(shape)}")
+    _need("k_cache", k_cache, dtype, shape, device)
+    _need("v_cache", v_cache, dtype, shape, device)
+    rows, n_pos, kv_dim = shape
     if kv_heads < 1 or kv_dim % kv_heads:
         raise ValueError(f"cache rows of {kv_dim} values do not hold {kv_heads} heads")
-    return device, kv, rows, n_pos, kv_dim // kv_heads
+    return torch, device, kv, rows, n_pos, kv_dim // kv_heads
 
 
 def attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window=-1, sinks=0, acc=False) -> int:
@@ -296,22 +321,17 @@ def attn_decode(q, k_cache, v_cache, pos, out, workspace, heads, kv_heads, windo
     """q, out: [rows, >= heads * head_dim] float32 with any row pitch; caches
     [rows, n_pos, kv_heads * head_dim]; pos int32 [rows]; acc float32
     [rows, kv_heads, n_pos] or None; scale None: 1 / sqrt(head_dim)."""
-    import torch
-    device, kv, rows, n_pos, dim = _kv_caches(k_cache, v_cache, kv_heads)
-    ldq = _row_pitch("q", q, torch.float32, rows, device)
-    ldo = _row_pitch("out", out, torch.float32, rows, device)
-    if min(q.shape[1], out.shape[1]) < heads * dim:
-        raise ValueError(f"rows of q and out must hold {heads} heads of {dim} values")
-    _need("pos", pos, torch.int32, (rows,), device)
-    if acc is not None:
-        _need("acc", acc, torch.float32, (rows, kv_heads, n_pos), device)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {device}")
-    _check(load().attn_decode(_ptr(q), ldq, _ptr(k_cache), _ptr(v_cache), kv, rows, n_pos, heads,
-                              kv_heads, dim, _ptr(pos), window, sinks,
-                              dim ** -0.5 if scale is None else float(scale), _ptr(out), ldo, _ptr(acc),
-                              _ptr(workspace), workspace.numel() * workspace.element_size(),
-                              _stream(stream)), "attn_decode")
+    torch, device, kv, rows, n_pos, dim = _kv_caches(k_cache, v_cache, kv_heads)
+    f32 = torch.float32
+    q_at, ldq = _need_rows("q", q, f32, rows, heads * dim, device)
+    out_at, ldo = _need_rows("out", out, f32, rows, heads * dim, device)
+    ws_at, ws_bytes = _workspace(workspace, device)
+    _check(load().attn_decode(
+        q_at, ldq, k_cache.data_ptr(), v_cache.data_ptr(), kv, rows, n_pos, heads, kv_heads, dim,
+        _need("pos", pos, torch.int32, (rows,), device), window, sinks,
+        dim ** -0.5 if scale is None else scale, out_at, ldo,
+        _maybe("acc", acc, f32, (rows, kv_heads, n_pos), device), ws_at, ws_bytes,
+        _raw_stream(torch, device, stream)), "attn_decode")
 
 
 def kv_evict_workspace(rows, kv_heads, budget) -> int:
@@ -322,39 +342,33 @@ def kv_evict(k_cache, v_cache, pos, acc, new_pos, new_acc, workspace, kv_heads, 
              recent=0, kept=None, stream=None):
     """Caches and acc as attn_decode; new_pos, new_acc may be pos, acc; kept
     int32 [rows, kv_heads, budget] or None."""
-    import torch
-    device, kv, rows, n_pos, dim = _kv_caches(k_cache, v_cache, kv_heads)
-    for what, t in (("pos", pos), ("new_pos", new_pos)):
-        _need(what, t, torch.int32, (rows,), device)
-    for what, t in (("acc", acc), ("new_acc", new_acc)):
-        _need(what, t, torch.float32, (rows, kv_heads, n_pos), device)
-    if kept is not None:
-        _need("kept", kept, torch.int32, (rows, kv_heads, budget), device)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {device}")
-    _check(load().kv_evict(_ptr(k_cache), _ptr(v_cache), kv, rows, n_pos, kv_heads, dim, _ptr(pos),
-                           _ptr(acc), budget, sinks, recent, _ptr(new_pos), _ptr(new_acc), _ptr(kept),
-                           _ptr(workspace), workspace.numel() * workspace.element_size(),
-                           _stream(stream)), "kv_evict")
+    torch, device, kv, rows, n_pos, dim = _kv_caches(k_cache, v_cache, kv_heads)
+    f32, i32, weights = torch.float32, torch.int32, (rows, kv_heads, n_pos)
+    ws_at, ws_bytes = _workspace(workspace, device)
+    _check(load().kv_evict(
+        k_cache.data_ptr(), v_cache.data_ptr(), kv, rows, n_pos, kv_heads, dim,
+        _need("pos", pos, i32, (rows,), device), _need("acc", acc, f32, weights, device), budget, sinks,
+        recent, _need("new_pos", new_pos, i32, (rows,), device),
+        _need("new_acc", new_acc, f32, weights, device),
+        _maybe("kept", kept, i32, (rows, kv_heads, budget), device), ws_at, ws_bytes,
+        _raw_stream(torch, device, stream)), "kv_evict")
 
 
 def head_sample(logits, u, tok, temperature=None, top_k=None, top_p=None, min_p=None, prob=None,
                 kept=None, stream=None):
     """logits float32 [rows, N] with any row pitch; u, temperature, top_p,
     min_p, prob float32 [rows]; top_k, tok, kept int32 [rows]."""
-    import torch
-    device = _on_current_device("logits", logits)
+    torch, device = _current("logits", logits)
     rows, n = logits.shape
-    ldl = _row_pitch("logits", logits, torch.float32, rows, device)
-    for what, t, dtype in (("u", u, torch.float32), ("temperature", temperature, torch.float32),
-                           ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32),
-                           ("min_p", min_p, torch.float32), ("tok", tok, torch.int32),
-                           ("prob", prob, torch.float32), ("kept", kept, torch.int32)):
-        if t is not None:
-            _need(what, t, dtype, (rows,), device)
-    _check(load().head_sample(_ptr(logits), ldl, rows, n, _ptr(u), _ptr(temperature), _ptr(top_k),
-                              _ptr(top_p), _ptr(min_p), _ptr(tok), _ptr(prob), _ptr(kept),
-                              _stream(stream)), "head_sample")
+    f32, i32, per_row = torch.float32, torch.int32, (rows,)
+    x_at, ldl = _need_rows("logits", logits, f32, rows, n, device)
+    _check(load().head_sample(
+        x_at, ldl, rows, n, _need("u", u, f32, per_row, device),
+        _maybe("temperature", temperature, f32, per_row, device),
+        _maybe("top_k", top_k, i32, per_row, device), _maybe("top_p", top_p, f32, per_row, device),
+        _maybe("min_p", min_p, f32, per_row, device), _need("tok", tok, i32, per_row, device),
+        _maybe("prob", prob, f32, per_row, device), _maybe("kept", kept, i32, per_row, device),
+        _raw_stream(torch, device, stream)), "head_sample")
 
 
 def q8_debug_block_dots(mode, q, xq, rows, isum, path=0, stream=None):
