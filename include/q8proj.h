@@ -386,9 +386,9 @@ size_t kv_evict_workspace(int64_t rows, int64_t kv_heads, int64_t budget);
  * 0.  A row without any other logit gives token 0, prob 0 and kept 0; so does
  * a row whose temperature is negative or NaN, or whose top_p or min_p is NaN,
  * which also sets device error 3.  Weights are integers in units of
- * 2^-(62 - ceil(log2 N)) of the largest, computed to about 2^-40 of their
- * value, and their sums are exact: a row's token depends on nothing but its
- * own row and settings.
+ * 2^-(62 - ceil(log2 N)) of the largest, rounded down, within 2^-29 of their
+ * value before that, and their sums are exact: a row's token depends on
+ * nothing but its own row and settings.
  * 1 <= rows <= Q8_MAX_ROWS, 1 <= N <= 2^20, logits 16-byte aligned, the
  * others 4-byte.  No workspace.
  */

@@ -4,24 +4,30 @@
 // units of 2^-shift rounded down, so every sum is exact and independent of its
 // order: what is drawn depends on nothing but the row and its settings.  The
 // filters cut the tokens in order of x (ties: the lowest index first), so what
-// they leave is "x > t, or x = t and index <= last".
+// they leave is "x > t, or x = t and index <= last".  Shares of a sum (top_p,
+// u) are exact products of integers too.
 //
 // Layout.  A cluster of 1 to 8 CTAs takes a row, each an equal part of it in
-// index order, read once into shared memory (rows past 8 x 48 K logits are read
+// index order, read once into shared memory (parts past 46 K logits are read
 // again from L2 instead).  The CTAs hand sums to one another through
 // distributed shared memory: one cluster barrier an exchange.
 //
-// A cut (the k-th largest; the end of the nucleus) is found without sorting
-// the row: a histogram of 1024 bins linear in x between M and a bound below the
-// cut (counts, or masses to 2^-22) names the bin that holds it; an exact pass
-// sums what lies above that bin and lists the bin's tokens in the first CTA,
-// which sorts them (some hundreds) and finds the cut's place.  Where the list
-// is too long (thousands of equal logits) or the histogram's rounding named a
-// neighbour, a binary search over the 32 bits of the ordered logits finds the
-// cut instead, with exact sums at each step.
+// Top-k of up to some hundreds: the lanes' maxima give a logit (`reach`) that
+// at least k tokens reach; the tokens that reach it, 600 of 128256 for k = 50,
+// are listed, and the first CTA does the rest on the list alone.
 //
-// What bounds it.  One row: latency (about ten exchanges).  A batch: the exact
-// weights, about 30 instructions each against 4 bytes read.
+// Otherwise a cut (the k-th largest; the end of the nucleus) is found without
+// sorting the row: a histogram of 1024 bins linear in x (counts, or masses to
+// 2^-21) names the bin that holds it; an exact pass sums what lies above that
+// bin and lists the bin's tokens, which the first CTA sorts (some hundreds).
+// Where the list is too long (thousands of equal logits), a binary search over
+// the 32 bits of the ordered logits finds the cut instead, with exact sums at
+// each step.
+//
+// What bounds it.  One row: latency, of exchanges and of code that runs once
+// (no arithmetic of 64-bit floats: at 2 lanes a clock and SM, one division in
+// every thread cost 5 us).  A batch: the exact weights, about 45 instructions
+// each against 4 bytes read, and the histogram's atomics.
 #include <cooperative_groups.h>
 #include <float.h>
 #include <math.h>
@@ -38,30 +44,39 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512, kWarpsN = kThreads / 32;
 constexpr int kTile = 128;                  // logits a warp takes at a time, four a lane
 constexpr int kPart = kWarpsN * kTile;      // a CTA's part is a multiple of this
-constexpr int kMaxPart = 48 * 1024;         // logits of a part held in shared memory
+constexpr int kMaxPart = 46 * 1024;         // logits of a part held in shared memory
 constexpr int kBins = 1024, kList = 2048, kMaxCluster = 8;
-constexpr float kOctaves = 48.0f;           // below 2^-48 of the largest a nucleus never ends
+constexpr int kShort = 128;                 // a longer list is cut by a histogram before it is sorted
 typedef unsigned long long u64;
 
-// What the CTAs of a cluster exchange: a slot a CTA, two sets used in turn, so
-// that a slot is written again only after a barrier behind its last reader.
+// What the CTAs of a cluster exchange: sums a, b, g, e and e2, the largest c
+// and c2, the smallest d.  A slot a CTA, two sets used in turn, so that a slot
+// is written again only after a barrier behind its last reader.
 struct Slot {
-    u64 a, b, g;
-    uint32_t c, d;
+    u64 a = 0, b = 0, g = 0;
+    uint32_t e = 0, e2 = 0, c = 0, c2 = 0, d = 0xffffffffu;
 };
+enum { kA = 1, kB = 2, kG = 4, kE = 8, kE2 = 16, kC = 32, kC2 = 64, kD = 128 };
 
 struct Shared {
     Slot slot[2][kMaxCluster];
-    u64 warp_a[kWarpsN], warp_b[kWarpsN], warp_g[kWarpsN];
-    uint32_t warp_c[kWarpsN], warp_d[kWarpsN];
+    Slot warp[kWarpsN];                     // the same by warp of this CTA
+    u64 scan[kWarpsN];
     uint32_t hist[kBins];
-    u64 list[kList];
-    uint32_t listed[2];                     // in the first CTA: tokens offered to the list, by attempt
+    u64 list[kList];                        // (ordered logit, ~index) of listed tokens
+    u64 mine[kList];                        // this CTA's part of the list; then weights, or what a histogram left
+    uint32_t listed;                        // tokens this CTA listed
     float cut_x;                            // the cut that the first CTA found
-    uint32_t cut_i, cut_ok;
-    uint32_t found;                         // an index that one CTA found
+    uint32_t cut_i;
+    uint32_t found;                         // an index, bin or place that one thread found
     uint2 pow2[32];                         // 2^(j/32): in units of 2^-31, and as a float of those
 };
+
+// The dynamic shared memory: Shared, then the CTA's part of the row.
+extern __shared__ __align__(16) unsigned char smem[];
+__device__ __forceinline__ Shared& sh() { return *reinterpret_cast<Shared*>(smem); }
+__device__ __forceinline__ float* sh_x() { return reinterpret_cast<float*>(smem + sizeof(Shared)); }
+static_assert(sizeof(Shared) % 16 == 0 && sizeof(Shared) + 4 * kMaxPart <= 227 * 1024, "shared memory");
 
 // Order of the logits as unsigned integers; 0: NaN or -inf, never drawn.
 __device__ __forceinline__ uint32_t logit_key(float x) {
@@ -87,39 +102,54 @@ __constant__ uint32_t kPow2[32] = {
 // product with a two-term constant), split into J/32 + h with |h| <= 1/64 and
 // a little; 2^h - 1 is its Taylor polynomial to degree 4 (remainder 2^-40).
 // The largest error is that polynomial's and h's own rounding, 2^-29 of the
-// weight; with 2^-30 typical, one draw in 10^7 falls next to a border that
-// this moves.
+// weight; sums over n tokens average it, so that fewer than one draw in 10^7
+// has a border within it.
 struct Weights {
     float M, pre, ch, cl;   // pre: 1/2 where differences could overflow
     int shift;
     bool inf;               // M is +inf
-    const uint2* pow2;
 
-    __device__ __forceinline__ u64 operator()(float x) const {
-        if (inf) return x == INFINITY ? u64(1) << shift : 0;
+    // 2^y as mantissa (in [2^31, 2^32)) * 2^(J/32 - 31 whole part); false: below half a unit
+    __device__ __forceinline__ bool parts(float x, uint32_t& mant, int& n) const {
         const float a = x * pre, s = a - M, bb = s - a;
         const float err = (a - (s - bb)) + (-M - bb);
-        const float p = __fmul_rn(s, ch);       // (rounded: e is what it lost)
-        if (!(p > -float(shift))) return 0;
+        const float p = __fmul_rn(s, ch);                // (rounded: e is what it lost)
         float e = fmaf(s, ch, -p);
         e = fmaf(s, cl, e);
         e = fmaf(err, ch, e);
-        const float kRound = 393216.0f;                 // 1.5 * 2^18: one step is 1/32
+        const float kRound = 393216.0f;                  // 1.5 * 2^18: one step is 1/32
         const float r = p + kRound;
         const int J = __float_as_int(r) - __float_as_int(kRound);
         const float h = (p - (r - kRound)) + e;
-        float q = fmaf(h, 0.009618129f, 0.05550411f);   // ln(2)^4/24, ln(2)^3/6, ...
+        float q = fmaf(h, 0.009618129f, 0.05550411f);    // ln(2)^4/24, ln(2)^3/6, ...
         q = fmaf(h, q, 0.2402265f);
         q = fmaf(h, q, 0.6931472f);
         q *= h;
-        const uint2 t = pow2[J & 31];
-        const uint32_t m = t.x + uint32_t(__float2int_rn(__uint_as_float(t.y) * q));
-        return (u64(m) << 31) >> (62 - shift - (J >> 5));
+        const uint2 t = sh().pow2[J & 31];
+        mant = t.x + uint32_t(__float2int_rn(__uint_as_float(t.y) * q));
+        n = J >> 5;
+        return p > -float(shift);
+    }
+    __device__ __forceinline__ u64 operator()(float x) const {
+        uint32_t mant;
+        int n;
+        const bool any = parts(x, mant, n);
+        if (inf) return x == INFINITY ? u64(1) << shift : 0;
+        const int up = shift - 31 + n;                   // mant * 2^up: one of the two factors is 1
+        const uint32_t lo = mant >> min(max(-up, 0), 31), hi = 1u << max(min(up, 31), 0);
+        return any ? u64(lo) * hi : 0;
+    }
+    // the histogram's bin: (M - x) * scale, the last one for all that lies lower
+    __device__ __forceinline__ int bin(float x, float scale) const {
+        const float y = inf ? (x == INFINITY ? 0.0f : float(kBins)) : (M - x * pre) * scale;
+        return y < float(kBins - 1) ? int(y) : kBins - 1;
     }
     // 2^y to about 2^-21, for the histogram
     __device__ __forceinline__ float rough(float x) const {
         if (inf) return x == INFINITY ? 1.0f : 0.0f;
-        return exp2f((x * pre - M) * ch);
+        float r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((x * pre - M) * ch));
+        return r;
     }
 };
 
@@ -129,120 +159,244 @@ struct Cut {
     __device__ __forceinline__ bool has(float x, uint32_t i) const { return x > t || (x == t && i <= last); }
 };
 
+// f * S for 0 <= f <= 1 as an integer, rounded down or up, exactly.
+__device__ __forceinline__ u64 share(float f, u64 S, bool up) {
+    const uint32_t bits = __float_as_uint(f), eb = bits >> 23;
+    const u64 m = (bits & 0x7fffffu) | (eb ? 0x800000u : 0u);        // f = m * 2^-k
+    const int k = 150 - int(max(eb, 1u));
+    const u64 lo = m * S, hi = __umul64hi(m, S);
+    u64 q = 0, rest = lo | hi;
+    if (k < 64) {
+        q = (hi << (64 - k)) | (lo >> k);
+        rest = lo << (64 - k);
+    } else if (k == 64) {
+        q = hi;
+        rest = lo;
+    } else if (k < 128) {
+        q = hi >> (k - 64);
+        rest = lo | (hi << (128 - k));
+    }
+    return q + (up && rest);
+}
+
+// Sum over the warp, in three fields that 32 lanes cannot overflow.
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+    const uint32_t lo = __reduce_add_sync(0xffffffffu, uint32_t(v) & 0x7ffffffu);
+    const uint32_t mid = __reduce_add_sync(0xffffffffu, uint32_t(v >> 27) & 0x7ffffffu);
+    const uint32_t hi = __reduce_add_sync(0xffffffffu, uint32_t(v >> 54));
+    return u64(lo) + (u64(mid) << 27) + (u64(hi) << 54);
+}
+
+__device__ __forceinline__ u64 warp_scan(u64 v) {     // inclusive
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += y;
+    }
+    return v;
+}
+
+// Exclusive prefix sum over the CTA's threads; the whole sum in *all.
+__device__ __noinline__ u64 block_scan(u64 v, u64* all) {
+    Shared& s = sh();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const u64 up = warp_scan(v);
+    __syncthreads();
+    if (lane == 31) s.scan[warp] = up;
+    __syncthreads();
+    const u64 w = warp_scan(lane < kWarpsN ? s.scan[lane] : 0);
+    *all = __shfl_sync(0xffffffffu, w, 31);
+    const u64 before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    return (warp ? before : 0) + up - v;
+}
+
+template <int F>
+__device__ __forceinline__ void warp_reduce(Slot& v) {
+    if constexpr (F & kA) v.a = warp_sum(v.a);
+    if constexpr (F & kB) v.b = warp_sum(v.b);
+    if constexpr (F & kG) v.g = warp_sum(v.g);
+    if constexpr (F & kE) v.e = __reduce_add_sync(0xffffffffu, v.e);
+    if constexpr (F & kE2) v.e2 = __reduce_add_sync(0xffffffffu, v.e2);
+    if constexpr (F & kC) v.c = __reduce_max_sync(0xffffffffu, v.c);
+    if constexpr (F & kC2) v.c2 = __reduce_max_sync(0xffffffffu, v.c2);
+    if constexpr (F & kD) v.d = __reduce_min_sync(0xffffffffu, v.d);
+}
+
+// The fields F of every thread's Slot over the cluster as one; before (if
+// given) receives the sum of a over the CTAs before this one.
+template <int F>
+__device__ __forceinline__ Slot exchange(Slot v, int& phase, u64* before = nullptr) {
+    Shared& s = sh();
+    cg::cluster_group cl = cg::this_cluster();
+    const unsigned rank = cl.block_rank(), size = cl.num_blocks();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    warp_reduce<F>(v);
+    if (lane == 0) s.warp[warp] = v;
+    __syncthreads();
+    Slot* const slots = s.slot[phase];
+    phase ^= 1;
+    if (warp == 0) {
+        v = Slot();
+        if (lane < kWarpsN) v = s.warp[lane];
+        warp_reduce<F>(v);
+        if (lane < int(size)) *cl.map_shared_rank(&slots[rank], lane) = v;
+    }
+    cl.sync();
+    v = Slot();
+    if (lane < int(size)) v = slots[lane];
+    if (before) *before = warp_sum(lane < int(rank) ? v.a : 0);
+    warp_reduce<F>(v);
+    return v;
+}
+
+// Bitonic steps k (all of j = 32 .. 1) on the 64 numbers a[lane], a[lane + 32]
+// of a warp, which begin at place `at` of what is sorted; the largest first.
+__device__ __forceinline__ void warp_steps(u64& lo, u64& hi, int at, int k, int j0) {
+    const int lane = threadIdx.x & 31;
+    for (int j = j0; j; j >>= 1) {
+        if (j == 32) {
+            const bool down = ((at + lane) & k) == 0;
+            if ((lo < hi) == down) {
+                const u64 t = lo;
+                lo = hi;
+                hi = t;
+            }
+        } else {
+            const u64 l2 = __shfl_xor_sync(0xffffffffu, lo, j), h2 = __shfl_xor_sync(0xffffffffu, hi, j);
+            const bool first = !(lane & j);
+            const bool lmax = first == (((at + lane) & k) == 0), hmax = first == (((at + lane + 32) & k) == 0);
+            lo = (lo < l2) == lmax ? l2 : lo;
+            hi = (hi < h2) == hmax ? h2 : hi;
+        }
+    }
+}
+
+// Sorts a[0, n) from the largest down (n <= kList) with the CTA's threads: 64
+// numbers a warp in registers, longer steps through shared memory.
+__device__ __noinline__ void sort_down(u64* a, int n) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int n2 = 64;
+    while (n2 < n) n2 *= 2;
+    __syncthreads();
+    for (int at = warp * 64; at < n2; at += kWarpsN * 64) {
+        u64 lo = at + lane < n ? a[at + lane] : 0, hi = at + lane + 32 < n ? a[at + lane + 32] : 0;
+        for (int k = 2; k <= 64; k *= 2) warp_steps(lo, hi, at, k, k / 2);
+        a[at + lane] = lo;
+        a[at + lane + 32] = hi;
+    }
+    __syncthreads();
+    for (int k = 128; k <= n2; k *= 2) {
+        for (int j = k / 2; j >= 64; j /= 2) {
+            for (int p = threadIdx.x; p < n2 / 2; p += kThreads) {
+                const int i = 2 * p - (p & (j - 1));
+                const u64 x = a[i], y = a[i + j];
+                if ((x < y) == ((i & k) == 0)) {
+                    a[i] = y;
+                    a[i + j] = x;
+                }
+            }
+            __syncthreads();
+        }
+        for (int at = warp * 64; at < n2; at += kWarpsN * 64) {
+            u64 lo = a[at + lane], hi = a[at + lane + 32];
+            warp_steps(lo, hi, at, k, 32);
+            a[at + lane] = lo;
+            a[at + lane + 32] = hi;
+        }
+        __syncthreads();
+    }
+}
+
+__device__ __forceinline__ float list_x(u64 v) { return key_logit(uint32_t(v >> 32)); }
+__device__ __forceinline__ uint32_t list_i(u64 v) { return ~uint32_t(v); }
+
 // One CTA's view of its row.  RES: the part lies in shared memory, padded with
 // -inf to whole tiles of every warp; else it is read from global memory.
 template <bool RES>
 struct Row {
-    Shared& s;
-    const float* x;            // the part
+    const float* x;            // the part in global memory
     uint32_t base, n;          // its first index and length
     int tiles;                 // tiles of each warp
     unsigned rank, size;
     int phase;
 
-    // f(four logits, index of the first) for each of this lane's quads, in index order a warp
+    // f(four logits, index of the first) for each of this lane's quads
+    template <typename F>
+    __device__ __forceinline__ void quads(F f) const {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        uint32_t e = warp * tiles * kTile + lane * 4;
+#pragma unroll 1
+        for (int k = 0; k < tiles; ++k, e += kTile) f(quad(e), base + e);
+    }
+    // f(logit, index) for each of this lane's logits
     template <typename F>
     __device__ __forceinline__ void each(F f) const {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const uint32_t e0 = warp * tiles * kTile + lane * 4;
-#pragma unroll 2
-        for (int k = 0; k < tiles; ++k) f(quad(e0 + k * kTile), base + e0 + k * kTile);
+        quads([&](float4 v, uint32_t i) { f(v.x, i), f(v.y, i + 1), f(v.z, i + 2), f(v.w, i + 3); });
     }
     __device__ __forceinline__ float4 quad(uint32_t e) const {
-        if constexpr (RES) return *reinterpret_cast<const float4*>(x + e);
-        float4 v;
-        v.x = at(e), v.y = at(e + 1), v.z = at(e + 2), v.w = at(e + 3);
-        return v;
+        if constexpr (RES) return *reinterpret_cast<const float4*>(sh_x() + e);
+        return make_float4(at(e), at(e + 1), at(e + 2), at(e + 3));
     }
     __device__ __forceinline__ float at(uint32_t e) const {
-        if constexpr (RES) return x[e];
         const float v = e < n ? __ldg(x + e) : -INFINITY;
         return v > -INFINITY ? v : -INFINITY;       // NaN too
     }
 
-    // Sums a, b and g, the largest c and the smallest d over the cluster's
-    // threads; before (if given) receives the sums of a over the CTAs before this one.
-    __device__ __forceinline__ Slot exchange(u64 a, u64 b, u64 g, uint32_t c, uint32_t d, u64* before = nullptr) {
-        cg::cluster_group cl = cg::this_cluster();
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // Lists those of a lane's four tokens that `in` names (all lanes call).
+    __device__ __forceinline__ void list(const bool (&in)[4], float4 v, uint32_t i) {
+        if (!__any_sync(0xffffffffu, in[0] | in[1] | in[2] | in[3])) return;
+        const float x[4] = {v.x, v.y, v.z, v.w};
+        Shared& s = sh();
 #pragma unroll
-        for (int k = 16; k; k >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, k);
-            b += __shfl_xor_sync(0xffffffffu, b, k);
-            g += __shfl_xor_sync(0xffffffffu, g, k);
-        }
-        c = __reduce_max_sync(0xffffffffu, c);
-        d = __reduce_min_sync(0xffffffffu, d);
-        if (lane == 0) {
-            s.warp_a[warp] = a;
-            s.warp_b[warp] = b;
-            s.warp_g[warp] = g;
-            s.warp_c[warp] = c;
-            s.warp_d[warp] = d;
+        for (int j = 0; j < 4; ++j)
+            if (in[j]) {
+                const uint32_t at = atomicAdd(&s.listed, 1u);
+                if (at < kList) s.mine[at] = (u64(logit_key(x[j])) << 32) | uint32_t(~(i + j));
+            }
+    }
+    // First CTA, behind the exchange (of e2: tokens listed) that ended the
+    // listing: the parts as one list of n <= kList tokens.  The other CTAs keep
+    // theirs until the next barrier.
+    __device__ __forceinline__ void gather(uint32_t n) {
+        Shared& s = sh();
+        cg::cluster_group cl = cg::this_cluster();
+        for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+            uint32_t at = i;
+            unsigned r = 0;
+            for (; r + 1 < size && at >= s.slot[phase ^ 1][r].e2; ++r) at -= s.slot[phase ^ 1][r].e2;
+            s.list[i] = cl.map_shared_rank(s.mine, r)[at];
         }
         __syncthreads();
-        Slot(&slots)[kMaxCluster] = s.slot[phase];
-        phase ^= 1;
-        if (warp == 0) {
-            a = lane < kWarpsN ? s.warp_a[lane] : 0;
-            b = lane < kWarpsN ? s.warp_b[lane] : 0;
-            g = lane < kWarpsN ? s.warp_g[lane] : 0;
-            c = __reduce_max_sync(0xffffffffu, lane < kWarpsN ? s.warp_c[lane] : 0u);
-            d = __reduce_min_sync(0xffffffffu, lane < kWarpsN ? s.warp_d[lane] : 0xffffffffu);
-#pragma unroll
-            for (int k = 8; k; k >>= 1) {
-                a += __shfl_xor_sync(0xffffffffu, a, k);
-                b += __shfl_xor_sync(0xffffffffu, b, k);
-                g += __shfl_xor_sync(0xffffffffu, g, k);
-            }
-            if (lane < size) *cl.map_shared_rank(&slots[rank], lane) = Slot{a, b, g, c, d};
-        }
-        cl.sync();
-        Slot all = slots[0];
-        u64 sum = rank > 0 ? slots[0].a : 0;
-        for (unsigned r = 1; r < size; ++r) {
-            if (r < rank) sum += slots[r].a;
-            all.a += slots[r].a;
-            all.b += slots[r].b;
-            all.g += slots[r].g;
-            all.c = max(all.c, slots[r].c);
-            all.d = min(all.d, slots[r].d);
-        }
-        if (before) *before = sum;
-        return all;
     }
 
     // The index whose running sum of w(x, index) in index order first reaches
-    // e (1 <= e <= the whole sum, which the caller knows is reached).
+    // e, where `before` is the sum of the CTAs before this one and s.warp[].a
+    // the sums of its warps (1 <= e <= the whole sum).
     template <typename W>
-    __device__ __forceinline__ uint32_t locate(u64 e, W w) {
+    __device__ __forceinline__ uint32_t pick(u64 e, u64 before, W w) {
+        Shared& s = sh();
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        u64 mine = 0, before;
-        each([&](float4 v, uint32_t i) { mine += w(v.x, i) + w(v.y, i + 1) + w(v.z, i + 2) + w(v.w, i + 3); });
-        exchange(mine, 0, 0, 0, 0, &before);
-        // (warp_a: this CTA's sums by warp, until the next exchange)
-        u64 at_warp = before;
-        for (int k = 0; k < warp; ++k) at_warp += s.warp_a[k];
-        if (at_warp < e && at_warp + s.warp_a[warp] >= e) {
-            u64 run = at_warp;
+        u64 run = before;
+        for (int k = 0; k < warp; ++k) run += s.warp[k].a;
+        if (run < e && run + s.warp[warp].a >= e) {
+#pragma unroll 1
             for (int k = 0; k < tiles; ++k) {
                 const uint32_t el = (warp * tiles + k) * kTile + lane * 4, i = base + el;
                 const float4 v = quad(el);
                 const u64 w0 = w(v.x, i), w1 = w0 + w(v.y, i + 1), w2 = w1 + w(v.z, i + 2), w3 = w2 + w(v.w, i + 3);
-                u64 up = w3;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const u64 y = __shfl_up_sync(0xffffffffu, up, d);
-                    if (lane >= d) up += y;
+                const u64 sum = warp_sum(w3);
+                if (run + sum < e) {
+                    run += sum;
+                    continue;
                 }
-                const u64 lo = run + up - w3;
-                if (lo < e && run + up >= e) {
+                const u64 up = run + warp_scan(w3), lo = up - w3;
+                if (lo < e && up >= e) {
                     const uint32_t hit = lo + w0 >= e ? 0 : lo + w1 >= e ? 1 : lo + w2 >= e ? 2 : 3;
                     cg::cluster_group cl = cg::this_cluster();
                     for (unsigned r = 0; r < size; ++r) *cl.map_shared_rank(&s.found, r) = i + hit;
                 }
-                run += __shfl_sync(0xffffffffu, up, 31);
-                if (run >= e) break;
+                break;
             }
         }
         cg::this_cluster().sync();
@@ -250,210 +404,249 @@ struct Row {
     }
 
     // The cut by exact sums of f(x, index) over what reaches a bound, bit by
-    // bit; goal(sum): whether the sum is enough.  e_of(sum above, one tie's f,
-    // ties) says how many of the tokens equal to the bound are taken.
-    template <typename F, typename G, typename E>
-    __device__ __noinline__ Cut search(uint32_t top, F f, G goal, E e_of) {
+    // bit: the largest bound whose sum is at least `need`.  e_of(sum above, one
+    // tie's f) says how many of the tokens equal to the bound are taken.
+    template <typename F, typename E>
+    __device__ __noinline__ Cut search(uint32_t top, F f, u64 need, E e_of) {
         uint32_t t = 0;
         for (int bit = 31; bit >= 0; --bit) {
             const uint32_t cand = t | (1u << bit);
             if (cand > top) continue;
-            u64 sum = 0;
-            each([&](float4 v, uint32_t i) {
-                if (logit_key(v.x) >= cand) sum += f(v.x, i);
-                if (logit_key(v.y) >= cand) sum += f(v.y, i + 1);
-                if (logit_key(v.z) >= cand) sum += f(v.z, i + 2);
-                if (logit_key(v.w) >= cand) sum += f(v.w, i + 3);
+            Slot v;
+            each([&](float x, uint32_t i) {
+                if (logit_key(x) >= cand) v.a += f(x, i);
             });
-            if (goal(exchange(sum, 0, 0, 0, 0).a)) t = cand;
+            if (exchange<kA>(v, phase).a >= need) t = cand;
         }
         if (t == 0) t = 1;
-        u64 above = 0, tie = 0;
-        uint32_t ties = 0;
-        const auto one = [&](float x, uint32_t i) {
+        Slot v;
+        u64 tie = 0;
+        each([&](float x, uint32_t i) {
             const uint32_t k = logit_key(x);
             const u64 w = k >= t ? f(x, i) : 0;
-            if (k > t) above += w;
-            if (k == t && f(x, i)) {
+            if (k > t) v.a += w;
+            if (k == t && w) {
                 tie = w;
-                ++ties;
+                ++v.e;
             }
-        };
-        each([&](float4 v, uint32_t i) { one(v.x, i), one(v.y, i + 1), one(v.z, i + 2), one(v.w, i + 3); });
-        // (ties weigh the same: the sum of their weights by their number)
-        const Slot all = exchange(above, ties, u64(ties) * tie, 0, 0);
+        });
+        v.g = tie * v.e;       // ties weigh the same
+        const Slot all = exchange<kA | kG | kE>(v, phase);
         const float x = key_logit(t);
-        const u64 n = all.b;
-        const u64 e = n ? min(max(e_of(all.a, all.g / n, n), u64(1)), n) : 1;
-        if (n == 0) return {x, 0xffffffffu};
-        const uint32_t last = locate(e, [&](float v, uint32_t i) { return u64(v == x && f(v, i)); });
-        return {x, last};
+        if (all.e == 0) return {x, 0xffffffffu};
+        const u64 e = min(max(e_of(all.a, all.g / all.e), u64(1)), u64(all.e));
+        const auto is_tie = [&](float y, uint32_t i) { return u64(y == x && f(y, i)); };
+        Slot ties;
+        each([&](float y, uint32_t i) { ties.a += is_tie(y, i); });
+        u64 before;
+        exchange<kA>(ties, phase, &before);
+        return {x, pick(e, before, is_tie)};
     }
 };
 
-// Sorts s.list[0, n) from the largest down (n <= kList) with the CTA's threads.
-__device__ __forceinline__ void sort_list(Shared& s, int n) {
-    int n2 = 2;
-    while (n2 < n) n2 *= 2;
-    for (int i = n + threadIdx.x; i < n2; i += kThreads) s.list[i] = 0;
-    __syncthreads();
-    for (int k = 2; k <= n2; k *= 2)
-        for (int j = k / 2; j; j /= 2) {
-            for (int p = threadIdx.x; p < n2 / 2; p += kThreads) {
-                const int i = 2 * p - (p & (j - 1));
-                const u64 a = s.list[i], b = s.list[i + j];
-                if ((a < b) == ((i & k) == 0)) {
-                    s.list[i] = b;
-                    s.list[i + j] = a;
-                }
-            }
-            __syncthreads();
-        }
-}
-
 // A cut by histogram, exact pass and sorted list.  f(x, i): what is summed (0:
-// not among the tokens); rough(x, i): f for the histogram; scale: bins a unit
-// of M - x; goal(sum): whether a sum from the top is enough; prep(total): called
-// with the exact sum of all f before goal.  False: not found this way.
-template <bool RES, typename F, typename R, typename P, typename G>
-__device__ __forceinline__ bool cut_by_bins(Row<RES>& row, const Weights& w, float scale, F f, R rough, u64 rough_goal,
-                                            P prep, G goal, Cut* cut) {
+// not among the tokens); rough(x, i): f for the histogram, whose sum from the
+// top reaches rough_need in the cut's bin; need_of(sum of all f): the sum that
+// the cut reaches; scale: bins a unit of M - x.  False: not found this way.
+// True: above and above_n are this thread's f and number of the tokens in bins
+// before the cut's, cut_bin.
+template <bool RES, typename F, typename R, typename P>
+__device__ __forceinline__ bool cut_by_bins(Row<RES>& row, const Weights& w, float scale, F f, R rough, u64 rough_need,
+                                            P need_of, Cut* cut, u64* above, uint32_t* above_n, int* cut_bin) {
     cg::cluster_group cl = cg::this_cluster();
-    Shared& s = row.s;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const auto bin = [&](float x) {
-        const float y = w.inf ? (x == INFINITY ? 0.0f : float(kBins)) : (w.M - x * w.pre) * scale;
-        return y < float(kBins - 1) ? int(y) : kBins - 1;
-    };
+    Shared& s = sh();
+    const int tid = threadIdx.x;
     for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
-    if (tid < 2) s.listed[tid] = 0;
-    __syncthreads();
-    row.each([&](float4 v, uint32_t i) {
-        const float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t r = rough(x[j], i + j);
-            if (r) atomicAdd(&s.hist[bin(x[j])], r);
-        }
-    });
-    cl.sync();
-    // every CTA sums the cluster's bins and finds the one that holds the cut
-    constexpr int PER = kBins / kThreads;
-    u64 mine[PER], sum = 0;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        mine[j] = 0;
-        for (unsigned r = 0; r < row.size; ++r) mine[j] += cl.map_shared_rank(s.hist, r)[tid * PER + j];
-        sum += mine[j];
-    }
-    u64 up = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const u64 y = __shfl_up_sync(0xffffffffu, up, d);
-        if (lane >= d) up += y;
-    }
-    if (lane == 31) s.warp_a[tid >> 5] = up;
     if (tid == 0) s.found = kBins;
     __syncthreads();
-    u64 before = up - sum;
-    for (int k = 0; k < tid >> 5; ++k) before += s.warp_a[k];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        if (before < rough_goal && before + mine[j] >= rough_goal) s.found = tid * PER + j;
-        before += mine[j];
+    // (the last bin holds all that lies lower: summed in a register)
+    uint32_t rest = 0;
+    row.each([&](float x, uint32_t i) {
+        const uint32_t r = rough(x, i);
+        const int b = w.bin(x, scale);
+        if (b == kBins - 1) rest += r;
+        else if (r) atomicAdd(&s.hist[b], r);
+    });
+    rest = __reduce_add_sync(0xffffffffu, rest);
+    if ((tid & 31) == 0 && rest) atomicAdd(&s.hist[kBins - 1], rest);
+    cl.sync();
+    // every CTA sums the cluster's bins and finds the one that holds the cut
+    static_assert(kBins == 2 * kThreads, "two bins a thread");
+    u64 b0 = 0, b1 = 0, all_bins;
+#pragma unroll 8
+    for (unsigned r = 0; r < row.size; ++r) {
+        const uint2 h = reinterpret_cast<const uint2*>(cl.map_shared_rank(s.hist, r))[tid];
+        b0 += h.x;
+        b1 += h.y;
     }
+    const u64 before = block_scan(b0 + b1, &all_bins);
+    if (before < rough_need && before + b0 + b1 >= rough_need) s.found = 2 * tid + (before + b0 < rough_need);
+    if (tid == 0) s.listed = 0;
     __syncthreads();
     int B = int(s.found);
     // (nobody reads another CTA's bins, or this CTA's `found`, behind the next barrier)
-    u64* const list = cl.map_shared_rank(s.list, 0);
     for (int attempt = 0; attempt < 3; ++attempt) {
-        uint32_t* const listed = cl.map_shared_rank(&s.listed[attempt & 1], 0);
-        u64 total = 0, above = 0, within = 0;
-        row.each([&](float4 v, uint32_t i) {
-            const float x[4] = {v.x, v.y, v.z, v.w};
+        Slot v;
+        row.quads([&](float4 x4, uint32_t i) {
+            const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+            bool in[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const u64 fx = f(x[j], i + j);
-                const int b = bin(x[j]);
-                const bool in = b == B && fx != 0;
-                total += fx;
-                if (b < B) above += fx;
-                if (in) within += fx;
-                const unsigned who = __ballot_sync(0xffffffffu, in);
-                if (who) {
-                    const int lead = __ffs(who) - 1;
-                    uint32_t at = 0;
-                    if (lane == lead) at = atomicAdd(listed, uint32_t(__popc(who)));
-                    at = __shfl_sync(0xffffffffu, at, lead) + __popc(who & ((1u << lane) - 1));
-                    if (in && at < kList) list[at] = (u64(logit_key(x[j])) << 32) | uint32_t(~(i + j));
+                const int b = w.bin(x[j], scale);
+                v.a += fx;
+                if (b < B) {
+                    v.b += fx;
+                    v.e += fx != 0;
+                }
+                in[j] = b == B && fx != 0;
+                if (in[j]) {
+                    v.g += fx;
+                    ++v.e2;
                 }
             }
+            row.list(in, x4, i);
         });
-        const Slot all = row.exchange(total, above, within, 0, 0);
-        prep(all.a);
-        if (goal(all.b) || !goal(all.b + all.g)) {      // the histogram's rounding named a neighbour
-            B += goal(all.b) ? -1 : 1;
-            if (tid == 0) s.listed[attempt & 1] = 0;    // (for the attempt after the next)
+        const Slot all = exchange<kA | kB | kG | kE2>(v, row.phase);
+        const u64 need = need_of(all.a);
+        if (all.b >= need || all.b + all.g < need) {      // the histogram's rounding named a neighbour
+            B += all.b >= need ? -1 : 1;
+            __syncthreads();
+            if (tid == 0) s.listed = 0;
+            __syncthreads();
             continue;
         }
+        if (all.e2 > kList) return false;
         if (row.rank == 0) {
-            const int n = int(s.listed[attempt & 1]);
-            if (tid == 0) s.cut_ok = n <= kList;
-            if (n <= kList) {
-                sort_list(s, n);
-                // the first place whose sum, itself included, is enough
-                const int per = (n + kThreads - 1) / kThreads;
-                u64 part = 0;
-                for (int j = 0; j < per; ++j) {
-                    const int at = tid * per + j;
-                    if (at < n) part += f(key_logit(uint32_t(s.list[at] >> 32)), ~uint32_t(s.list[at]));
-                }
-                u64 upto = part;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const u64 y = __shfl_up_sync(0xffffffffu, upto, d);
-                    if (lane >= d) upto += y;
-                }
-                if (lane == 31) s.warp_b[tid >> 5] = upto;
-                __syncthreads();
-                u64 run = all.b + upto - part;
-                for (int k = 0; k < tid >> 5; ++k) run += s.warp_b[k];
-                for (int j = 0; j < per; ++j) {
-                    const int at = tid * per + j;
-                    if (at >= n) break;
-                    const float x = key_logit(uint32_t(s.list[at] >> 32));
-                    const uint32_t i = ~uint32_t(s.list[at]);
-                    const u64 fx = f(x, i);
-                    if (!goal(run) && goal(run + fx)) {
-                        s.cut_x = x;
-                        s.cut_i = i;
+            const int n = int(all.e2);
+            row.gather(all.e2);
+            sort_down(s.list, n);
+            // the first place whose sum, itself included, is enough
+            const int per = (n + kThreads - 1) / kThreads, at0 = tid * per, at1 = min(at0 + per, n);
+            u64 part = 0, sum;
+            for (int j = at0; j < at1; ++j) part += f(list_x(s.list[j]), list_i(s.list[j]));
+            u64 run = all.b + block_scan(part, &sum);
+            for (int j = at0; j < at1; ++j) {
+                const u64 fx = f(list_x(s.list[j]), list_i(s.list[j]));
+                if (run < need && run + fx >= need) {
+                    for (unsigned r = 0; r < row.size; ++r) {
+                        *cl.map_shared_rank(&s.cut_x, r) = list_x(s.list[j]);
+                        *cl.map_shared_rank(&s.cut_i, r) = list_i(s.list[j]);
                     }
-                    run += fx;
                 }
-            }
-            __syncthreads();
-            if (tid < int(row.size) && tid > 0) {
-                *cl.map_shared_rank(&s.cut_x, tid) = s.cut_x;
-                *cl.map_shared_rank(&s.cut_i, tid) = s.cut_i;
-                *cl.map_shared_rank(&s.cut_ok, tid) = s.cut_ok;
+                run += fx;
             }
         }
         cl.sync();
         *cut = {s.cut_x, s.cut_i};
-        return s.cut_ok != 0;
+        *above = v.b;
+        *above_n = v.e;
+        *cut_bin = B;
+        return true;
     }
     return false;
 }
 
+// What one row is given.
+struct Settings {
+    float p, u;
+    u64 floor_w;     // the smallest weight that min-p keeps
+    int k;
+};
+
+// The first CTA alone, on a list of n tokens that holds the row's k largest
+// (k <= n): the filters and the draw.  scale: bins over the list's logits.
+__device__ __noinline__ void draw_from_list(const Weights& w, const Settings& g, int n, float scale, uint32_t* tok,
+                                            u64* mass, uint32_t* kept) {
+    Shared& s = sh();
+    const int tid = threadIdx.x, k = g.k;
+    u64* a = s.list;       // the tokens
+    u64* wt = s.mine;      // their weights
+    u64 sum;
+    if (n > kShort) {
+        // those in the bins up to the one that holds the k-th
+        for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
+        if (tid == 0) s.listed = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) atomicAdd(&s.hist[w.bin(list_x(a[i]), scale)], 1u);
+        __syncthreads();
+        const uint32_t b0 = s.hist[2 * tid], b1 = s.hist[2 * tid + 1];
+        const u64 before = block_scan(b0 + b1, &sum);
+        if (before < u64(k) && before + b0 + b1 >= u64(k)) s.found = 2 * tid + (before + b0 < u64(k));
+        __syncthreads();
+        const int B = int(s.found);
+        for (int i = tid; i < n; i += kThreads)
+            if (w.bin(list_x(a[i]), scale) <= B) s.mine[atomicAdd(&s.listed, 1u)] = a[i];
+        __syncthreads();
+        n = int(s.listed);
+        a = s.mine;
+        wt = s.list;
+    }
+    sort_down(a, n);
+    const int per = (k + kThreads - 1) / kThreads, at0 = tid * per, at1 = min(at0 + per, k);
+    u64 part = 0;
+    for (int j = at0; j < at1; ++j) {
+        const u64 x = w(list_x(a[j]));
+        wt[j] = x;
+        part += x;
+    }
+    u64 run = block_scan(part, &sum);
+    if (tid == 0) s.found = uint32_t(k);
+    __syncthreads();
+    if (g.p < 1.0f) {
+        // the shortest beginning that holds p of the mass
+        const u64 need = share(g.p, sum, true);
+        for (int j = at0; j < at1; ++j) {
+            if (run < need && run + wt[j] >= need) s.found = uint32_t(j + 1);
+            run += wt[j];
+        }
+    }
+    __syncthreads();
+    n = int(s.found);
+    // what is left, in index order: (~index, place), 0 for what min-p drops
+    part = 0;
+    uint32_t cnt = 0;
+    for (int j = at0; j < at1; ++j) {
+        const bool in = j < n && (j == 0 || wt[j] >= g.floor_w);
+        if (in) {
+            part += wt[j];
+            ++cnt;
+        }
+        a[j] = in ? (a[j] << 32) | uint32_t(j) : 0;
+    }
+    block_scan(part, &sum);
+    u64 cnt_all;
+    block_scan(cnt, &cnt_all);
+    sort_down(a, n);
+    const int at2 = min(at0 + per, int(cnt_all));
+    // the first sum above u * S
+    const u64 e = g.u >= 1.0f ? sum : g.u > 0.0f ? share(g.u, sum, false) + 1 : 1;
+    part = 0;
+    for (int j = at0; j < at2; ++j) part += wt[uint32_t(a[j])];
+    u64 whole;
+    run = block_scan(part, &whole);
+    for (int j = at0; j < at2; ++j) {
+        const u64 x = wt[uint32_t(a[j])];
+        // (u = 0 draws the first, whose weight may be below half a unit)
+        const bool hit = g.u > 0.0f || w.inf ? run < e && run + x >= e : j == 0;
+        if (hit) s.found = uint32_t(j);
+        run += x;
+    }
+    __syncthreads();
+    *tok = ~uint32_t(a[s.found] >> 32);
+    *mass = sum;
+    *kept = uint32_t(cnt_all);
+}
+
 template <bool RES>
 __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const SampleArgs a, int part, int shift, int* err) {
-    extern __shared__ __align__(16) float s_x[];
-    __shared__ Shared s;
+    Shared& s = sh();
     cg::cluster_group cl = cg::this_cluster();
     const unsigned rank = cl.block_rank(), size = cl.num_blocks();
     const int tid = threadIdx.x, lane = tid & 31;
     const int64_t m = blockIdx.x / size;
     if (tid < 32) s.pow2[tid] = make_uint2(kPow2[tid], __float_as_uint(float(kPow2[tid])));
+    if (tid == 0) s.listed = 0;
     pdl_wait();
     pdl_launch_dependents();
 
@@ -462,190 +655,224 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
     const float p = a.top_p ? a.top_p[m] : 1.0f, mp = a.min_p ? a.min_p[m] : 0.0f;
     const float u = a.u[m];
     const auto give = [&](int64_t tok, float prob, int32_t kept) {
-        if (rank == 0 && tid == 0) {
-            a.tok[m] = int32_t(tok);
-            if (a.prob) a.prob[m] = prob;
-            if (a.kept) a.kept[m] = kept;
-        }
+        a.tok[m] = int32_t(tok);
+        if (a.prob) a.prob[m] = prob;
+        if (a.kept) a.kept[m] = kept;
     };
+    const bool writes = rank == 0 && tid == 0;
     if (!(T >= 0.0f) || isnan(p) || isnan(mp)) {      // the whole cluster alike
-        if (rank == 0 && tid == 0) atomicExch(err, Q8_DEVERR_PARAM);
-        return give(0, 0.0f, 0);
+        if (writes) {
+            atomicExch(err, Q8_DEVERR_PARAM);
+            give(0, 0.0f, 0);
+        }
+        return;
     }
 
     // the part: [base, base + n) of the row
     const uint32_t base = rank * uint32_t(part), N = uint32_t(a.N);
     const uint32_t n = base < N ? min(uint32_t(part), N - base) : 0;
     const float* gx = a.x + m * a.ldx + base;
-    Row<RES> row{s, RES ? s_x : gx, base, n, part / kPart, rank, size, 0};
+    Row<RES> row{gx, base, n, part / kPart, rank, size, 0};
     if constexpr (RES) {
+        float* x = sh_x();
+        const auto clean = [](float v) { return v > -INFINITY ? v : -INFINITY; };   // NaN is never drawn
+        if ((reinterpret_cast<uintptr_t>(gx) & 15) == 0) {
 #pragma unroll 8
-        for (int e = tid; e < part; e += kThreads) {
-            const float v = e < int(n) ? __ldg(gx + e) : -INFINITY;
-            s_x[e] = v > -INFINITY ? v : -INFINITY;   // NaN too
+            for (int e = tid * 4; e < part; e += kThreads * 4) {
+                float4 v;
+                if (e + 3 < int(n)) {
+                    v = __ldg(reinterpret_cast<const float4*>(gx + e));
+                } else {
+                    v.x = e < int(n) ? __ldg(gx + e) : -INFINITY;
+                    v.y = e + 1 < int(n) ? __ldg(gx + e + 1) : -INFINITY;
+                    v.z = e + 2 < int(n) ? __ldg(gx + e + 2) : -INFINITY;
+                    v.w = -INFINITY;
+                }
+                *reinterpret_cast<float4*>(x + e) = make_float4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+            }
+        } else {
+#pragma unroll 8
+            for (int e = tid; e < part; e += kThreads) x[e] = clean(e < int(n) ? __ldg(gx + e) : -INFINITY);
         }
         __syncthreads();
     }
 
-    cl.sync();      // every CTA has begun before another writes to it
-
-    // the largest, the smallest, how many can be drawn
-    uint32_t top = 0, low = 0xffffffffu, cnt = 0;
+    // the largest and the smallest that can be drawn, and how many can
+    Slot v;
     float best = -INFINITY;
-    row.each([&](float4 v, uint32_t) {
-        const float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            best = fmaxf(best, x[j]);
-            const uint32_t key = logit_key(x[j]);
-            if (key) {
-                low = min(low, key);
-                ++cnt;
-            }
-        }
+    row.each([&](float x, uint32_t) {
+        best = fmaxf(best, x);
+        const uint32_t key = logit_key(x);
+        v.d = min(v.d, key - 1);               // (0, never drawn: the largest)
+        v.e += key != 0;
     });
-    top = logit_key(best);
-    const Slot all = row.exchange(cnt, 0, 0, top, low);
-    top = all.c;
-    const u64 count = all.a;
-    if (top == 0) return give(0, 0.0f, 0);
-    const float M = key_logit(top);
-    uint32_t first = 0xffffffffu;
-    row.each([&](float4 v, uint32_t i) {
-        if (v.w == M) first = min(first, i + 3);
-        if (v.z == M) first = min(first, i + 2);
-        if (v.y == M) first = min(first, i + 1);
-        if (v.x == M) first = min(first, i);
-    });
+    v.c = logit_key(best);
     // with top-k: a logit that at least k reach, from the lanes' maxima: the
     // q-th largest of each full warp, the smallest of those over the warps
-    uint32_t reach = 1;
-    const bool by_k = k > 0 && u64(k) < count;
+    uint32_t reach = 0xffffffffu;
     const uint32_t of_warp = uint32_t(row.tiles) * kTile, full = N / of_warp;     // warps whose logits all exist
-    const uint32_t q = by_k && full ? (uint32_t(k) + full - 1) / full : 0;
-    if (q >= 1 && q <= 32) {
-        uint32_t v = logit_key(best);
+    const uint32_t q = k > 0 && full ? (uint32_t(k) + full - 1) / full : 0;
+    if (q >= 1 && q <= 32 && base / of_warp + (tid >> 5) < full) {
+        uint32_t key = v.c;
         for (uint32_t j = 1; j < q; ++j) {
-            const uint32_t most = __reduce_max_sync(0xffffffffu, v);
-            const unsigned who = __ballot_sync(0xffffffffu, v == most);
-            if (lane == __ffs(who) - 1) v = 0;
+            const uint32_t most = __reduce_max_sync(0xffffffffu, key);
+            const unsigned who = __ballot_sync(0xffffffffu, key == most);
+            if (lane == __ffs(who) - 1) key = 0;
         }
-        reach = __reduce_max_sync(0xffffffffu, v);
-        if (base / of_warp + (tid >> 5) >= full) reach = 0xffffffffu;
+        reach = __reduce_max_sync(0xffffffffu, key);
     }
-    {
-        // (the smallest over threads of `reach`, and of `first`)
-        const Slot r = row.exchange(0, 0, 0, ~reach, first);
-        reach = ~r.c;
-        first = r.d;
+    v.c2 = ~reach;
+    cl.sync();      // every CTA has begun before another writes to it
+    const Slot all = exchange<kE | kC | kC2 | kD>(v, row.phase);
+    const uint32_t top = all.c, low = all.d + 1;
+    reach = ~all.c2;
+    if (top == 0) {
+        if (writes) give(0, 0.0f, 0);
+        return;
     }
-    if (T < 0x1p-60f) {
-        return give(first, 1.0f, 1);
+    const float M = key_logit(top);
+    if (T < 0x1p-60f || p <= 0.0f || mp > 1.0f) {      // the first alone
+        v = Slot();
+        row.each([&](float x, uint32_t i) {
+            if (x == M) v.d = min(v.d, i);
+        });
+        const uint32_t first = exchange<kD>(v, row.phase).d;
+        if (writes) give(first, 1.0f, 1);
+        return;
     }
 
     Weights w;
-    const double c = 1.4426950408889634 / double(T);
     w.inf = M == INFINITY;
-    w.pre = fmaxf(fabsf(M), fabsf(key_logit(all.d))) > 1e38f ? 0.5f : 1.0f;
+    w.pre = fmaxf(fabsf(M), fabsf(key_logit(low))) > 1e38f ? 0.5f : 1.0f;
     w.M = M * w.pre;
-    w.ch = float(c / w.pre);
-    w.cl = float(c / w.pre - double(w.ch));
+    // log2(e) / T in two floats, from log2(e) in two
+    const float c = __fdiv_rn(1.44269502f, T);
+    const float c2 = isinf(T) ? 0.0f : __fdiv_rn(fmaf(-c, T, 1.44269502f) + 1.925963e-8f, T);
+    w.ch = c / w.pre;
+    w.cl = c2 / w.pre;
     w.shift = shift;
-    w.pow2 = s.pow2;
-    const float span = w.M - key_logit(all.d) * w.pre;      // of all logits (0: all equal)
+    const u64 one = u64(1) << shift;
+    Settings set{p, u, mp > 0.0f ? share(mp, one, true) : 0, k};
+    const auto finish = [&](uint32_t tok, u64 S, uint32_t kept) {
+        uint32_t mant;
+        int e;
+        w.parts(a.x[m * a.ldx + tok], mant, e);
+        const double wt = w.inf ? double(one) : ldexp(double(mant), shift - 31 + e);
+        give(tok, float(wt / double(S)), int32_t(kept));
+    };
+    const float span = w.M - key_logit(low) * w.pre;      // of all logits (0: all equal)
     const auto bins_over = [&](float d) {
         d = fminf(d, span);
         return d > 0.0f && d < INFINITY ? fminf(float(kBins) / d, FLT_MAX) : 0.0f;
     };
+    const bool by_k = k > 0 && uint32_t(k) < all.e;
+    const bool reached = reach > 0 && reach <= top;
+    const float bound = reached ? key_logit(reach) : M;
+    const float k_scale = reached && bound < M ? bins_over((w.M - bound * w.pre) * 1.001f) : bins_over(span);
+    if (by_k && k <= kList && reached) {
+        // every token that reaches `bound`, at least k of them
+        v = Slot();
+        row.quads([&](float4 x, uint32_t i) {
+            const bool in[4] = {x.x >= bound, x.y >= bound, x.z >= bound, x.w >= bound};
+            v.e2 += in[0] + in[1] + in[2] + in[3];
+            row.list(in, x, i);
+        });
+        const uint32_t listed = exchange<kE2>(v, row.phase).e2;
+        if (listed <= kList) {
+            if (rank == 0) {
+                row.gather(listed);
+                uint32_t tok, kept;
+                u64 S;
+                draw_from_list(w, set, int(listed), k_scale, &tok, &S, &kept);
+                if (writes) finish(tok, S, kept);
+            }
+            cl.sync();      // (the first CTA has read the others' parts of the list)
+            return;
+        }
+    }
 
     Cut cut{-FLT_MAX, 0xffffffffu};      // everything above -inf
+    u64 above = 0;
+    uint32_t above_n = 0;
+    int cut_bin = 0;
     if (by_k) {
-        const float d = reach > 1 && reach < top ? (w.M - key_logit(reach) * w.pre) * 1.001f : span;
-        const auto one = [&](float x, uint32_t) { return u64(x > -INFINITY); };
-        const auto goal = [&](u64 n) { return n >= u64(k); };
-        if (!cut_by_bins(row, w, bins_over(d), one, [&](float x, uint32_t) { return uint32_t(x > -INFINITY); }, u64(k),
-                         [](u64) {}, goal, &cut))
-            cut = row.search(top, one, goal, [&](u64 above, u64, u64) { return u64(k) - above; });
+        const auto counted = [&](float x, uint32_t) { return uint32_t(x > -INFINITY); };
+        if (!cut_by_bins(row, w, k_scale, counted, counted, u64(k), [&](u64) { return u64(k); }, &cut, &above, &above_n,
+                         &cut_bin))
+            cut = row.search(top, counted, u64(k), [&](u64 sum, u64) { return u64(k) - sum; });
     }
-    if (p <= 0.0f) {
-        cut = {M, first};
-    } else if (p < 1.0f) {
+    bool summed = false;                 // above, above_n, cut_bin are the kept weights' before the cut's bin
+    float scale = 0.0f;
+    if (p < 1.0f) {
         // bins hold masses in units of 2^-31 of the sum, by its estimate
         float est = 0.0f;
         const Cut before = cut;
-        row.each([&](float4 v, uint32_t i) {
-            if (before.has(v.x, i)) est += w.rough(v.x);
-            if (before.has(v.y, i + 1)) est += w.rough(v.y);
-            if (before.has(v.z, i + 2)) est += w.rough(v.z);
-            if (before.has(v.w, i + 3)) est += w.rough(v.w);
+        row.each([&](float x, uint32_t i) {
+            if (before.has(x, i)) est += w.rough(x);
         });
-        const u64 whole = row.exchange(u64(est * 16777216.0f), 0, 0, 0, 0).a;      // at least 2^24: M itself
-        const float unit = 2147483648.0f / (float(whole) * 0x1p-24f);
-        double P = 0.0;
-        u64 S = 0;
-        const auto f = [&](float x, uint32_t i) { return before.has(x, i) ? w(x) : 0; };
-        const auto rough = [&](float x, uint32_t i) { return before.has(x, i) ? __float2uint_rn(w.rough(x) * unit) : 0u; };
-        const auto prep = [&](u64 total) {
-            S = total;
-            P = double(p) * double(total);
+        v = Slot();
+        v.a = u64(est * 16777216.0f);
+        const float S = float(exchange<kA>(v, row.phase).a) * 0x1p-24f;      // at least 1: M itself
+        const float unit = 2147483648.0f / S;
+        // tokens of less than (1 - p) S / N hold less than the share 1 - p
+        // together, so the nucleus ends above them: the bins stop there
+        const float least = (1.0f - p) * S / float(all.e) * 0.99f;
+        scale = bins_over(w.inf ? span : -log2f(least) / w.ch);
+        const auto f = [&](float x, uint32_t i) {
+            const u64 wx = w(x);
+            return before.has(x, i) ? wx : 0;
         };
-        const auto goal = [&](u64 mass) { return double(mass) >= P; };
-        Cut c2;
-        if (!cut_by_bins(row, w, bins_over(kOctaves / w.ch), f, rough, u64(double(p) * 2147483648.0) + 1, prep, goal, &c2)) {
-            c2 = row.search(top, f, goal, [&](u64 above, u64 tie, u64 ties) {
-                // the fewest ties that reach the mass
-                u64 lo = 1, hi = ties;
-                while (lo < hi) {
-                    const u64 e = (lo + hi) / 2;
-                    if (goal(above + e * tie)) hi = e; else lo = e + 1;
-                }
-                return lo;
-            });
-        }
-        cut = c2;
+        const auto rough = [&](float x, uint32_t i) {
+            const uint32_t r = __float2uint_rn(w.rough(x) * unit);
+            return before.has(x, i) ? r : 0u;
+        };
+        u64 need = 0;
+        const auto need_of = [&](u64 sum) { return need = share(p, sum, true); };
+        summed = cut_by_bins(row, w, scale, f, rough, u64(share(p, u64(1) << 31, true)), need_of, &cut, &above, &above_n,
+                             &cut_bin);
+        if (!summed)
+            // (`need` is of the exact sum by now) the fewest ties that reach the mass
+            cut = row.search(top, f, need, [&](u64 sum, u64 tie) { return (need - sum + tie - 1) / tie; });
     }
-    if (mp > 1.0f) cut = {M, first};
-    const double floor_d = ceil(double(mp) * double(u64(1) << shift));
-    const u64 floor_w = floor_d >= 1.0 ? (floor_d > double(u64(1) << shift) ? u64(1) << shift : u64(floor_d)) : 0;
 
     // what is kept: its mass and number, and its lowest index
-    u64 mass = 0;
-    uint32_t kept = 0, lowest = 0xffffffffu;
-    const auto keeps = [&](float x, uint32_t i, u64& wx) {
-        wx = 0;
-        if (!(x > -INFINITY) || !cut.has(x, i)) return false;
-        wx = w(x);
-        return wx >= floor_w;
+    const u64 floor_w = set.floor_w;
+    const auto kept_w = [&](float x, uint32_t i) -> u64 {
+        const u64 wx = w(x);
+        return cut.has(x, i) && wx >= floor_w ? wx : 0;
     };
-    row.each([&](float4 v, uint32_t i) {
-        const float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            u64 wx;
-            if (keeps(x[j], i + j, wx)) {
-                mass += wx;
-                ++kept;
-                // (with +inf among the logits the others weigh nothing)
-                if (!w.inf || wx) lowest = min(lowest, i + j);
+    v = Slot();
+    if (summed && floor_w == 0) {
+        v.a = above;
+        v.e = above_n;
+        row.each([&](float x, uint32_t i) {
+            if (cut.has(x, i)) {
+                v.d = min(v.d, i);
+                if (w.bin(x, scale) == cut_bin) {
+                    v.a += w(x);
+                    ++v.e;
+                }
             }
-        }
-    });
-    const Slot fin = row.exchange(mass, kept, 0, 0, lowest);
-    const u64 S = fin.a;
-    uint32_t tok = fin.d;
-    if (u > 0.0f) {
-        const double r = floor(double(u) * double(S));
-        const u64 e = r >= double(S) ? S : min(u64(r) + 1, S);       // the first sum above u * S
-        tok = row.locate(e, [&](float x, uint32_t i) {
-            u64 wx;
-            return keeps(x, i, wx) ? wx : 0;
+        });
+    } else {
+        row.each([&](float x, uint32_t i) {
+            const u64 wx = w(x);
+            const bool in = cut.has(x, i) && wx >= floor_w;
+            v.a += in ? wx : 0;
+            v.e += in;
+            // (with +inf among the logits the others weigh nothing)
+            v.d = in && (!w.inf || wx) ? min(v.d, i) : v.d;
         });
     }
-    if (rank == 0 && tid == 0) {
-        const float x = a.x[m * a.ldx + tok];
-        const double wt = x == M ? 1.0 : exp((double(x) - double(M)) / double(T));
-        give(tok, float(wt * double(u64(1) << shift) / double(S)), int32_t(fin.b));
+    u64 before;
+    const Slot fin = exchange<kA | kE | kD>(v, row.phase, &before);
+    uint32_t tok = fin.d;
+    if (u > 0.0f) {
+        // the first sum above u * S
+        const u64 e = u >= 1.0f ? fin.a : share(u, fin.a, false) + 1;
+        tok = row.pick(e, before, kept_w);
     }
+    if (writes) finish(tok, fin.a, fin.e);
     cl.sync();      // nobody leaves while another may still write here
 }
 
@@ -653,13 +880,13 @@ template <bool RES>
 cudaError_t launch_sample_kernel(const SampleArgs& a, int size, int part, int shift, const LaunchCtx& ctx) {
     static std::atomic<bool> ready[kMaxDevices];
     const cudaError_t e =
-        set_smem_once(sample_kernel<RES>, RES ? size_t(kMaxPart) * 4 : 0, ctx.dev, ready);
+        set_smem_once(sample_kernel<RES>, sizeof(Shared) + (RES ? size_t(kMaxPart) * 4 : 0), ctx.dev, ready);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attrs[2];
     cfg.gridDim = dim3(unsigned(a.rows * size));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = RES ? size_t(part) * 4 : 0;
+    cfg.dynamicSmemBytes = sizeof(Shared) + (RES ? size_t(part) * 4 : 0);
     cfg.stream = ctx.stream;
     cfg.numAttrs = pdl_attrs(ctx, attrs);
     attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;

@@ -374,15 +374,19 @@ def draw(x, u, t=None, k=None, p=None, mp=None):
 
 
 def check_draw(x, u, t=None, k=None, p=None, mp=None):
-    """Token and count as the 64-bit form's; prob to its own rounding (2^-24)
-    and the weights' 2^-40."""
+    """Token and count as the 64-bit form's.  prob is w / S rounded to binary32
+    (2^-24): w and each term of S carry at most 2^-29 of themselves, so their
+    quotient 2^-28, and a term loses less than one unit of 2^-shift, shift = 62
+    - ceil(log2 N), of the largest weight, which S is no less than: N 2^-shift."""
+    n = x.shape[1]
+    units = n * 2.0 ** ((n - 1).bit_length() - 62)
     got = draw(x, u, t, k, p, mp)
     f32 = lambda v, d: [d] * x.shape[0] if v is None else [float(np.float32(a)) for a in v]  # noqa: E731
     xs = x.cpu().numpy()
     for m, (uu, tt, pp, mm) in enumerate(zip(f32(u, 0), f32(t, 1.0), f32(p, 1.0), f32(mp, 0.0))):
         tok, prob, kept = ref.sample(xs[m], uu, tt, 0 if k is None else k[m], pp, mm)
         assert (got[0][m], got[2][m]) == (tok, kept), (m, got[0][m], got[2][m], tok, kept)
-        assert abs(got[1][m] - prob) <= prob * (2.0 ** -24 + 2.0 ** -36) + 2.0 ** -149
+        assert abs(float(got[1][m]) - prob) <= prob * (2.0 ** -24 + 2.0 ** -28 + units) + 2.0 ** -149
 
 
 def logits(rows, n, spread=2.0, seed=0, pad=0):
