@@ -323,8 +323,10 @@ size_t head_argmax_noalloc_scratch_bytes(void);
  * cache at most 2^40 bytes; window >= -1, sinks >= 0; out overlaps no input.
  *   workspace: attn_decode_workspace(...) bytes for the same arguments (with_acc:
  *   acc is given), zeroed whole before the first call on it; every completed
- *   call leaves what it counts with at zero, so that calls of any sizes may
- *   follow one another on one workspace.  Calls sharing it must not overlap.
+ *   call leaves what it counts with at zero, so that calls of any sizes, of
+ *   kv_evict and of head_argmax too, may follow one another on one workspace
+ *   (nothing else may write its first 4096 bytes).  Calls sharing it must not
+ *   overlap.
  *   (0 bytes: arguments that attn_decode refuses.)
  */
 q8_status attn_decode(const float* q, int64_t ldq, const void* k_cache, const void* v_cache,
@@ -356,7 +358,8 @@ size_t attn_decode_workspace(int64_t rows, int64_t heads, int64_t kv_heads, int6
  * A position outside [-1, n_pos) leaves its row as it was (kept: -1) and sets
  * device error 2.  1 <= budget <= n_pos, sinks + recent <= budget, other
  * limits as attn_decode.
- *   workspace: kv_evict_workspace(rows, kv_heads, budget) bytes, of any content.
+ *   workspace: kv_evict_workspace(rows, kv_heads, budget) bytes, of any content
+ *   (the first 4096 bytes stay as they are).
  */
 q8_status kv_evict(void* k_cache, void* v_cache, int kv_type, int64_t rows, int64_t n_pos,
                    int64_t kv_heads, int64_t head_dim, const int32_t* pos, const float* acc,

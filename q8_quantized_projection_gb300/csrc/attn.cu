@@ -66,7 +66,7 @@ size_t part_bytes(int gsz, int64_t dim) {
 // [tickets][partial states][per query head: reference, 1 / sum][scores]
 size_t attn_workspace_bytes(int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim, int64_t n_pos,
                             int64_t window, int64_t sinks, bool acc) {
-    size_t n = kAttnHeader + part_bytes(block_heads(heads / kv_heads), dim);
+    size_t n = kCounterBytes + part_bytes(block_heads(heads / kv_heads), dim);
     if (acc)
         n += round256(size_t(rows * heads) * 8) +
              round256(size_t(rows * heads) * size_t(visible_cap(n_pos, window, sinks)) * 4);
@@ -86,7 +86,7 @@ cudaError_t launch_attn(const AttnArgs& a, const LaunchCtx& ctx) {
     while (a.rows * a.kv_heads * p.nb * (p.cap / (8 * p.tile_its) + 13) > INT32_MAX) p.tile_its *= 2;
     p.qscale = float(double(a.scale) * 1.4426950408889634);
     p.err = ctx.dev_err;
-    unsigned char* ws = static_cast<unsigned char*>(a.ws) + kAttnHeader;
+    unsigned char* ws = static_cast<unsigned char*>(a.ws) + kCounterBytes;
     p.part = reinterpret_cast<float*>(ws);
     if (a.acc) {
         ws += part_bytes(p.gsz, a.dim);

@@ -46,7 +46,7 @@ constexpr int kAttnWarps = 4;                         // two CTAs an SM
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnRing = 24 * 1024;                  // bytes a warp
 constexpr int kAttnMaxCtas = 512;
-constexpr size_t kAttnHeader = 4 * kAttnMaxCtas;      // one ticket a CTA
+static_assert(4 * kAttnMaxCtas <= kCounterBytes, "one ticket a CTA");
 
 struct AttnParams {
     AttnArgs a;

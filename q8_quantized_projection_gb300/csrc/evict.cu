@@ -1,11 +1,26 @@
 // evict.cu -- eviction from the K/V caches by accumulated attention weight.
 //
-// evict_select_kernel, one CTA a row and K/V head: the smallest kept weight by
-// a binary search over the 32 bits of an ordered key, then one ordered pass
-// that lists the kept entries and moves acc.  evict_move_kernel: K and V move
-// to the front, in place.  Entry j of the result comes from an entry idx[j]
-// >= j, so a tile of rows may be written as soon as the tile has been read:
-// what it overwrites is read by itself and earlier tiles only.
+// evict_select_kernel, a cluster of 1 to 8 CTAs a row and K/V head: a radix
+// selection over the weights' ordered 32-bit keys (four digits of 8 bits, a
+// histogram each, summed over the cluster through distributed shared memory;
+// three digits of 11 bits: 64 KB a CTA of 8 reads there, 25 against 17 us at
+// 32768 entries) gives the smallest kept key and how many equal to it stay; then
+// every warp counts and lists the kept entries of its own range in order.  A
+// lane holds its keys in registers where a warp's range is at most 256 entries
+// and reads them again (4 bytes against the caches' hundreds) where it is
+// longer; bound by the latency of its steps.
+//
+// evict_move_kernel: K, V and acc to the front, in place and in order.  Entry
+// j of the result comes from an entry idx[j] >= j.  A CTA owns a column slice
+// of one row and head and walks j upwards in batches: what a batch overwrites
+// is read by itself and earlier batches only, so a batch may be written once
+// all of it has been read, and the next one's reads go out before that.
+// Slices never touch, so CTAs need no order among them; the slice is as wide
+// as leaves a CTA an SM, 64 bytes at least (at 4 x 8 heads x 24576 of 32768
+// f32 entries, slices of 64, 128 and 256 bytes: 339, 299 and 361 us with the
+// selection's 52).  Bound: HBM, each moved byte read and written once.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "launch.h"
 #include "q8proj.h"
@@ -14,7 +29,12 @@ namespace q8 {
 
 namespace {
 
-constexpr int kSelThreads = 1024, kMoveThreads = 256;
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kDigit = 256, kMaxCluster = 8;
+constexpr int kHeld = 8;                      // keys a lane holds at a time
+constexpr int kBatch = 4;                     // pieces a thread has in a batch of moves
 
 // Order of the weights as unsigned integers: NaN lowest, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -23,151 +43,279 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Exclusive prefix sum over the CTA's threads; total in *all.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* s_warp, uint32_t* all) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t x = v;
-    for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-    }
-    if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
-    uint32_t before = 0, total = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-        const uint32_t t = s_warp[w];
-        if (w < warp) before += t;
-        total += t;
-    }
-    __syncthreads();
-    *all = total;
-    return before + x - v;
+// The workspace, behind other calls' counters: per row and head the place of
+// the first entry that moves (-1: none does), then its list of kept entries.
+__device__ __forceinline__ int32_t* first_moved(const EvictArgs& a) {
+    return reinterpret_cast<int32_t*>(static_cast<unsigned char*>(a.ws) + kCounterBytes);
+}
+__device__ __forceinline__ int32_t* kept_list(const EvictArgs& a, int64_t unit) {
+    return first_moved(a) + (a.rows * a.kv_heads + 63) / 64 * 64 + unit * a.budget;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int* err) {
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a, int* err) {
+    __shared__ uint32_t s_hist[2][kDigit], s_scan[kWarps], s_digit, s_above;
+    __shared__ uint2 s_warp[kWarps];                 // sure ones and ties by warp
+    __shared__ uint2 s_cta[kMaxCluster];             // and by CTA
+    cg::cluster_group cl = cg::this_cluster();
+    const unsigned rank = cl.block_rank(), size = cl.num_blocks();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t unit = blockIdx.x / size, m = unit / a.kv_heads;
+    if (tid < kDigit) s_hist[1][tid] = 0;                // (the first digit's)
     pdl_wait();
     pdl_launch_dependents();
-    __shared__ uint32_t s_warp[kSelThreads / 32];
-    const int64_t m = blockIdx.y, h = blockIdx.x, unit = m * a.kv_heads + h;
     const int pos = a.pos[m];
-    const bool bad = pos < -1 || pos >= a.n_pos;
-    if (bad && h == 0 && threadIdx.x == 0) atomicExch(err, Q8_DEVERR_POSITION);
-    const int64_t n = bad ? 0 : int64_t(pos) + 1;
+    const bool bad = pos < -1 || pos >= a.n_pos, writes = rank == 0 && tid == 0;
+    if (bad && writes && unit == m * a.kv_heads) atomicExch(err, Q8_DEVERR_POSITION);
+    const uint32_t n = bad ? 0 : uint32_t(pos) + 1;      // (n and some steps more fit 32 bits)
     const float* acc = a.acc + unit * a.n_pos;
-    float* new_acc = a.new_acc + unit * a.n_pos;
     int32_t* kept = a.kept ? a.kept + unit * a.budget : nullptr;
-    int32_t* idx = static_cast<int32_t*>(a.ws) + unit * a.budget;
-    if (n <= a.budget) {
-        for (int64_t i = threadIdx.x; i < a.n_pos; i += kSelThreads)
-            if (new_acc != acc) new_acc[i] = acc[i];
-        for (int64_t i = threadIdx.x; i < a.budget; i += kSelThreads)
-            if (kept) kept[i] = i < n ? int32_t(i) : -1;
+    int32_t* idx = kept_list(a, unit);
+    const uint32_t budget = uint32_t(a.budget);
+    if (n <= budget) {                                   // the whole cluster alike
+        if (writes) first_moved(a)[unit] = -1;
+        if (kept)
+            for (uint32_t i = rank * kThreads + tid; i < budget; i += size * kThreads) kept[i] = i < n ? int32_t(i) : -1;
         return;
     }
-    const int64_t lo = a.sinks, hi = n - a.recent;
-    const uint32_t need = uint32_t(a.budget - a.sinks - a.recent);
-    // the largest key that at least `need` entries reach (0xffffffff: need = 0)
-    uint32_t t = 0, above = 0;
-    if (need == 0) {
-        t = 0xffffffffu;
-    } else {
-        for (int b = 31; b >= 0; --b) {
-            const uint32_t cand = t | (1u << b);
-            uint32_t c = 0, all;
-            for (int64_t i = lo + threadIdx.x; i < hi; i += kSelThreads) c += weight_key(acc[i]) >= cand;
-            block_scan(c, s_warp, &all);
-            if (all >= need) t = cand;
-        }
-        uint32_t c = 0;
-        for (int64_t i = lo + threadIdx.x; i < hi; i += kSelThreads) c += weight_key(acc[i]) > t;
-        block_scan(c, s_warp, &above);
-    }
-    const uint32_t ties = need - above;   // entries equal to t that stay, the first ones
-    uint32_t done = 0, ties_seen = 0;
-    for (int64_t i0 = 0; i0 < n; i0 += kSelThreads) {
-        const int64_t i = i0 + threadIdx.x;
-        float w = 0.0f;
-        bool keep = false, tie = false;
-        if (i < n) {
-            w = acc[i];
-            keep = i < lo || i >= hi;
-            if (!keep && need) {
-                const uint32_t key = weight_key(w);
-                keep = key > t;
-                tie = key == t;
+    const uint32_t lo = uint32_t(a.sinks), hi = n - uint32_t(a.recent);
+    const uint32_t need = budget - lo - uint32_t(a.recent);
+    // this warp's range of all entries, in whole steps of 32
+    const uint32_t span = (n + size * kWarps * 32 - 1) / (size * kWarps * 32) * 32;
+    const uint32_t w0 = min((rank * kWarps + warp) * span, n), w1 = min(w0 + span, n);
+    const bool held = span <= 32 * kHeld;
+    uint32_t key[kHeld];                                 // of entries [at, at + 256), lanes in turn
+    const auto fetch = [&](uint32_t at) {
+        float w[kHeld];
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) w[j] = at + 32 * j + lane < w1 ? acc[at + 32 * j + lane] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) key[j] = weight_key(w[j]);
+    };
+    if (held) fetch(w0);
+
+    // t: the key of the need-th largest weight in [lo, hi); above: how many are larger
+    uint32_t t = 0xffffffffu, above = 0;
+    if (need) {
+        t = 0;
+        uint32_t mask = 0;                               // the digits found so far
+        const uint32_t zero = weight_key(0.0f), c1 = min(w1, hi);
+#pragma unroll 1
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            uint32_t* hist = s_hist[shift >> 3 & 1];
+            __syncthreads();                             // (the bins are zero)
+            // weights of zero, the commonest one, are counted in a register
+            uint32_t zeros = 0;
+            for (uint32_t at = w0; at < w1; at += 32 * kHeld) {
+                if (!held) fetch(at);
+#pragma unroll
+                for (int j = 0; j < kHeld; ++j) {
+                    const uint32_t i = at + 32 * j + lane;
+                    if (i < lo || i >= c1 || (key[j] & mask) != t) continue;
+                    if (key[j] == zero) ++zeros;
+                    else atomicAdd(&hist[(key[j] >> shift) & 255u], 1u);
+                }
             }
+            zeros = __reduce_add_sync(0xffffffffu, zeros);
+            if (lane == 0 && zeros) atomicAdd(&hist[(zero >> shift) & 255u], zeros);
+            cl.sync();
+            // (the other bins were last read before this barrier's other side)
+            if (tid < kDigit) s_hist[~(shift >> 3) & 1][tid] = 0;
+            // from the largest digit down: where the cluster's count reaches what is left
+            const uint32_t digit = kDigit - 1 - tid, left = need - above;
+            uint32_t c = 0, up;
+            if (tid < kDigit) {
+#pragma unroll 8
+                for (unsigned r = 0; r < size; ++r) c += cl.map_shared_rank(hist, r)[digit];
+            }
+            up = c;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, up, d);
+                if (lane >= d) up += y;
+            }
+            if (lane == 31) s_scan[warp] = up;
+            __syncthreads();
+            uint32_t before = up - c;
+            for (int k = 0; k < warp; ++k) before += s_scan[k];
+            if (tid < kDigit && before < left && before + c >= left) {
+                s_digit = digit;
+                s_above = before;
+            }
+            __syncthreads();
+            t |= s_digit << shift;
+            above += s_above;
+            mask |= 255u << shift;
         }
-        uint32_t all;
-        const uint32_t tb = block_scan(tie, s_warp, &all);
-        keep = keep || (tie && ties_seen + tb < ties);
-        ties_seen += all;
-        const uint32_t kb = block_scan(keep, s_warp, &all);
-        if (keep) {
-            const uint32_t j = done + kb;
-            idx[j] = int32_t(i);
-            if (kept) kept[j] = int32_t(i);
-            new_acc[j] = w;
-        }
-        done += all;
     }
+    const uint32_t ties = need - above;      // entries equal to t that stay, the first ones
+
+    // count this warp's kept ones: those that stay for sure, and ties
+    const auto judge = [&](uint32_t i, uint32_t k, bool& sure, bool& tie) {
+        const bool in = i < w1, mid = i >= lo && i < hi;
+        sure = in && (!mid || (need && k > t));
+        tie = in && mid && need && k == t;
+    };
+    uint2 cnt = make_uint2(0, 0);
+    for (uint32_t at = w0; at < w1; at += 32 * kHeld) {
+        if (!held) fetch(at);
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            bool sure, tie;
+            judge(at + 32 * j + lane, key[j], sure, tie);
+            cnt.x += __popc(__ballot_sync(0xffffffffu, sure));
+            cnt.y += __popc(__ballot_sync(0xffffffffu, tie));
+        }
+    }
+    if (lane == 0) s_warp[warp] = cnt;
+    if (need == 0) cl.sync();                            // (every CTA runs, else the passes' barriers say so)
     __syncthreads();
-    for (int64_t i = a.budget + threadIdx.x; i < a.n_pos; i += kSelThreads) new_acc[i] = 0.0f;
+    uint2 off = make_uint2(0, 0), all = off;
+    for (int k = 0; k < kWarps; ++k) {
+        const uint2 c = s_warp[k];
+        if (k < warp) off.x += c.x, off.y += c.y;
+        all.x += c.x, all.y += c.y;
+    }
+    if (tid < int(size)) *cl.map_shared_rank(&s_cta[rank], tid) = all;
+    cl.sync();
+    for (unsigned r = 0; r < rank; ++r) {
+        off.x += s_cta[r].x;
+        off.y += s_cta[r].y;
+    }
+    // list them; the first that does not stay lies in the warp before whose
+    // range every entry stays
+    const bool all_before = off.x + min(off.y, ties) == w0;
+    uint32_t first = n;
+    for (uint32_t at = w0; at < w1; at += 32 * kHeld) {
+        if (!held) fetch(at);
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            const uint32_t i = at + 32 * j + lane, below = (1u << lane) - 1;
+            bool sure, tie;
+            judge(i, key[j], sure, tie);
+            const unsigned vs = __ballot_sync(0xffffffffu, sure), vt = __ballot_sync(0xffffffffu, tie);
+            const uint32_t s = off.x + __popc(vs & below), e = off.y + __popc(vt & below);
+            if (sure || (tie && e < ties)) {
+                const uint32_t to = s + min(e, ties);
+                idx[to] = int32_t(i);
+                if (kept) kept[to] = int32_t(i);
+            } else if (i < w1) {
+                first = min(first, i);
+            }
+            off.x += __popc(vs);
+            off.y += __popc(vt);
+        }
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (all_before && first < n && lane == 0) first_moved(a)[unit] = int32_t(first);     // as many stay where they are
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int elt) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t m = blockIdx.y, h = blockIdx.x, unit = m * a.kv_heads + h;
-    const int pos = a.pos[m];
-    const bool over = pos < a.n_pos && int64_t(pos) + 1 > a.budget;
-    if (!over) return;
-    const int64_t chunks = a.dim * elt / 16, pitch = a.kv_heads * a.dim * elt;
-    unsigned char* base = static_cast<unsigned char*>(blockIdx.z ? a.v : a.k) +
-                          m * a.n_pos * pitch + h * a.dim * elt;
-    const int32_t* idx = static_cast<const int32_t*>(a.ws) + unit * a.budget;
-    for (int64_t c0 = 0; c0 < a.budget * chunks; c0 += kMoveThreads) {
-        const int64_t c = c0 + threadIdx.x, j = c / chunks, col = (c % chunks) * 16;
-        int4 x{};
-        const bool in = j < a.budget;
-        if (in) x = *reinterpret_cast<const int4*>(base + int64_t(idx[j]) * pitch + col);
-        __syncthreads();
-        if (in) *reinterpret_cast<int4*>(base + j * pitch + col) = x;
+// Moves items [from, budget) of 16 bytes (caches) or 4 (acc), `pitch` bytes
+// apart, each thread those that are `mine` of every `rows`; src may be dst.
+template <typename V>
+__device__ __forceinline__ void move_items(const unsigned char* src, unsigned char* dst, int64_t pitch, const int32_t* idx,
+                                           int64_t from, int64_t budget, int rows, int mine, bool has) {
+    V next[kBatch], now[kBatch];
+    const auto load = [&](int64_t j0) {
+        int at[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int64_t j = j0 + b * rows + mine;
+            at[b] = has && j < budget ? idx[j] : -1;
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (at[b] >= 0) next[b] = *reinterpret_cast<const V*>(src + int64_t(at[b]) * pitch);
+    };
+    const int step = rows * kBatch;
+    load(from);
+    for (int64_t j0 = from; j0 < budget; j0 += step) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) now[b] = next[b];
+        if (j0 + step < budget) load(j0 + step);
+        __syncthreads();                 // every read of this batch is done
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int64_t j = j0 + b * rows + mine;
+            if (has && j < budget) *reinterpret_cast<V*>(dst + j * pitch) = now[b];
+        }
     }
 }
 
-// after the moves: the new positions (pos may be new_pos)
-__global__ void evict_pos_kernel(const EvictArgs a) {
+// CTA: acc of one row and K/V head (the first ones), or its K or V in one
+// column slice of 16 << lanes_log bytes.
+__global__ void __launch_bounds__(kThreads) evict_move_kernel(const EvictArgs a, int elt, int lanes_log, int slices) {
     pdl_wait();
     pdl_launch_dependents();
-    const int m = threadIdx.x;
-    if (m >= a.rows) return;
-    const int pos = a.pos[m];
-    a.new_pos[m] = pos < a.n_pos && int64_t(pos) + 1 > a.budget ? int32_t(a.budget - 1) : pos;
+    const int64_t units = a.rows * a.kv_heads;
+    const int tid = threadIdx.x;
+    if (blockIdx.x < units) {
+        const int64_t unit = blockIdx.x, m = unit / a.kv_heads;
+        const int from = first_moved(a)[unit];
+        if (unit == m * a.kv_heads && tid == 0) {
+            // (pos may be new_pos: nobody else reads it in this kernel)
+            a.new_pos[m] = from < 0 ? a.pos[m] : int32_t(a.budget - 1);
+        }
+        const float* acc = a.acc + unit * a.n_pos;
+        float* new_acc = a.new_acc + unit * a.n_pos;
+        int64_t kept_as_is = from < 0 ? a.n_pos : from;
+        if (new_acc != acc)
+            for (int64_t i = tid; i < kept_as_is; i += kThreads) new_acc[i] = acc[i];
+        if (from < 0) return;
+        move_items<float>(reinterpret_cast<const unsigned char*>(acc), reinterpret_cast<unsigned char*>(new_acc), 4,
+                          kept_list(a, unit), from, a.budget, kThreads, tid, true);
+        __syncthreads();
+        for (int64_t i = a.budget + tid; i < a.n_pos; i += kThreads) new_acc[i] = 0.0f;
+        return;
+    }
+    const int64_t id = blockIdx.x - units;
+    const int slice = int(id % slices), kv = int(id / slices % 2);
+    const int64_t unit = id / slices / 2, m = unit / a.kv_heads, h = unit % a.kv_heads;
+    const int from = first_moved(a)[unit];
+    if (from < 0) return;
+    const int64_t row_bytes = a.dim * elt, pitch = a.kv_heads * row_bytes;
+    const int64_t col = int64_t((slice << lanes_log) + (tid & ((1 << lanes_log) - 1))) * 16;
+    unsigned char* base = static_cast<unsigned char*>(kv ? a.v : a.k) + m * a.n_pos * pitch + h * row_bytes + col;
+    move_items<int4>(base, base, pitch, kept_list(a, unit), from, a.budget, kThreads >> lanes_log, tid >> lanes_log,
+                     col < row_bytes);
 }
 
 }  // namespace
 
 size_t evict_workspace_bytes(int64_t rows, int64_t kv_heads, int64_t budget) {
-    return size_t(rows * kv_heads) * size_t(budget) * sizeof(int32_t);
+    const size_t units = size_t(rows * kv_heads);
+    return kCounterBytes + ((units + 63) / 64 * 64 + units * size_t(budget)) * sizeof(int32_t);
 }
 
 cudaError_t launch_evict(const EvictArgs& a, const LaunchCtx& ctx) {
+    const int64_t units = a.rows * a.kv_heads;
+    // CTAs a row and head: so many that lanes hold their keys, where 8 reach that
+    // (4096 entries on one CTA: 9 us, on four: 12)
+    int size = 1;
+    while (size < kMaxCluster && a.n_pos > int64_t(size) * kThreads * kHeld) size *= 2;
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attrs[1];
+    cudaLaunchAttribute attrs[2];
     cfg.stream = ctx.stream;
     cfg.numAttrs = pdl_attrs(ctx, attrs);
+    attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attrs[cfg.numAttrs].val.clusterDim.x = unsigned(size);
+    attrs[cfg.numAttrs].val.clusterDim.y = 1;
+    attrs[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
     cfg.attrs = attrs;
-    cfg.gridDim = dim3(unsigned(a.kv_heads), unsigned(a.rows));
-    cfg.blockDim = dim3(kSelThreads);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ctx.dev_err);
+    cfg.gridDim = dim3(unsigned(units * size));
+    cfg.blockDim = dim3(kThreads);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ctx.dev_err);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(unsigned(a.kv_heads), unsigned(a.rows), 2);
-    cfg.blockDim = dim3(kMoveThreads);
-    e = cudaLaunchKernelEx(&cfg, evict_move_kernel, a, a.kv_type == Q8_KV_F32 ? 4 : 2);
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(256);
-    return cudaLaunchKernelEx(&cfg, evict_pos_kernel, a);
+    // the widest slice that leaves a CTA an SM, 64 bytes at least
+    const int elt = a.kv_type == Q8_KV_F32 ? 4 : 2, chunks = int(a.dim) * elt / 16;      // 16-byte pieces an entry
+    int lanes_log = 5;
+    const auto slices_at = [&](int log) { return (chunks + (1 << log) - 1) >> log; };
+    while (lanes_log > 2 && ((1 << (lanes_log - 1)) >= chunks || units * 2 * slices_at(lanes_log) < ctx.num_sms))
+        --lanes_log;
+    const int slices = slices_at(lanes_log);
+    cfg.numAttrs = pdl_attrs(ctx, attrs);
+    cfg.gridDim = dim3(unsigned(units + units * 2 * slices));
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel, a, elt, lanes_log, slices);
 }
 
 }  // namespace q8

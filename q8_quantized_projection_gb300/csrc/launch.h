@@ -157,6 +157,13 @@ static_assert(gemv_max_rows(0) <= kArgmaxGroupRows && gemv_max_rows(1) <= kArgma
 constexpr int64_t kMaxHeads = 1024;                 // query or K/V heads of one call
 constexpr int64_t kSampleMaxN = int64_t(1) << 20;   // logits of one row
 
+// The first bytes of a workspace hold counters that are zero between calls
+// (head_argmax's and attn_decode's); kv_evict leaves them alone and
+// attn_decode's states begin behind them, so that one workspace may serve the
+// three in turn.
+constexpr size_t kCounterBytes = 4096;
+static_assert(kArgmaxGemvOff + kArgmaxHeader <= kCounterBytes, "head_argmax's counters");
+
 // Attention of one token a sequence over its K/V cache (attn.cu).
 struct AttnArgs {
     const float* q;

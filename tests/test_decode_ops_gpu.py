@@ -215,6 +215,33 @@ def test_attn_one_workspace_for_calls_of_other_sizes():
         c.check()
 
 
+def test_one_workspace_for_attention_eviction_and_head():
+    """The three calls whose workspace may be one buffer, in turn, several times."""
+    t = torch()
+    from q8_quantized_projection_gb300 import synth
+    a = Attn("f16", [3000, 100, 2500], 8, 2, 64, 3001, seed=1)
+    e = Evict("f32", [799, 300], 3, 32, 800, 400, sinks=2, recent=9, seed=2)
+    rows, n, k = 3, 4096, 1024
+    rng = synth.rng_for(5)
+    q, s = synth.q8_weights(rng, n, k)
+    qd, sd = t.from_numpy(q).cuda(), t.from_numpy(s.view(np.int16)).cuda()
+    xq, xd = native.activation_buffers("i8", rows, k)
+    native.act_quant("i8", t.randn(rows, k, device="cuda"), xq, xd)
+    y = t.empty(rows, n, device="cuda")
+    native.q8_proj("i8", qd, sd, xq, xd, rows, y)
+    size = max(a.ws.numel(), e.ws.numel(), native.head_argmax_workspace(rows))
+    ws = t.zeros(size, dtype=t.uint8, device="cuda")
+    a.ws = e.ws = ws
+    tok = t.empty(rows, dtype=t.int32, device="cuda")
+    for _ in range(3):
+        a.check()
+        e.posd.copy_(t.tensor(e.pos, dtype=t.int32))
+        e.check()
+        tok.fill_(-1)
+        native.head_argmax("i8", qd, sd, xq, xd, rows, tok, ws)
+        assert t.equal(tok.long(), y.argmax(1))
+
+
 def test_attn_offsets_past_32_bits():
     """The second row's entries lie past 2^31 values and 2^32 bytes."""
     t = torch()
