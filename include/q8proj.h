@@ -381,14 +381,15 @@ size_t kv_evict_workspace(int64_t rows, int64_t kv_heads, int64_t budget);
  * all), then to the shortest beginning that holds at least top_p of the mass
  * left (>= 1: all), then to those with w_i >= min_p; the first always stays.
  *   tok[m]   the smallest kept i whose sum of w over the kept j <= i exceeds
- *            u times their whole sum (u = 0: the lowest kept one)
+ *            u times their whole sum (u = 0: the lowest kept one of a weight
+ *            of at least 2^-126)
  *   prob     float [rows] or NULL: w over that sum, for the token
  *   kept     int32 [rows] or NULL: how many tokens were kept
- * temperature 0 (or below 2^-60) takes the arg-max (prob 1, kept 1).  Logits of -inf
- * or NaN are never drawn; where there are +inf, those weigh 1 and all others
- * 0.  A row without any other logit gives token 0, prob 0 and kept 0; so does
- * a row whose temperature is negative or NaN, or whose top_p or min_p is NaN,
- * which also sets device error 3.  Weights are integers in units of
+ * temperature 0 (or below 2^-60) takes the arg-max (prob 1, kept 1).  Logits of
+ * -inf or NaN are never drawn; +inf counts as the largest float.  A row
+ * without any other logit gives token 0, prob 0 and kept 0; so does a row whose
+ * temperature is negative or NaN, or whose top_p or min_p is NaN, which also
+ * sets device error 3.  Weights are integers in units of
  * 2^-(62 - ceil(log2 N)) of the largest, rounded down, within 2^-29 of their
  * value before that, and their sums are exact: a row's token depends on
  * nothing but its own row and settings.

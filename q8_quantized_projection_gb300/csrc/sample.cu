@@ -69,7 +69,7 @@ struct Shared {
     float cut_x;                            // the cut that the first CTA found
     uint32_t cut_i;
     uint32_t found;                         // an index, bin or place that one thread found
-    uint2 pow2[32];                         // 2^(j/32): in units of 2^-31, and as a float of those
+    uint2 pow2[64];                         // 2^(j/64): in units of 2^-31, and as a float of those
 };
 
 // The dynamic shared memory: Shared, then the CTA's part of the row.
@@ -77,6 +77,9 @@ extern __shared__ __align__(16) unsigned char smem[];
 __device__ __forceinline__ Shared& sh() { return *reinterpret_cast<Shared*>(smem); }
 __device__ __forceinline__ float* sh_x() { return reinterpret_cast<float*>(smem + sizeof(Shared)); }
 static_assert(sizeof(Shared) % 16 == 0 && sizeof(Shared) + 4 * kMaxPart <= 227 * 1024, "shared memory");
+
+// A logit as it is taken: NaN as -inf (never drawn), +inf as the largest float.
+__device__ __forceinline__ float clean(float v) { return v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY; }
 
 // Order of the logits as unsigned integers; 0: NaN or -inf, never drawn.
 __device__ __forceinline__ uint32_t logit_key(float x) {
@@ -88,28 +91,29 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// 2^(j/32) in units of 2^-31.
-__constant__ uint32_t kPow2[32] = {
-    2147483648u, 2194507417u, 2242560872u, 2291666561u, 2341847524u, 2393127307u,
-    2445529972u, 2499080105u, 2553802834u, 2609723834u, 2666869345u, 2725266179u,
-    2784941738u, 2845924021u, 2908241642u, 2971923842u, 3037000500u, 3103502151u,
-    3171459999u, 3240905930u, 3311872529u, 3384393094u, 3458501653u, 3534232978u,
-    3611622603u, 3690706840u, 3771522796u, 3854108391u, 3938502376u, 4024744348u,
-    4112874773u, 4202935003u};
+// 2^(j/64) in units of 2^-31.
+__constant__ uint32_t kPow2[64] = {
+    2147483648u, 2170868212u, 2194507417u, 2218404036u, 2242560872u, 2266980759u, 2291666561u, 2316621173u,
+    2341847524u, 2367348571u, 2393127307u, 2419186755u, 2445529972u, 2472160047u, 2499080105u, 2526293303u,
+    2553802834u, 2581611923u, 2609723834u, 2638141863u, 2666869345u, 2695909648u, 2725266179u, 2754942382u,
+    2784941738u, 2815267765u, 2845924021u, 2876914102u, 2908241642u, 2939910317u, 2971923842u, 3004285971u,
+    3037000500u, 3070071267u, 3103502151u, 3137297074u, 3171459999u, 3205994934u, 3240905930u, 3276197082u,
+    3311872529u, 3347936457u, 3384393094u, 3421246719u, 3458501653u, 3496162267u, 3534232978u, 3572718252u,
+    3611622603u, 3650950594u, 3690706840u, 3730896002u, 3771522796u, 3812591987u, 3854108391u, 3896076880u,
+    3938502376u, 3981389855u, 4024744348u, 4068570940u, 4112874773u, 4157661043u, 4202935003u, 4248701965u};
 
 // Weights of a row.  The exponent y = (x - M) log2(e) / T is carried as an
 // unevaluated sum of two floats (the difference by the exact two-term sum, its
-// product with a two-term constant), split into J/32 + h with |h| <= 1/64 and
-// a little; 2^h - 1 is its Taylor polynomial to degree 4 (remainder 2^-40).
+// product with a two-term constant), split into J/64 + h with |h| <= 1/128 and
+// a little; 2^h - 1 is its Taylor polynomial to degree 3 (remainder 2^-34).
 // The largest error is that polynomial's and h's own rounding, 2^-29 of the
 // weight; sums over n tokens average it, so that fewer than one draw in 10^7
 // has a border within it.
 struct Weights {
     float M, pre, ch, cl;   // pre: 1/2 where differences could overflow
     int shift;
-    bool inf;               // M is +inf
 
-    // 2^y as mantissa (in [2^31, 2^32)) * 2^(J/32 - 31 whole part); false: below half a unit
+    // 2^y as mantissa (in units of 2^-31, up to 2^32) * 2^n; false: below one unit
     __device__ __forceinline__ bool parts(float x, uint32_t& mant, int& n) const {
         const float a = x * pre, s = a - M, bb = s - a;
         const float err = (a - (s - bb)) + (-M - bb);
@@ -117,36 +121,35 @@ struct Weights {
         float e = fmaf(s, ch, -p);
         e = fmaf(s, cl, e);
         e = fmaf(err, ch, e);
-        const float kRound = 393216.0f;                  // 1.5 * 2^18: one step is 1/32
+        const float kRound = 196608.0f;                  // 1.5 * 2^17: one step is 1/64
         const float r = p + kRound;
         const int J = __float_as_int(r) - __float_as_int(kRound);
         const float h = (p - (r - kRound)) + e;
-        float q = fmaf(h, 0.009618129f, 0.05550411f);    // ln(2)^4/24, ln(2)^3/6, ...
-        q = fmaf(h, q, 0.2402265f);
+        float q = fmaf(h, 0.05550411f, 0.2402265f);      // ln(2)^3/6, ln(2)^2/2, ln(2)
         q = fmaf(h, q, 0.6931472f);
         q *= h;
-        const uint2 t = sh().pow2[J & 31];
+        const uint2 t = sh().pow2[J & 63];
         mant = t.x + uint32_t(__float2int_rn(__uint_as_float(t.y) * q));
-        n = J >> 5;
+        n = J >> 6;
         return p > -float(shift);
     }
     __device__ __forceinline__ u64 operator()(float x) const {
         uint32_t mant;
         int n;
         const bool any = parts(x, mant, n);
-        if (inf) return x == INFINITY ? u64(1) << shift : 0;
-        const int up = shift - 31 + n;                   // mant * 2^up: one of the two factors is 1
-        const uint32_t lo = mant >> min(max(-up, 0), 31), hi = 1u << max(min(up, 31), 0);
-        return any ? u64(lo) * hi : 0;
+        return (u64(any ? mant : 0u) << 31) >> ((62 - shift - n) & 63);
+    }
+    // the histogram's coordinate: bin b holds b <= y < b + 1, the last one all that lies lower
+    __device__ __forceinline__ float depth(float x, float scale) const {
+        return (M - x * pre) * scale;
     }
     // the histogram's bin: (M - x) * scale, the last one for all that lies lower
     __device__ __forceinline__ int bin(float x, float scale) const {
-        const float y = inf ? (x == INFINITY ? 0.0f : float(kBins)) : (M - x * pre) * scale;
+        const float y = depth(x, scale);
         return y < float(kBins - 1) ? int(y) : kBins - 1;
     }
-    // 2^y to about 2^-21, for the histogram
+    // 2^y to about 2^-21, for the histogram; 0 below 2^-126
     __device__ __forceinline__ float rough(float x) const {
-        if (inf) return x == INFINITY ? 1.0f : 0.0f;
         float r;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((x * pre - M) * ch));
         return r;
@@ -339,13 +342,13 @@ struct Row {
         return make_float4(at(e), at(e + 1), at(e + 2), at(e + 3));
     }
     __device__ __forceinline__ float at(uint32_t e) const {
-        const float v = e < n ? __ldg(x + e) : -INFINITY;
-        return v > -INFINITY ? v : -INFINITY;       // NaN too
+        return e < n ? clean(__ldg(x + e)) : -INFINITY;
     }
 
-    // Lists those of a lane's four tokens that `in` names (all lanes call).
-    __device__ __forceinline__ void list(const bool (&in)[4], float4 v, uint32_t i) {
-        if (!__any_sync(0xffffffffu, in[0] | in[1] | in[2] | in[3])) return;
+    // Lists those of a lane's four tokens that `in` names (all lanes call);
+    // whether the warp had any.
+    __device__ __forceinline__ bool list(const bool (&in)[4], float4 v, uint32_t i) {
+        if (!__any_sync(0xffffffffu, in[0] | in[1] | in[2] | in[3])) return false;
         const float x[4] = {v.x, v.y, v.z, v.w};
         Shared& s = sh();
 #pragma unroll
@@ -354,6 +357,7 @@ struct Row {
                 const uint32_t at = atomicAdd(&s.listed, 1u);
                 if (at < kList) s.mine[at] = (u64(logit_key(x[j])) << 32) | uint32_t(~(i + j));
             }
+        return true;
     }
     // First CTA, behind the exchange (of e2: tokens listed) that ended the
     // listing: the parts as one list of n <= kList tokens.  The other CTAs keep
@@ -487,25 +491,28 @@ __device__ __forceinline__ bool cut_by_bins(Row<RES>& row, const Weights& w, flo
     // (nobody reads another CTA's bins, or this CTA's `found`, behind the next barrier)
     for (int attempt = 0; attempt < 3; ++attempt) {
         Slot v;
+        const float y0 = float(B), y1 = B < kBins - 1 ? float(B + 1) : INFINITY;
         row.quads([&](float4 x4, uint32_t i) {
             const float x[4] = {x4.x, x4.y, x4.z, x4.w};
             bool in[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const u64 fx = f(x[j], i + j);
-                const int b = w.bin(x[j], scale);
+                const float y = w.depth(x[j], scale);
                 v.a += fx;
-                if (b < B) {
-                    v.b += fx;
-                    v.e += fx != 0;
-                }
-                in[j] = b == B && fx != 0;
-                if (in[j]) {
-                    v.g += fx;
-                    ++v.e2;
-                }
+                const bool up = y < y0 && fx != 0;
+                v.b += up ? fx : 0;
+                v.e += up;
+                in[j] = !(y < y0) && y <= y1 && fx != 0 && (y < y1 || B == kBins - 1);
             }
-            row.list(in, x4, i);
+            if (row.list(in, x4, i)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (in[j]) {
+                        v.g += f(x[j], i + j);
+                        ++v.e2;
+                    }
+            }
         });
         const Slot all = exchange<kA | kB | kG | kE2>(v, row.phase);
         const u64 need = need_of(all.a);
@@ -603,7 +610,8 @@ __device__ __noinline__ void draw_from_list(const Weights& w, const Settings& g,
     }
     __syncthreads();
     n = int(s.found);
-    // what is left, in index order: (~index, place), 0 for what min-p drops
+    // what is left, in index order: (~index, weight not 0 in binary32, place); 0
+    // for what min-p drops
     part = 0;
     uint32_t cnt = 0;
     for (int j = at0; j < at1; ++j) {
@@ -612,24 +620,24 @@ __device__ __noinline__ void draw_from_list(const Weights& w, const Settings& g,
             part += wt[j];
             ++cnt;
         }
-        a[j] = in ? (a[j] << 32) | uint32_t(j) : 0;
+        const uint32_t positive = w.rough(list_x(a[j])) > 0.0f ? 0x10000u : 0u;
+        a[j] = in ? (a[j] << 32) | positive | uint32_t(j) : 0;
     }
     block_scan(part, &sum);
     u64 cnt_all;
     block_scan(cnt, &cnt_all);
     sort_down(a, n);
     const int at2 = min(at0 + per, int(cnt_all));
-    // the first sum above u * S
+    // the first sum above u * S; u = 0: the first whose weight is not 0
     const u64 e = g.u >= 1.0f ? sum : g.u > 0.0f ? share(g.u, sum, false) + 1 : 1;
+    const auto counts = [&](u64 v) { return g.u > 0.0f ? wt[v & 0xffffu] : v >> 16 & 1; };
     part = 0;
-    for (int j = at0; j < at2; ++j) part += wt[uint32_t(a[j])];
+    for (int j = at0; j < at2; ++j) part += counts(a[j]);
     u64 whole;
     run = block_scan(part, &whole);
     for (int j = at0; j < at2; ++j) {
-        const u64 x = wt[uint32_t(a[j])];
-        // (u = 0 draws the first, whose weight may be below half a unit)
-        const bool hit = g.u > 0.0f || w.inf ? run < e && run + x >= e : j == 0;
-        if (hit) s.found = uint32_t(j);
+        const u64 x = counts(a[j]);
+        if (run < e && run + x >= e) s.found = uint32_t(j);
         run += x;
     }
     __syncthreads();
@@ -645,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
     const unsigned rank = cl.block_rank(), size = cl.num_blocks();
     const int tid = threadIdx.x, lane = tid & 31;
     const int64_t m = blockIdx.x / size;
-    if (tid < 32) s.pow2[tid] = make_uint2(kPow2[tid], __float_as_uint(float(kPow2[tid])));
+    if (tid < 64) s.pow2[tid] = make_uint2(kPow2[tid], __float_as_uint(float(kPow2[tid])));
     if (tid == 0) s.listed = 0;
     pdl_wait();
     pdl_launch_dependents();
@@ -675,7 +683,6 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
     Row<RES> row{gx, base, n, part / kPart, rank, size, 0};
     if constexpr (RES) {
         float* x = sh_x();
-        const auto clean = [](float v) { return v > -INFINITY ? v : -INFINITY; };   // NaN is never drawn
         if ((reinterpret_cast<uintptr_t>(gx) & 15) == 0) {
 #pragma unroll 8
             for (int e = tid * 4; e < part; e += kThreads * 4) {
@@ -692,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
             }
         } else {
 #pragma unroll 8
-            for (int e = tid; e < part; e += kThreads) x[e] = clean(e < int(n) ? __ldg(gx + e) : -INFINITY);
+            for (int e = tid; e < part; e += kThreads) x[e] = e < int(n) ? clean(__ldg(gx + e)) : -INFINITY;
         }
         __syncthreads();
     }
@@ -742,7 +749,6 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
     }
 
     Weights w;
-    w.inf = M == INFINITY;
     w.pre = fmaxf(fabsf(M), fabsf(key_logit(low))) > 1e38f ? 0.5f : 1.0f;
     w.M = M * w.pre;
     // log2(e) / T in two floats, from log2(e) in two
@@ -754,11 +760,18 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
     const u64 one = u64(1) << shift;
     Settings set{p, u, mp > 0.0f ? share(mp, one, true) : 0, k};
     const auto finish = [&](uint32_t tok, u64 S, uint32_t kept) {
+        // the weight's mantissa over the sum's 48 leading bits, both in two floats
         uint32_t mant;
         int e;
-        w.parts(a.x[m * a.ldx + tok], mant, e);
-        const double wt = w.inf ? double(one) : ldexp(double(mant), shift - 31 + e);
-        give(tok, float(wt / double(S)), int32_t(kept));
+        w.parts(clean(a.x[m * a.ldx + tok]), mant, e);
+        const int z = __clzll(S);
+        const u64 top48 = S << z >> 16;                                // S = top48 * 2^(16 - z)
+        const float nh = float(mant & 0xffffff00u), nl = float(mant & 255u);
+        const float dh = float(uint32_t(top48 >> 24)) * 16777216.0f, dl = float(uint32_t(top48) & 0xffffffu);
+        const float q = __fdiv_rn(nh, dh), r = fmaf(-q, dh, nh) + fmaf(-q, dl, nl);
+        const int by = e - 31 + shift - 16 + z;                        // mant * 2^(e - 31 + shift) / S
+        const float prob = q + __fdiv_rn(r, dh);                       // (of 2^-17 to 2^-14)
+        give(tok, ldexpf(prob, by), int32_t(kept));
     };
     const float span = w.M - key_logit(low) * w.pre;      // of all logits (0: all equal)
     const auto bins_over = [&](float d) {
@@ -817,14 +830,15 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
         // tokens of less than (1 - p) S / N hold less than the share 1 - p
         // together, so the nucleus ends above them: the bins stop there
         const float least = (1.0f - p) * S / float(all.e) * 0.99f;
-        scale = bins_over(w.inf ? span : -log2f(least) / w.ch);
+        scale = bins_over(-log2f(least) / w.ch);
+        // (the weight of -inf is 0: without a cut before, every logit may be asked)
         const auto f = [&](float x, uint32_t i) {
             const u64 wx = w(x);
-            return before.has(x, i) ? wx : 0;
+            return !by_k || before.has(x, i) ? wx : 0;
         };
         const auto rough = [&](float x, uint32_t i) {
             const uint32_t r = __float2uint_rn(w.rough(x) * unit);
-            return before.has(x, i) ? r : 0u;
+            return !by_k || before.has(x, i) ? r : 0u;
         };
         u64 need = 0;
         const auto need_of = [&](u64 sum) { return need = share(p, sum, true); };
@@ -847,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
         v.e = above_n;
         row.each([&](float x, uint32_t i) {
             if (cut.has(x, i)) {
-                v.d = min(v.d, i);
+                if (w.rough(x) > 0.0f) v.d = min(v.d, i);
                 if (w.bin(x, scale) == cut_bin) {
                     v.a += w(x);
                     ++v.e;
@@ -860,8 +874,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
             const bool in = cut.has(x, i) && wx >= floor_w;
             v.a += in ? wx : 0;
             v.e += in;
-            // (with +inf among the logits the others weigh nothing)
-            v.d = in && (!w.inf || wx) ? min(v.d, i) : v.d;
+            v.d = in && w.rough(x) > 0.0f ? min(v.d, i) : v.d;
         });
     }
     u64 before;
