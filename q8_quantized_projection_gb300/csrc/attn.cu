@@ -23,21 +23,27 @@ __global__ void __launch_bounds__(kAccThreads) attn_acc_kernel(const AttnParams 
     const Visible vis = visible(a.pos[m], a.n_pos, a.window, a.sinks);
     float* acc = a.acc + int64_t(blockIdx.x) * a.n_pos;
     const int64_t step = int64_t(gridDim.y) * kAccThreads * kAccPer;
-    for (int64_t v0 = int64_t(blockIdx.y) * kAccThreads * kAccPer; v0 < vis.nvis; v0 += step) {
-        float w[kAccPer] = {};
+    for (int64_t v0 = int64_t(blockIdx.y) * kAccThreads * kAccPer + threadIdx.x; v0 < vis.nvis; v0 += step) {
+        float w[kAccPer] = {}, old[kAccPer];
+#pragma unroll
+        for (int j = 0; j < kAccPer; ++j) {
+            const int64_t v = v0 + j * kAccThreads;
+            if (v < vis.nvis) old[j] = acc[v + (v < vis.ns ? 0 : vis.gap)];
+        }
+#pragma unroll 4
         for (int64_t g = m * a.heads + h * group; g < m * a.heads + (h + 1) * group; ++g) {
             const float2 ml = p.ml[g];
             const float* s = p.scores + g * p.cap;
 #pragma unroll
             for (int j = 0; j < kAccPer; ++j) {
-                const int64_t v = v0 + j * kAccThreads + threadIdx.x;
+                const int64_t v = v0 + j * kAccThreads;
                 if (v < vis.nvis) w[j] += ex2(s[v] - ml.x) * ml.y;
             }
         }
 #pragma unroll
         for (int j = 0; j < kAccPer; ++j) {
-            const int64_t v = v0 + j * kAccThreads + threadIdx.x;
-            if (v < vis.nvis) acc[v + (v < vis.ns ? 0 : vis.gap)] += w[j];
+            const int64_t v = v0 + j * kAccThreads;
+            if (v < vis.nvis) acc[v + (v < vis.ns ? 0 : vis.gap)] = old[j] + w[j];
         }
     }
 }
@@ -58,7 +64,7 @@ int block_heads(int64_t group) {
 
 size_t part_bytes(int gsz, int64_t dim) {
     const int ng = gsz <= 2 ? gsz : gsz <= 4 ? 4 : 8;
-    return round256(size_t(2) * kAttnMaxCtas * ng * size_t(dim + 2) * 4);
+    return round256(size_t(2) * kAttnMaxCtas * attn_slot(ng, dim) * 4);
 }
 
 }  // namespace
@@ -81,9 +87,9 @@ cudaError_t launch_attn(const AttnArgs& a, const LaunchCtx& ctx) {
     p.nb = int((group + p.gsz - 1) / p.gsz);
     p.cap = visible_cap(a.n_pos, a.window, a.sinks);
     // all tiles of all units number below 2^31: a stage of all warps holds 8
-    // entries at least, and a unit counts at most 12 tiles more
+    // entries at least, and a unit counts at most 16 tiles more
     p.tile_its = 1;
-    while (a.rows * a.kv_heads * p.nb * (p.cap / (8 * p.tile_its) + 13) > INT32_MAX) p.tile_its *= 2;
+    while (a.rows * a.kv_heads * p.nb * (p.cap / (8 * p.tile_its) + 17) > INT32_MAX) p.tile_its *= 2;
     p.qscale = float(double(a.scale) * 1.4426950408889634);
     p.err = ctx.dev_err;
     unsigned char* ws = static_cast<unsigned char*>(a.ws) + kCounterBytes;

@@ -24,8 +24,9 @@
 //
 // Split.  A unit is a row's K/V head (and block of at most 8 query heads); its
 // visible entries are tiles of 4 warps x KT (several such where the tiles would
-// not fit 32 bits), and it counts EXTRA tiles more for what it costs to begin
-// and end.  The tiles of all units in one line are cut evenly over the CTAs, so
+// not fit 32 bits), and it counts some tiles more for what it costs to begin
+// and end (128 KB of loads where CTAs have long shares: of 64,
+// 128, 192 and 256 KB the best on long and ragged batches).  The tiles of all units in one line are cut evenly over the CTAs, so
 // ragged batches balance and one long sequence fills the GPU; lengths are read
 // on the device, so one captured graph serves every step.  Two CTAs of four
 // warps an SM: one streams while the other ends a unit.  A unit cut between CTAs leaves
@@ -48,12 +49,17 @@ constexpr int kAttnRing = 24 * 1024;                  // bytes a warp
 constexpr int kAttnMaxCtas = 512;
 static_assert(4 * kAttnMaxCtas <= kCounterBytes, "one ticket a CTA");
 
+// Floats of a partial state, whole 16-byte words.
+__host__ __device__ constexpr size_t attn_slot(int ng, int64_t dim) {
+    return size_t(ng) * size_t(dim) + size_t(ng == 1 ? 4 : 2 * ng);
+}
+
 struct AttnParams {
     AttnArgs a;
     int nb, gsz;          // blocks of query heads a K/V head, heads a block
     int tile_its;         // stages a warp takes in one tile
     int64_t cap;          // entries of a row that can be visible
-    float* part;          // [2 * CTAs][NG][D + 2]: o, r, l
+    float* part;          // [2 * CTAs][attn_slot(NG, D)]: o [NG][D], then (r, l) [NG]
     float2* ml;           // [rows][heads]: reference and 1 / sum (acc)
     float* scores;        // [rows][heads][cap] (acc)
     float qscale;         // scale * log2(e)
@@ -62,15 +68,15 @@ struct AttnParams {
 
 // The visible entries in order: entry v of nvis is cache row v + (v < ns ? 0 : gap).
 struct Visible {
-    int64_t nvis, ns, gap;
+    uint32_t nvis, ns, gap;
 };
 
 __device__ __forceinline__ Visible visible(int pos, int64_t n_pos, int64_t window, int64_t sinks) {
     if (pos < -1 || pos >= n_pos) return {0, 0, 0};
-    const int64_t n = int64_t(pos) + 1;
+    const uint32_t n = uint32_t(pos) + 1;
     if (window < 0 || window >= n) return {n, n, 0};
-    const int64_t ns = sinks < n - window ? sinks : n - window;
-    return {ns + window, ns, n - window - ns};
+    const uint32_t rest = n - uint32_t(window), ns = sinks < rest ? uint32_t(sinks) : rest;
+    return {ns + uint32_t(window), ns, rest - ns};
 }
 
 typedef unsigned long long f32x2;   // two binary32 values
@@ -148,7 +154,7 @@ struct AttnShape {
     static constexpr int S0 = kAttnRing / (2 * HALF);
     static constexpr int S = S0 > 6 ? 6 : S0;                 // stages
     static constexpr int TK = kAttnWarps * KT;                // entries a stage of all warps
-    static constexpr int EXTRA = (48 * 1024 + kAttnWarps * 2 * HALF - 1) / (kAttnWarps * 2 * HALF);
+    static constexpr int EXTRA = (128 * 1024 + kAttnWarps * 2 * HALF - 1) / (kAttnWarps * 2 * HALF);
     static constexpr int NV = U * NG;                         // scores of an entry group a stage
     static constexpr int R = NV > LPK ? NV / LPK : 1;         // scores a lane ends with
     static constexpr int DUP = LPK > NV ? LPK / NV : 1;       // lanes holding the same scores
@@ -198,8 +204,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                 s_pos[m] = pos;
                 if (blockIdx.x == 0 && (pos < -1 || pos >= a.n_pos)) atomicExch(p.err, Q8_DEVERR_POSITION);
                 // (up to 2^31 - 1 entries, so 32 bits hold the rounding up)
-                const uint32_t nvis = uint32_t(visible(pos, a.n_pos, a.window, a.sinks).nvis);
-                x += ((nvis ? (nvis + TT - 1) / TT : 1) + T::EXTRA) * per_row;
+                const uint32_t nvis = visible(pos, a.n_pos, a.window, a.sinks).nvis;
+                x += (nvis ? (nvis + TT - 1) / TT : 1) * per_row;
             }
             n[i] = x;
         }
@@ -217,10 +223,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         for (int i = 0; i < PER; ++i) s_pre[tid * PER + i + 1] = x - own + n[i];
         __syncthreads();
     }
-    // CTA c has tiles [first(c), first(c + 1)): W in equal shares, the first ones
-    // one longer, none below 4 (a shorter share costs more to join than it saves)
-    const uint32_t W = s_pre[rows];
-    const uint32_t ctas = max(min(W / 4, gridDim.x), 1u), cta = blockIdx.x;
+    // CTA c has tiles [first(c), first(c + 1)): all of them in equal shares, the
+    // first ones one longer.  Small problems: two tiles a CTA (fewer cost more to
+    // join than they save), or a unit.
+    const uint32_t real = s_pre[rows], units = uint32_t(rows) * per_row;
+    const uint32_t extra = real >= 4 * gridDim.x ? T::EXTRA : 1, W = real + extra * units;
+    const uint32_t ctas = min(max(real / 2, units), gridDim.x), cta = blockIdx.x;
+    __syncthreads();
+    for (int i = tid; i <= rows; i += kAttnThreads) s_pre[i] += extra * i * per_row;
+    __syncthreads();
     if (cta >= ctas) return;
     const uint32_t share = W / ctas, longer = W % ctas;
     const auto first = [&](uint32_t c) { return c * share + min(c, longer); };
@@ -239,7 +250,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
             if (s_pre[mid] <= t0) lo = mid; else hi = mid - 1;
         }
         const int m = lo;
-        const uint32_t span = (s_pre[m + 1] - s_pre[m]) / per_row, tiles = span - T::EXTRA;
+        const uint32_t span = (s_pre[m + 1] - s_pre[m]) / per_row, tiles = span - extra;
         const uint32_t unit = (t0 - s_pre[m]) / span;
         const uint32_t unit0 = s_pre[m] + unit * span;              // the unit's first tile
         if (t0 >= unit0 + tiles) {                                  // in its extra ones
@@ -252,34 +263,41 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         const int g0 = h * group + b * p.gsz;                       // the block's first query head
         const int ng = min(p.gsz, group - b * p.gsz);
         const Visible vis = visible(s_pos[m], a.n_pos, a.window, a.sinks);
-        const int64_t pitch = a.kv_heads * D * T::ELT;
+        const uint32_t pitch = uint32_t(a.kv_heads) * D * T::ELT;      // (below 2^21)
         const int64_t off = (int64_t(m) * a.n_pos * a.kv_heads + h) * D * T::ELT;
-        const unsigned char* kp = static_cast<const unsigned char*>(a.k) + off;
-        const unsigned char* vp = static_cast<const unsigned char*>(a.v) + off;
-        // this warp's entries: KT of every TK from v_begin on (at most 2^31 - 1 are visible)
-        const int64_t upto = int64_t(t1 - unit0) * TT;
-        const int v_end = int(vis.nvis < upto ? vis.nvis : upto);
-        const int64_t v_begin = int64_t(t0 - unit0) * TT + warp * T::KT;
-        const int its = v_end > v_begin ? int((v_end - v_begin + T::TK - 1) / T::TK) : 0;
+        // this warp's entries: KT of every TK from v_begin on.  At most 2^31 - 1 are
+        // visible, so 32 bits hold every index and a tile more.
+        const uint64_t upto = uint64_t(t1 - unit0) * TT;
+        const uint32_t v_end = uint32_t(vis.nvis < upto ? vis.nvis : upto);
+        const uint64_t v_from = uint64_t(t0 - unit0) * TT + warp * T::KT;
+        const uint32_t v_begin = uint32_t(v_from);
+        const int its = v_end > v_from ? int((v_end - v_begin + T::TK - 1) / T::TK) : 0;
+        // (a lane copies the same 16-byte column of every row it copies)
+        constexpr int CPR = T::PITCH / 16, RPI = CPR < 32 ? 32 / CPR : 1;   // chunks a row, rows at a time
+        const int r0 = CPR < 32 ? lane / CPR : 0, c0 = lane % CPR;
+        const unsigned char* kp = static_cast<const unsigned char*>(a.k) + off + c0 * 16;
+        const unsigned char* vp = static_cast<const unsigned char*>(a.v) + off + c0 * 16;
+        const uint32_t dst0 = ring_s + r0 * T::PITCH + (LPK == 4 ? c0 ^ (r0 & 1) * 4 : c0) * 16;
 
         float ref = -INFINITY, l = 0.0f;    // of query head gl, over this lane group's entries
 
         int in_slot = 0, out_slot = 0;
         const auto load = [&](int it) {
             if (it < its) {
-                const uint32_t st = ring_s + in_slot * (2 * T::HALF);
+                const uint32_t st = dst0 + in_slot * (2 * T::HALF), vb = v_begin + uint32_t(it) * T::TK + r0;
                 in_slot = in_slot + 1 == T::S ? 0 : in_slot + 1;
-                constexpr int CPR = T::PITCH / 16;
 #pragma unroll
-                for (int i = 0; i < T::HALF / 512; ++i) {
-                    const int c = i * 32 + lane, r = c / CPR, col = c % CPR;
-                    const int64_t v = v_begin + int64_t(it) * T::TK + r;
+                for (int r = 0; r < T::KT; r += RPI) {
+                    const uint32_t v = vb + r, i = v + (v < vis.ns ? 0 : vis.gap);
                     const bool in = v < v_end;
-                    const int64_t at = (in ? v + (v < vis.ns ? 0 : vis.gap) : 0) * pitch + col * 16;
-                    const uint32_t dst = st + r * T::PITCH + ((LPK == 4 ? col ^ (r & 1) * 4 : col) * 16);
-                    if (col * T::CD < D) {
-                        cp16(dst, kp + at, in);
-                        cp16(dst + T::HALF, vp + at, in);
+                    const uint64_t at = in ? uint64_t(i) * pitch : 0;
+#pragma unroll
+                    for (int c = 0; c < CPR; c += 32) {
+                        static_assert(LPK != 4 || RPI % 2 == 0, "a lane's rows swap their halves alike");
+                        if ((c0 + c) * T::CD < D) {
+                            cp16(st + r * T::PITCH + c * 16, kp + at + c * 16, in);
+                            cp16(st + T::HALF + r * T::PITCH + c * 16, vp + at + c * 16, in);
+                        }
                     }
                 }
             }
@@ -310,7 +328,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
             load(it + T::S - 1);
             const uint32_t st = ring_s + out_slot * (2 * T::HALF);
             out_slot = out_slot + 1 == T::S ? 0 : out_slot + 1;
-            const int64_t vb = v_begin + int64_t(it) * T::TK;
+            const uint32_t vb = v_begin + uint32_t(it) * T::TK;
             // partial scores over this lane's values, x[g * U + u]
             float x[T::NV];
 #pragma unroll
@@ -349,7 +367,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
             bool moves = false;
 #pragma unroll
             for (int r = 0; r < T::R; ++r) {
-                const int64_t v = vb + (u0 + r) * T::KPS + grp;
+                const uint32_t v = vb + (u0 + r) * T::KPS + grp;
                 if (p.scores && v < v_end && gl < ng && sl % T::DUP == 0)
                     p.scores[(int64_t(m) * a.heads + g0 + gl) * p.cap + v] = x[r];
                 x[r] = v < v_end ? x[r] : -INFINITY;
@@ -448,33 +466,38 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         __syncthreads();
 
         // the CTA's state of the segment, and the whole unit's where it is all here
+        const auto put = [&](int g, int d, float4 v, float sum, bool any) {
+            float* out = a.out + m * a.ldo + int64_t(g0 + g) * D + d;      // (ldo may be odd)
+            out[0] = any ? v.x / sum : 0.0f;
+            out[1] = any ? v.y / sum : 0.0f;
+            out[2] = any ? v.z / sum : 0.0f;
+            out[3] = any ? v.w / sum : 0.0f;
+        };
         const bool whole = t0 == unit0 && t1 == unit0 + tiles;
         const uint32_t c_first = owner(unit0), c_last = owner(unit0 + tiles - 1);
-        const size_t slot = size_t(NG) * (D + 2);
+        const size_t slot = attn_slot(NG, D);
         float* part = p.part + (2 * cta + (t_begin >= unit0 ? 0 : 1)) * slot;
-        const int D2 = D / 2;
-        for (int e = tid; e < ng * D2; e += kAttnThreads) {
-            const int g = e / D2, d = (e - g * D2) * 2;
+        const int D4 = D / 4;
+        for (int e = tid; e < ng * D4; e += kAttnThreads) {
+            const int g = e / D4, d = (e - g * D4) * 4;
             float top = s_m[0][g];
 #pragma unroll
             for (int w = 1; w < kAttnWarps; ++w) top = fmaxf(top, s_m[w][g]);
-            float sum = 0.0f, v0 = 0.0f, v1 = 0.0f;
+            float sum = 0.0f;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
                 const float f = s_m[w][g] == -INFINITY ? 1.0f : ex2(s_m[w][g] - top);   // l and o: 0 or NaN
-                const float2 o2 = *reinterpret_cast<const float2*>(ring_all + w * kAttnRing + (g * T::DMAX + d) * 4);
+                const float4 o4 = *reinterpret_cast<const float4*>(ring_all + w * kAttnRing + (g * T::DMAX + d) * 4);
                 sum += s_l[w][g] * f;
-                v0 += o2.x * f;
-                v1 += o2.y * f;
+                v.x += o4.x * f, v.y += o4.y * f, v.z += o4.z * f, v.w += o4.w * f;
             }
             if (whole) {
-                float* out = a.out + m * a.ldo + int64_t(g0 + g) * D + d;
-                out[0] = vis.nvis ? v0 / sum : 0.0f;
-                out[1] = vis.nvis ? v1 / sum : 0.0f;
+                put(g, d, v, sum, vis.nvis != 0);
                 if (d == 0 && p.ml) p.ml[int64_t(m) * a.heads + g0 + g] = make_float2(top, 1.0f / sum);
             } else {
-                *reinterpret_cast<float2*>(part + g * (D + 2) + d) = make_float2(v0, v1);
-                if (d == 0) *reinterpret_cast<float2*>(part + g * (D + 2) + D) = make_float2(top, sum);
+                *reinterpret_cast<float4*>(part + g * D + d) = v;
+                if (d == 0) *reinterpret_cast<float2*>(part + NG * D + 2 * g) = make_float2(top, sum);
             }
         }
         if (!whole) {
@@ -494,9 +517,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                 const float* p0 = p.part + (2 * c_first + (first(c_first) < unit0 ? 1 : 0)) * slot;
                 const float* p1 = p.part + 2 * (c_first + 1) * slot;
                 const int n = int(c_last - c_first) + 1;
+                const auto from = [&](int i) { return i ? p1 + (i - 1) * 2 * slot : p0; };
                 const auto state = [&](int i, int g) {      // reference and sum of part i
-                    const float* x = (i ? p1 + (i - 1) * 2 * slot : p0) + g * (D + 2) + D;
-                    return __ldcg(reinterpret_cast<const float2*>(x));
+                    return __ldcg(reinterpret_cast<const float2*>(from(i) + NG * D + 2 * g));
                 };
                 float* s_f = reinterpret_cast<float*>(ring_all);   // (the states there have been read)
                 // one warp a query head: factors 2^(r_i - r), the sum and 1 / sum
@@ -520,20 +543,23 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                     }
                 }
                 __syncthreads();
-                for (int e = tid; e < ng * D2; e += kAttnThreads) {
-                    const int g = e / D2, d = (e - g * D2) * 2;
-                    const float2 x0 = __ldcg(reinterpret_cast<const float2*>(p0 + g * (D + 2) + d));
-                    float v0 = x0.x * s_f[g], v1 = x0.y * s_f[g];
-                    const float* src = p1 + g * (D + 2) + d;
-#pragma unroll 8
-                    for (int i = 1; i < n; ++i, src += 2 * slot) {
-                        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-                        v0 += x.x * s_f[i * NG + g];
-                        v1 += x.y * s_f[i * NG + g];
+                for (int e = tid; e < ng * D4; e += kAttnThreads) {
+                    const int g = e / D4, d = (e - g * D4) * 4;
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    constexpr int AHEAD = 8;                       // parts in flight
+                    for (int i0 = 0; i0 < n; i0 += AHEAD) {
+                        float4 x[AHEAD];
+#pragma unroll
+                        for (int i = 0; i < AHEAD; ++i)
+                            if (i0 + i < n) x[i] = __ldcg(reinterpret_cast<const float4*>(from(i0 + i) + g * D + d));
+#pragma unroll
+                        for (int i = 0; i < AHEAD; ++i)
+                            if (i0 + i < n) {
+                                const float f = s_f[(i0 + i) * NG + g];
+                                v.x += x[i].x * f, v.y += x[i].y * f, v.z += x[i].z * f, v.w += x[i].w * f;
+                            }
                     }
-                    float* out = a.out + m * a.ldo + int64_t(g0 + g) * D + d;
-                    out[0] = v0 / s_l[0][g];
-                    out[1] = v1 / s_l[0][g];
+                    put(g, d, v, s_l[0][g], true);
                 }
             }
         }
