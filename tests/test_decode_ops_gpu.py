@@ -447,6 +447,42 @@ def test_sample_batches(rows):
                p=list(np.where(i % 3 == 0, 1.0, 0.5 + (i % 50) * 0.01)), mp=list((i % 6) * 0.02))
 
 
+@pytest.mark.parametrize("n", [9001, 128256])
+def test_sample_long_cuts(n):
+    """Top-k past what one list holds, nuclei of nearly everything, and both."""
+    x = logits(4, n, spread=1.5, seed=n % 13)
+    u = [0.03, 0.4, 0.77, 0.98]
+    check_draw(x, u, k=[2047, 2048, 2049, 5000])
+    check_draw(x, u, p=[0.999, 0.9999, 0.99999, 1.0 - 2.0 ** -24])
+    check_draw(x, u, k=[8000, 2500, 4000, 600], p=[0.9, 0.99, 0.5, 0.999], t=[1.0, 3.0, 0.4, 1.0])
+    check_draw(x, u, k=[7000, 0, 3000, 0], mp=[0.01, 0.001, 1e-6, 1e-3], t=[1.0, 2.0, 5.0, 0.2])
+
+
+def test_sample_few_levels():
+    """Logits of few values (as 8-bit mantissas give): cuts fall among many ties."""
+    x = (logits(6, 40000, spread=2.0, seed=2) * 4).round() / 4
+    u = [0.1, 0.3, 0.5, 0.7, 0.9, 0.99]
+    check_draw(x, u, k=[50, 1000, 5000, 20000, 1, 39999])
+    check_draw(x, u, p=[0.1, 0.3, 0.5, 0.7, 0.9, 0.99])
+    check_draw(x, u, k=[500, 3000, 0, 100, 30000, 10], p=[0.9, 0.5, 0.95, 0.99, 0.8, 0.3], mp=[0.0, 0.01, 0.1, 0.05, 0.0, 0.2])
+
+
+def test_sample_rows_masked_by_the_lowest_float():
+    """Masks of -3.4e38 beside ordinary logits, and a row of nothing else."""
+    t = torch()
+    low = t.finfo(t.float32).min
+    x = logits(5, 5000, seed=6)
+    x[0, 10:] = low
+    x[1, ::2] = low
+    x[2, 1:] = low
+    x[3] = low
+    x[4, 100:4000] = -math.inf
+    u = [0.5, 0.9, 0.3, 0.6, 0.999]
+    for kw in (dict(), dict(k=[5, 100, 3, 7, 900]), dict(p=[0.9, 0.8, 0.5, 0.25, 0.95]), dict(mp=[0.1] * 5),
+               dict(k=[2400] * 5, p=[0.7] * 5)):
+        check_draw(x, u, **kw)
+
+
 def test_sample_every_token_can_be_drawn():
     """Weights 1 : 2 : 4 (exact in logits of log 2 only to rounding): each number falls in its own share."""
     t = torch()
@@ -572,6 +608,93 @@ def test_calls_on_another_stream_and_in_a_graph():
     graph.replay()
     t.cuda.synchronize()
     assert np.all(np.abs(a.out.cpu().double().numpy() - want[0]) <= want[1])
+    no_error()
+
+
+@pytest.mark.parametrize("mode", ["f32", "i8", "i8x2"])
+def test_decode_steps_together(mode):
+    """Some decode steps as a program runs them, captured into one graph: the fused QKV projection
+    writes the caches, attention reads them and accumulates, a full cache is evicted, the head's
+    logits are sampled.  Each operator is held to its 64-bit form on what the step gave it."""
+    from q8_quantized_projection_gb300 import synth
+    t = torch()
+    rows, heads, kv_heads, dim, n_pos, budget, vocab, hidden = 3, 8, 2, 64, 24, 16, 1500, 1024
+    sinks, recent, window = 2, 6, 14
+    kv_dim, width = kv_heads * dim, (heads + 2 * kv_heads) * dim
+    rng = synth.rng_for(3)
+    put = lambda w: (t.from_numpy(w[0]).cuda(), t.from_numpy(w[1].view(np.int16)).cuda())  # noqa: E731
+    wqkv, whead = put(synth.q8_weights(rng, width, hidden)), put(synth.q8_weights(rng, vocab, hidden))
+    g = t.Generator(device="cuda").manual_seed(1)
+    h = t.empty(rows, hidden, device="cuda")
+    y, out = t.empty(rows, width, device="cuda"), t.empty(rows, heads * dim, device="cuda")
+    logit, u = t.empty(rows, vocab, device="cuda"), t.empty(rows, device="cuda")
+    k = t.full((rows, n_pos, kv_dim), math.nan, device="cuda")       # nothing may read what was never written
+    v = t.full((rows, n_pos, kv_dim), math.nan, device="cuda")
+    acc = t.zeros(rows, kv_heads, n_pos, device="cuda")
+    pos = t.tensor([-1, 5, 14], dtype=t.int32, device="cuda")
+    for m in range(rows):
+        n = int(pos[m]) + 1
+        k[m, :n], v[m, :n] = (t.randn(n, kv_dim, device="cuda", generator=g) for _ in range(2))
+    tok = t.zeros(rows, dtype=t.int32, device="cuda")
+    kept = t.zeros(rows, dtype=t.int32, device="cuda")
+    ws = t.empty(native.q8_proj_fused_workspace(mode, rows, hidden), dtype=t.uint8, device="cuda")
+    xq, xd = native.activation_buffers(mode, rows, hidden)
+    aws = native.attn_workspace(rows, heads, kv_heads, dim, n_pos, window, sinks, True)
+    top_p, temp = t.full((rows,), 0.9, device="cuda"), t.full((rows,), 0.8, device="cuda")
+
+    def step():
+        pos.add_(1)
+        native.q8_proj_fused_kv(mode, *wqkv, h, y, ws, pos, heads * dim, k, v)
+        native.attn_decode(y, k, v, pos, out, aws, heads, kv_heads, window=window, sinks=sinks, acc=acc)
+        native.act_quant(mode, h, xq, xd, norm=True)
+        native.q8_proj(mode, *whead, xq, xd, rows, logit)
+        native.head_sample(logit, u, tok, temperature=temp, top_p=top_p, kept=kept)
+
+    def shorten():
+        ews = t.empty(native.kv_evict_workspace(rows, kv_heads, budget), dtype=t.uint8, device="cuda")
+        native.kv_evict(k, v, pos, acc, pos, acc, ews, kv_heads, budget, sinks=sinks, recent=recent)
+
+    f = lambda a: a.cpu().double().numpy()  # noqa: E731
+    graph = None
+    for i in range(20):
+        h.normal_(generator=g)
+        u.uniform_(generator=g)
+        before = [pos.clone(), acc.clone(), k.clone(), v.clone()]
+        if i == 1:
+            graph = t.cuda.CUDAGraph()
+            state = [b.clone() for b in before]
+            with t.cuda.graph(graph):
+                step()
+            for dst, src in zip((pos, acc, k, v), state):
+                dst.copy_(src)
+        if graph is None:
+            step()
+        else:
+            graph.replay()
+        t.cuda.synchronize()
+        at = pos.tolist()
+        assert at == [p + 1 for p in before[0].tolist()]
+        for m in range(rows):       # only the new entry of each cache changed
+            now, old = k[m].clone(), before[2][m].clone()
+            assert t.equal(now[at[m]], y[m, heads * dim:heads * dim + kv_dim])
+            now[at[m]], old[at[m]] = 0, 0
+            assert t.equal(now.nan_to_num(7.0), old.nan_to_num(7.0))
+        kd, vd = f(k), f(v)
+        for m in range(rows):
+            kd[m, at[m] + 1:], vd[m, at[m] + 1:] = 0, 0
+        want, tol, want_acc, acc_tol = ref.attn(f(y[:, :heads * dim]), kd, vd, at, heads, kv_heads, window, sinks,
+                                                dim ** -0.5, f(before[1]))
+        assert np.all(np.abs(f(out) - want) <= tol)
+        assert np.all(np.abs(f(acc) - want_acc) <= acc_tol)
+        for m in range(rows):
+            assert (int(tok[m]), int(kept[m])) == ref.sample(f(logit[m]), float(u[m]), float(np.float32(0.8)), 0,
+                                                              float(np.float32(0.9)))[::2]
+        if max(at) == n_pos - 1:
+            bits = lambda x: x.view(t.int32).cpu().numpy()  # noqa: E731
+            want = ref.evict(bits(k), bits(v), at, acc.cpu().numpy(), kv_heads, budget, sinks, recent, n_pos)
+            shorten()
+            assert np.array_equal(bits(k), want[0]) and np.array_equal(bits(v), want[1])
+            assert pos.tolist() == want[2].tolist() and np.array_equal(acc.cpu().numpy(), want[3])
     no_error()
 
 
