@@ -31,7 +31,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32, kThreads = 512;
 constexpr int kDigit = 256, kMaxCluster = 8;
 constexpr int kHeld = 8;                      // keys a lane holds at a time
 constexpr int kBatch = 4;                     // pieces a thread has in a batch of moves
@@ -52,9 +52,9 @@ __device__ __forceinline__ int32_t* kept_list(const EvictArgs& a, int64_t unit) 
     return first_moved(a) + (a.rows * a.kv_heads + 63) / 64 * 64 + unit * a.budget;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a, int* err) {
-    __shared__ uint32_t s_hist[2][kDigit], s_scan[kWarps], s_digit, s_above;
-    __shared__ uint2 s_warp[kWarps];                 // sure ones and ties by warp
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int* err) {
+    __shared__ uint32_t s_hist[2][kDigit], s_scan[kSelWarps], s_digit, s_above;
+    __shared__ uint2 s_warp[kSelWarps];                 // sure ones and ties by warp
     __shared__ uint2 s_cta[kMaxCluster];             // and by CTA
     cg::cluster_group cl = cg::this_cluster();
     const unsigned rank = cl.block_rank(), size = cl.num_blocks();
@@ -74,14 +74,14 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     if (n <= budget) {                                   // the whole cluster alike
         if (writes) first_moved(a)[unit] = -1;
         if (kept)
-            for (uint32_t i = rank * kThreads + tid; i < budget; i += size * kThreads) kept[i] = i < n ? int32_t(i) : -1;
+            for (uint32_t i = rank * kSelThreads + tid; i < budget; i += size * kSelThreads) kept[i] = i < n ? int32_t(i) : -1;
         return;
     }
     const uint32_t lo = uint32_t(a.sinks), hi = n - uint32_t(a.recent);
     const uint32_t need = budget - lo - uint32_t(a.recent);
     // this warp's range of all entries, in whole steps of 32
-    const uint32_t span = (n + size * kWarps * 32 - 1) / (size * kWarps * 32) * 32;
-    const uint32_t w0 = min((rank * kWarps + warp) * span, n), w1 = min(w0 + span, n);
+    const uint32_t span = (n + size * kSelWarps * 32 - 1) / (size * kSelWarps * 32) * 32;
+    const uint32_t w0 = min((rank * kSelWarps + warp) * span, n), w1 = min(w0 + span, n);
     const bool held = span <= 32 * kHeld;
     uint32_t key[kHeld];                                 // of entries [at, at + 256), lanes in turn
     const auto fetch = [&](uint32_t at) {
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
             }
             zeros = __reduce_add_sync(0xffffffffu, zeros);
             if (lane == 0 && zeros) atomicAdd(&hist[(zero >> shift) & 255u], zeros);
-            cl.sync();
+            cluster_sync(size);
             // (the other bins were last read before this barrier's other side)
             if (tid < kDigit) s_hist[~(shift >> 3) & 1][tid] = 0;
             // from the largest digit down: where the cluster's count reaches what is left
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
             if (lane == 31) s_scan[warp] = up;
             __syncthreads();
             uint32_t before = up - c;
-            for (int k = 0; k < warp; ++k) before += s_scan[k];
+            for (int k = 0; k < min(warp, kDigit / 32); ++k) before += s_scan[k];
             if (tid < kDigit && before < left && before + c >= left) {
                 s_digit = digit;
                 s_above = before;
@@ -167,19 +167,28 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
         }
     }
     if (lane == 0) s_warp[warp] = cnt;
-    if (need == 0) cl.sync();                            // (every CTA runs, else the passes' barriers say so)
+    if (need == 0) cluster_sync(size);                            // (every CTA runs, else the passes' barriers say so)
     __syncthreads();
-    uint2 off = make_uint2(0, 0), all = off;
-    for (int k = 0; k < kWarps; ++k) {
-        const uint2 c = s_warp[k];
-        if (k < warp) off.x += c.x, off.y += c.y;
-        all.x += c.x, all.y += c.y;
+    // kept ones before this warp: of the CTA's warps, then of the CTAs before
+    static_assert(kSelWarps == 32, "one lane a warp");
+    const uint2 of = s_warp[lane];
+    uint2 up = of;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, up.x, d), y = __shfl_up_sync(0xffffffffu, up.y, d);
+        if (lane >= d) up.x += x, up.y += y;
     }
-    if (tid < int(size)) *cl.map_shared_rank(&s_cta[rank], tid) = all;
-    cl.sync();
-    for (unsigned r = 0; r < rank; ++r) {
-        off.x += s_cta[r].x;
-        off.y += s_cta[r].y;
+    uint2 off = make_uint2(__shfl_sync(0xffffffffu, up.x - of.x, warp), __shfl_sync(0xffffffffu, up.y - of.y, warp));
+    if (size > 1) {
+        if (warp == 0) {
+            const uint2 all = make_uint2(__shfl_sync(0xffffffffu, up.x, 31), __shfl_sync(0xffffffffu, up.y, 31));
+            if (lane < int(size)) *cl.map_shared_rank(&s_cta[rank], lane) = all;
+        }
+        cluster_sync(size);
+        for (unsigned r = 0; r < rank; ++r) {
+            off.x += s_cta[r].x;
+            off.y += s_cta[r].y;
+        }
     }
     // list them; the first that does not stay lies in the warp before whose
     // range every entry stays
@@ -291,7 +300,7 @@ cudaError_t launch_evict(const EvictArgs& a, const LaunchCtx& ctx) {
     // CTAs a row and head: so many that lanes hold their keys, where 8 reach that
     // (4096 entries on one CTA: 9 us, on four: 12)
     int size = 1;
-    while (size < kMaxCluster && a.n_pos > int64_t(size) * kThreads * kHeld) size *= 2;
+    while (size < kMaxCluster && a.n_pos > int64_t(size) * kSelThreads * kHeld) size *= 2;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attrs[2];
     cfg.stream = ctx.stream;
@@ -303,7 +312,7 @@ cudaError_t launch_evict(const EvictArgs& a, const LaunchCtx& ctx) {
     ++cfg.numAttrs;
     cfg.attrs = attrs;
     cfg.gridDim = dim3(unsigned(units * size));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kSelThreads);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ctx.dev_err);
     if (e != cudaSuccess) return e;
     // the widest slice that leaves a CTA an SM, 64 bytes at least
@@ -315,6 +324,7 @@ cudaError_t launch_evict(const EvictArgs& a, const LaunchCtx& ctx) {
     const int slices = slices_at(lanes_log);
     cfg.numAttrs = pdl_attrs(ctx, attrs);
     cfg.gridDim = dim3(unsigned(units + units * 2 * slices));
+    cfg.blockDim = dim3(kThreads);
     return cudaLaunchKernelEx(&cfg, evict_move_kernel, a, elt, lanes_log, slices);
 }
 

@@ -245,7 +245,7 @@ __device__ __forceinline__ Slot exchange(Slot v, int& phase, u64* before = nullp
         warp_reduce<F>(v);
         if (lane < int(size)) *cl.map_shared_rank(&slots[rank], lane) = v;
     }
-    cl.sync();
+    cluster_sync(size);
     v = Slot();
     if (lane < int(size)) v = slots[lane];
     if (before) *before = warp_sum(lane < int(rank) ? v.a : 0);
@@ -403,7 +403,7 @@ struct Row {
                 break;
             }
         }
-        cg::this_cluster().sync();
+        cluster_sync(size);
         return s.found;
     }
 
@@ -473,7 +473,7 @@ __device__ __forceinline__ bool cut_by_bins(Row<RES>& row, const Weights& w, flo
     });
     rest = __reduce_add_sync(0xffffffffu, rest);
     if ((tid & 31) == 0 && rest) atomicAdd(&s.hist[kBins - 1], rest);
-    cl.sync();
+    cluster_sync(row.size);
     // every CTA sums the cluster's bins and finds the one that holds the cut
     static_assert(kBins == 2 * kThreads, "two bins a thread");
     u64 b0 = 0, b1 = 0, all_bins;
@@ -516,11 +516,24 @@ __device__ __forceinline__ bool cut_by_bins(Row<RES>& row, const Weights& w, flo
         });
         const Slot all = exchange<kA | kB | kG | kE2>(v, row.phase);
         const u64 need = need_of(all.a);
-        if (all.b >= need || all.b + all.g < need) {      // the histogram's rounding named a neighbour
-            B += all.b >= need ? -1 : 1;
+        const bool deep = all.b >= need;
+        if (deep || all.b + all.g < need) {      // the histogram's rounding named a neighbour
             __syncthreads();
-            if (tid == 0) s.listed = 0;
+            if (tid == 0) {
+                s.listed = 0;
+                s.found = deep ? 0 : kBins - 1;
+            }
             __syncthreads();
+            // the nearest bin on the side of the cut that holds anything
+            const uint32_t at[2] = {2u * tid, 2u * tid + 1};
+            const u64 holds[2] = {b0, b1};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (holds[j] && deep && int(at[j]) < B) atomicMax(&s.found, at[j]);
+                if (holds[j] && !deep && int(at[j]) > B) atomicMin(&s.found, at[j]);
+            }
+            __syncthreads();
+            B = int(s.found);
             continue;
         }
         if (all.e2 > kList) return false;
@@ -544,7 +557,7 @@ __device__ __forceinline__ bool cut_by_bins(Row<RES>& row, const Weights& w, flo
                 run += fx;
             }
         }
-        cl.sync();
+        cluster_sync(row.size);
         *cut = {s.cut_x, s.cut_i};
         *above = v.b;
         *above_n = v.e;
@@ -729,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
         reach = __reduce_max_sync(0xffffffffu, key);
     }
     v.c2 = ~reach;
-    cl.sync();      // every CTA has begun before another writes to it
+    cluster_sync(size);      // every CTA has begun before another writes to it
     const Slot all = exchange<kE | kC | kC2 | kD>(v, row.phase);
     const uint32_t top = all.c, low = all.d + 1;
     reach = ~all.c2;
@@ -799,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
                 draw_from_list(w, set, int(listed), k_scale, &tok, &S, &kept);
                 if (writes) finish(tok, S, kept);
             }
-            cl.sync();      // (the first CTA has read the others' parts of the list)
+            cluster_sync(size);      // (the first CTA has read the others' parts of the list)
             return;
         }
     }
@@ -886,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
         tok = row.pick(e, before, kept_w);
     }
     if (writes) finish(tok, fin.a, fin.e);
-    cl.sync();      // nobody leaves while another may still write here
+    cluster_sync(size);      // nobody leaves while another may still write here
 }
 
 template <bool RES>

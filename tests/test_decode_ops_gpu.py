@@ -467,6 +467,23 @@ def test_sample_few_levels():
     check_draw(x, u, k=[500, 3000, 0, 100, 30000, 10], p=[0.9, 0.5, 0.95, 0.99, 0.8, 0.3], mp=[0.0, 0.01, 0.1, 0.05, 0.0, 0.2])
 
 
+def test_sample_shares_next_to_a_border():
+    """Nuclei that end a few steps of binary32 beside a token's border, tokens far apart."""
+    t = torch()
+    x = t.full((24, 3000), -9.0, device="cuda")
+    at = [(i * 251 + 7) % 3000 for i in range(24)]
+    x[:, at] = t.arange(24, device="cuda") * -0.21 + 1.3
+    w = np.exp(np.sort(x[0].cpu().double().numpy())[::-1] - 1.3)
+    cum = w.cumsum() / w.sum()
+    p = []
+    for i in range(24):                     # 2 to 5 steps above or below the border of token i // 2
+        v = np.float32(cum[i // 2])
+        for _ in range(2 + i % 4):
+            v = np.nextafter(v, np.float32(2 if i % 2 else 0), dtype=np.float32)
+        p.append(float(v))
+    check_draw(x, [0.5 + 0.02 * i for i in range(24)], p=p)
+
+
 def test_sample_rows_masked_by_the_lowest_float():
     """Masks of -3.4e38 beside ordinary logits, and a row of nothing else."""
     t = torch()
