@@ -26,8 +26,15 @@
 //
 // What bounds it.  One row: latency, of exchanges and of code that runs once
 // (no arithmetic of 64-bit floats: at 2 lanes a clock and SM, one division in
-// every thread cost 5 us).  A batch: the exact weights, about 45 instructions
-// each against 4 bytes read, and the histogram's atomics.
+// every thread cost 5 us).  A batch: instructions, 45 for an exact weight and
+// about 200 a token in all against 4 bytes read, at 0.45 issued a clock and
+// scheduler; barriers are most of the rest.
+//
+// Measured (device time): 3 rows of 1001 tokens 11 us, one of 128256 with every
+// filter 18 us, 64 of 128256 with top-p 100 us, 256 of 32003 with settings of
+// their own 75 us.  CTAs of 512 threads and parts of 16 K tokens, two CTAs an
+// SM: 256 threads and 8 K (clusters of 16) 137 us, 1024 and 32 K 103 us on the
+// 64 rows, 86 and 93 on the 256.
 #include <cooperative_groups.h>
 #include <float.h>
 #include <math.h>
