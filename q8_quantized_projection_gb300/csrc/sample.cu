@@ -718,8 +718,23 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
                 *reinterpret_cast<float4*>(x + e) = make_float4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
             }
         } else {
+            // a row that begins off a 16-byte boundary: whole words, stored a float at
+            // a time (behind the first row only, so the word before it is the row before's)
+            const int off = int(reinterpret_cast<uintptr_t>(gx) >> 2 & 3);
 #pragma unroll 8
-            for (int e = tid; e < part; e += kThreads) x[e] = e < int(n) ? clean(__ldg(gx + e)) : -INFINITY;
+            for (int e = tid * 4 - off; e < part; e += kThreads * 4) {
+                float f[4];
+                if (e + 3 < int(n)) {
+                    const float4 v = __ldg(reinterpret_cast<const float4*>(gx + e));
+                    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) f[j] = e + j < int(n) && e + j >= 0 ? __ldg(gx + e + j) : -INFINITY;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (e + j >= 0 && e + j < part) x[e + j] = clean(f[j]);
+            }
         }
         __syncthreads();
     }
