@@ -316,7 +316,9 @@ size_t head_argmax_noalloc_scratch_bytes(void);
  * A row with nothing visible (pos[m] = -1, or window = 0 and sinks = 0) gives
  * zeros and leaves acc as it was; a position outside [-1, n_pos) does the
  * same and sets device error 2.  What an entry that is not visible holds
- * (NaN, infinity) does not matter.  Scores, weights and sums are binary32;
+ * (NaN, infinity) does not matter.  Scores, weights and sums are binary32
+ * (the sums before they are divided, of up to 2^8 a visible entry: cache values
+ * below 2^88 cannot overflow them);
  * the result does not depend on what else runs (no atomics on values).
  * 1 <= rows <= Q8_MAX_ROWS; heads a multiple of kv_heads, heads <= 1024;
  * head_dim a multiple of 8, 8 <= head_dim <= 256; 1 <= n_pos <= 2^31 - 1, each

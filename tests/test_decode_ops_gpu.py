@@ -97,6 +97,11 @@ def test_attn_window_and_sinks(window, sinks):
     Attn("f32", [199, 99, 64, 0, 3], 4, 2, 32, 200, window=window, sinks=sinks, seed=window % 97 + sinks % 89).check()
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim", [(1024, 4, 16), (128, 1, 64), (1024, 1024, 8), (71, 71, 128)])
+def test_attn_many_heads(heads, kv_heads, dim):
+    Attn("bf16", [90, 12], heads, kv_heads, dim, 91, window=60, sinks=1, seed=heads).check()
+
+
 @pytest.mark.parametrize("rows", [1, 3, 40, 256])
 def test_attn_ragged_batches(rows):
     pos = [(37 * i * i + 11) % 400 - 1 for i in range(rows)]
@@ -323,6 +328,14 @@ def test_evict_types_and_dims(kv, dim, in_place):
 def test_evict_sizes(n, budget, sinks, recent):
     Evict("bf16", [n - 1], 2, 32, n + 3, budget, sinks, recent, seed=n).check()
     Evict("f32", [n - 1], 1, 16, n, budget, sinks, recent, seed=n + 1).check(in_place=True)
+
+
+@pytest.mark.parametrize("n,budget,sinks,recent", [
+    (8193, 4000, 4, 100), (9000, 100, 60, 40), (20000, 19999, 0, 0), (40001, 33, 3, 30), (66000, 30000, 4, 2000),
+    (70001, 69000, 100, 1), (131073, 1, 0, 0)])
+def test_evict_long_rows(n, budget, sinks, recent):
+    """Selections on several CTAs, and past what their lanes hold."""
+    Evict("bf16", [n - 1, n // 2], 1, 8, n, budget, sinks, recent, seed=n).check()
 
 
 def test_evict_rows_at_most_the_budget_stay():
@@ -712,6 +725,47 @@ def test_decode_steps_together(mode):
             shorten()
             assert np.array_equal(bits(k), want[0]) and np.array_equal(bits(v), want[1])
             assert pos.tolist() == want[2].tolist() and np.array_equal(acc.cpu().numpy(), want[3])
+    no_error()
+
+
+def test_calls_at_once_on_two_streams():
+    """Calls that overlap, each with its own buffers and workspace, give what they give alone."""
+    t = torch()
+    a = [Attn("bf16", [2500, 900, 4000], 8, 2, 128, 4001, seed=i) for i in range(2)]
+    e = [Evict("f32", [1999, 700], 4, 64, 2000, 900, sinks=1, recent=50, seed=i) for i in range(2)]
+    x = [logits(20, 5000, seed=i) for i in range(2)]
+    u = t.rand(20, device="cuda", generator=t.Generator(device="cuda").manual_seed(3))
+    tok = [t.zeros(20, dtype=t.int32, device="cuda") for _ in range(2)]
+    top_p = t.full((20,), 0.8, device="cuda")
+    start = [[v.clone() for v in (a[i].acc, e[i].k, e[i].v)] for i in range(2)]
+    new = [(t.zeros_like(e[i].posd), t.zeros_like(e[i].acc)) for i in range(2)]
+
+    def reset():
+        for i in range(2):
+            for dst, src in zip((a[i].acc, e[i].k, e[i].v), start[i]):
+                dst.copy_(src)
+
+    def call(i, stream=None):
+        a[i].call(stream)
+        e[i].call(*new[i], e[i].kept, stream)
+        native.head_sample(x[i], u, tok[i], top_p=top_p, stream=stream)
+
+    def results(i):
+        return [v.clone() for v in (a[i].out, a[i].acc, e[i].k, e[i].v, *new[i], e[i].kept, tok[i])]
+
+    want = []
+    for i in range(2):
+        call(i)
+        want.append(results(i))
+    streams = [t.cuda.Stream(), t.cuda.Stream()]
+    for _ in range(5):
+        reset()
+        t.cuda.synchronize()
+        for i in range(2):
+            call(i, streams[i])
+        t.cuda.synchronize()
+        for i in range(2):
+            assert all(t.equal(g, w) for g, w in zip(results(i), want[i]))
     no_error()
 
 
