@@ -18,7 +18,9 @@
 // all of it has been read, and the next one's reads go out before that.
 // Slices never touch, so CTAs need no order among them; the slice is as wide as
 // leaves a CTA an SM, 64 bytes at least (8 heads of 24576 of 32768 f32 entries
-// in 4 rows: 128 bytes 246 us; 64 bytes 40 us and 256 bytes 60 us more).
+// in 4 rows: 128 bytes 246 us; 64 bytes 40 us and 256 bytes 60 us more).  Where
+// that leaves few CTAs (few rows and heads) and long walks, a cluster of up to 8
+// walks a slice together, with a cluster barrier a batch.
 // Bound: HBM, each moved byte read and written once; measured there 6.6 TB/s
 // (read and write), and 9 us for 2048 of 4096 entries of one row.
 #include <cooperative_groups.h>
@@ -221,64 +223,74 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 }
 
 // Moves items [from, budget) of 16 bytes (caches) or 4 (acc), `pitch` bytes
-// apart, each thread those that are `mine` of every `rows`; src may be dst.
-template <typename V>
+// apart; src may be dst.  In a batch the cluster has size * kBatch * rows items,
+// this thread those that are `mine` of its CTA's rows.
+template <bool CLUSTER, typename V>
 __device__ __forceinline__ void move_items(const unsigned char* src, unsigned char* dst, int64_t pitch, const int32_t* idx,
-                                           int64_t from, int64_t budget, int rows, int mine, bool has) {
+                                           int64_t from, int64_t budget, int rows, int mine, bool has, unsigned rank,
+                                           unsigned size) {
     V next[kBatch], now[kBatch];
+    const int64_t every = int64_t(rows) * size, at0 = int64_t(rank) * rows + mine;
     const auto load = [&](int64_t j0) {
         int at[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int64_t j = j0 + b * rows + mine;
+            const int64_t j = j0 + b * every + at0;
             at[b] = has && j < budget ? idx[j] : -1;
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
             if (at[b] >= 0) next[b] = *reinterpret_cast<const V*>(src + int64_t(at[b]) * pitch);
     };
-    const int step = rows * kBatch;
+    const int64_t step = every * kBatch;
     load(from);
     for (int64_t j0 = from; j0 < budget; j0 += step) {
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) now[b] = next[b];
+        // a barrier: every read of this batch is done
+        if (CLUSTER) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
         if (j0 + step < budget) load(j0 + step);
-        __syncthreads();                 // every read of this batch is done
+        if (CLUSTER) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        else __syncthreads();
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int64_t j = j0 + b * rows + mine;
+            const int64_t j = j0 + b * every + at0;
             if (has && j < budget) *reinterpret_cast<V*>(dst + j * pitch) = now[b];
         }
     }
 }
 
-// CTA: acc of one row and K/V head (the first ones), or its K or V in one
+// Cluster: acc of one row and K/V head (the first ones), or its K or V in one
 // column slice of 16 << lanes_log bytes.
-__global__ void __launch_bounds__(kThreads) evict_move_kernel(const EvictArgs a, int elt, int lanes_log, int slices) {
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, 2)
+    evict_move_kernel(const EvictArgs a, int elt, int lanes_log, int slices) {
+    const unsigned rank = CLUSTER ? cg::this_cluster().block_rank() : 0;
+    const unsigned size = CLUSTER ? cg::this_cluster().num_blocks() : 1;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t units = a.rows * a.kv_heads;
+    const int64_t units = a.rows * a.kv_heads, cluster = blockIdx.x / size;
     const int tid = threadIdx.x;
-    if (blockIdx.x < units) {
-        const int64_t unit = blockIdx.x, m = unit / a.kv_heads;
+    if (cluster < units) {
+        const int64_t unit = cluster, m = unit / a.kv_heads;
         const int from = first_moved(a)[unit];
-        if (unit == m * a.kv_heads && tid == 0) {
+        if (unit == m * a.kv_heads && rank == 0 && tid == 0) {
             // (pos may be new_pos: nobody else reads it in this kernel)
             a.new_pos[m] = from < 0 ? a.pos[m] : int32_t(a.budget - 1);
         }
         const float* acc = a.acc + unit * a.n_pos;
         float* new_acc = a.new_acc + unit * a.n_pos;
-        int64_t kept_as_is = from < 0 ? a.n_pos : from;
+        const int64_t as_is = from < 0 ? a.n_pos : from, me = int64_t(rank) * kThreads + tid, all = int64_t(size) * kThreads;
         if (new_acc != acc)
-            for (int64_t i = tid; i < kept_as_is; i += kThreads) new_acc[i] = acc[i];
-        if (from < 0) return;
-        move_items<float>(reinterpret_cast<const unsigned char*>(acc), reinterpret_cast<unsigned char*>(new_acc), 4,
-                          kept_list(a, unit), from, a.budget, kThreads, tid, true);
-        __syncthreads();
-        for (int64_t i = a.budget + tid; i < a.n_pos; i += kThreads) new_acc[i] = 0.0f;
+            for (int64_t i = me; i < as_is; i += all) new_acc[i] = acc[i];
+        if (from < 0) return;                                // (the whole cluster alike)
+        move_items<CLUSTER, float>(reinterpret_cast<const unsigned char*>(acc), reinterpret_cast<unsigned char*>(new_acc), 4,
+                             kept_list(a, unit), from, a.budget, kThreads, tid, true, rank, size);
+        // (every read ended before the last batch's barrier)
+        for (int64_t i = a.budget + me; i < a.n_pos; i += all) new_acc[i] = 0.0f;
         return;
     }
-    const int64_t id = blockIdx.x - units;
+    const int64_t id = cluster - units;
     const int slice = int(id % slices), kv = int(id / slices % 2);
     const int64_t unit = id / slices / 2, m = unit / a.kv_heads, h = unit % a.kv_heads;
     const int from = first_moved(a)[unit];
@@ -286,8 +298,27 @@ __global__ void __launch_bounds__(kThreads) evict_move_kernel(const EvictArgs a,
     const int64_t row_bytes = a.dim * elt, pitch = a.kv_heads * row_bytes;
     const int64_t col = int64_t((slice << lanes_log) + (tid & ((1 << lanes_log) - 1))) * 16;
     unsigned char* base = static_cast<unsigned char*>(kv ? a.v : a.k) + m * a.n_pos * pitch + h * row_bytes + col;
-    move_items<int4>(base, base, pitch, kept_list(a, unit), from, a.budget, kThreads >> lanes_log, tid >> lanes_log,
-                     col < row_bytes);
+    move_items<CLUSTER, int4>(base, base, pitch, kept_list(a, unit), from, a.budget, kThreads >> lanes_log, tid >> lanes_log,
+                        col < row_bytes, rank, size);
+}
+
+template <bool CLUSTER>
+cudaError_t launch_move(const EvictArgs& a, int size, int elt, int lanes_log, int slices, const LaunchCtx& ctx) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attrs[2];
+    cfg.gridDim = dim3(unsigned(a.rows * a.kv_heads * (1 + 2 * slices) * size));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = ctx.stream;
+    cfg.numAttrs = pdl_attrs(ctx, attrs);
+    if (CLUSTER) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attrs[cfg.numAttrs].val.clusterDim.x = unsigned(size);
+        attrs[cfg.numAttrs].val.clusterDim.y = 1;
+        attrs[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    cfg.attrs = attrs;
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel<CLUSTER>, a, elt, lanes_log, slices);
 }
 
 }  // namespace
@@ -324,10 +355,17 @@ cudaError_t launch_evict(const EvictArgs& a, const LaunchCtx& ctx) {
     while (lanes_log > 2 && ((1 << (lanes_log - 1)) >= chunks || units * 2 * slices_at(lanes_log) < ctx.num_sms))
         --lanes_log;
     const int slices = slices_at(lanes_log);
-    cfg.numAttrs = pdl_attrs(ctx, attrs);
-    cfg.gridDim = dim3(unsigned(units + units * 2 * slices));
-    cfg.blockDim = dim3(kThreads);
-    return cudaLaunchKernelEx(&cfg, evict_move_kernel, a, elt, lanes_log, slices);
+    // where even those leave an SM one CTA and a long walk, clusters walk
+    // together: up to 5 CTAs an SM in all, three batches each at least (1 x 8 heads
+    // of 64 f16 values, 41475 of 55887 entries: 123 us alone, 57 in eights; 16 x 8
+    // heads of 128, two CTAs an SM: 76 alone, 96 in pairs)
+    const int64_t ctas = units * 2 * slices, batch = int64_t(kThreads >> lanes_log) * kBatch;
+    size = 1;
+    while (size < kMaxCluster && ctas <= ctx.num_sms + ctx.num_sms / 10 && ctas * size * 2 <= 5 * int64_t(ctx.num_sms) &&
+           a.budget >= 3 * batch * size * 2)
+        size *= 2;
+    if (size > 1) return launch_move<true>(a, size, elt, lanes_log, slices, ctx);
+    return launch_move<false>(a, size, elt, lanes_log, slices, ctx);
 }
 
 }  // namespace q8

@@ -333,9 +333,10 @@ def test_evict_sizes(n, budget, sinks, recent):
 @pytest.mark.parametrize("n,budget,sinks,recent", [
     (8193, 4000, 4, 100), (9000, 100, 60, 40), (20000, 19999, 0, 0), (40001, 33, 3, 30), (66000, 30000, 4, 2000),
     (70001, 69000, 100, 1), (131073, 1, 0, 0)])
-def test_evict_long_rows(n, budget, sinks, recent):
-    """Selections on several CTAs, and past what their lanes hold."""
-    Evict("bf16", [n - 1, n // 2], 1, 8, n, budget, sinks, recent, seed=n).check()
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_long_rows(n, budget, sinks, recent, in_place):
+    """Selections on several CTAs and past what their lanes hold, walks of clusters."""
+    Evict("bf16", [n - 1, n // 2], 1, 8, n, budget, sinks, recent, seed=n).check(in_place)
 
 
 def test_evict_rows_at_most_the_budget_stay():
