@@ -155,7 +155,7 @@ struct AttnShape {
     static constexpr int DMAX = DPL * LPK;
     static constexpr int PITCH = DMAX * ELT;                  // bytes an entry in a stage
     static constexpr int KPS = 32 / LPK;                      // entries a warp takes at a time
-    static constexpr int U = NG == 8 ? 2 : KV == Q8_KV_F32 ? 2 : 4;
+    static constexpr int U = KV == Q8_KV_F32 ? 2 : 4;
     static constexpr int KT = KPS * U;                        // entries a stage
     static constexpr int HALF = KT * PITCH;                   // bytes of K (and of V) a stage
     static constexpr int S0 = kAttnRing / (2 * HALF);
@@ -232,10 +232,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     }
     // CTA c has tiles [first(c), first(c + 1)): all of them in equal shares, the
     // first ones one longer.  Small problems: two tiles a CTA (fewer cost more to
-    // join than they save), or a unit.
+    // join than they save; of eight query heads, whose tiles are half as many bytes
+    // and twice the work, one), or a unit.
     const uint32_t real = s_pre[rows], units = uint32_t(rows) * per_row;
     const uint32_t extra = real >= 4 * gridDim.x ? T::EXTRA : 1, W = real + extra * units;
-    const uint32_t ctas = min(max(real / 2, units), gridDim.x), cta = blockIdx.x;
+    const uint32_t ctas = min(max(NG == 8 ? real : real / 2, units), gridDim.x), cta = blockIdx.x;
     __syncthreads();
     for (int i = tid; i <= rows; i += kAttnThreads) s_pre[i] += extra * i * per_row;
     __syncthreads();
