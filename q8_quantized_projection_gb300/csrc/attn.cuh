@@ -54,6 +54,12 @@ constexpr int kAttnWarps = 4;                         // two CTAs an SM
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnRing = 24 * 1024;                  // bytes a warp
 constexpr int kAttnMaxCtas = 512;
+// 16-bit caches take the matrix instructions (attn_mma.cuh) from five query heads
+// a block and up to heads of 128 values on.  (32 rows of 4096 bf16 entries, 8 K/V
+// heads of 128 values: 4 query heads each 91 us on the lanes, 96 on the matrix
+// instructions; 8 query heads 145 and 101; of 256 values their states would not
+// fit the registers.)
+constexpr int kAttnLanesHeads = 4, kAttnMmaDim = 128;
 static_assert(4 * kAttnMaxCtas <= kCounterBytes, "one ticket a CTA");
 
 // Floats of a partial state, whole 16-byte words.
@@ -145,8 +151,239 @@ __device__ __forceinline__ void chunk_pairs(int4 c, f32x2* out) {
     }
 }
 
-template <int KV, int NG, int LPK>
-struct AttnShape {
+// What a warp computes of a segment: its own entries KT of every TK from v_begin
+// on, for the block's query heads.
+struct Segment {
+    const AttnParams& p;
+    int row, g0, ng;
+    Visible vis;
+    uint32_t pitch;          // bytes from one entry to the next
+    int64_t off;             // of the row and K/V head in the caches
+    uint32_t v_end, v_begin;
+    int its;                 // stages
+    unsigned char* ring;
+    float* q;                // shared: the block's query heads [NG][DMAX]
+    float *m, *l;            // the warp's references and sums; its o goes to the ring [NG][DMAX]
+};
+
+// q by way of shared memory, scaled; zero behind D and behind the block's heads.
+template <class T>
+__device__ __forceinline__ void stage_q(const Segment& s) {
+    const AttnArgs& a = s.p.a;
+    const int D = int(a.dim);
+#pragma unroll 4
+    for (int e = threadIdx.x; e < T::NG * T::DMAX; e += kAttnThreads) {
+        const int g = e / T::DMAX, d = e % T::DMAX;
+        s.q[e] = g < s.ng && d < D ? a.q[s.row * a.ldq + int64_t(s.g0 + g) * D + d] * s.p.qscale : 0.0f;
+    }
+    __syncthreads();
+}
+
+template <class T>
+__device__ __forceinline__ void lanes_states(const Segment& s) {
+    constexpr int NG = T::NG, LPK = T::LPK, KV = T::KV;
+    const AttnParams& p = s.p;
+    const AttnArgs& a = p.a;
+    const int lane = threadIdx.x & 31, D = int(a.dim), ng = s.ng, its = s.its;
+    const int sl = lane % LPK, grp = lane / LPK, grp0 = lane - sl;
+    const int gl = sl / T::LG;                             // this lane's query head of the block
+    const int u0 = (sl / T::DUP) * T::R % T::U;            // and its first of R entry steps
+    const int swz = LPK == 4 ? (grp & 1) * 4 : 0;          // rows next to each other on other banks
+    const uint32_t ring_s = smem_u32(s.ring), v_begin = s.v_begin, v_end = s.v_end, pitch = s.pitch;
+    const Visible vis = s.vis;
+    // (a lane copies the same 16-byte column of every row it copies)
+    constexpr int CPR = T::PITCH / 16, RPI = CPR < 32 ? 32 / CPR : 1;   // chunks a row, rows at a time
+    const int r0 = CPR < 32 ? lane / CPR : 0, c0 = lane % CPR;
+    const unsigned char* kp = static_cast<const unsigned char*>(a.k) + s.off + c0 * 16;
+    const unsigned char* vp = static_cast<const unsigned char*>(a.v) + s.off + c0 * 16;
+    const uint32_t dst0 = ring_s + r0 * T::PITCH + (LPK == 4 ? c0 ^ (r0 & 1) * 4 : c0) * 16;
+
+    // (where the weights are accumulated: one lane of those that hold a score)
+    float* const scores = p.scores && gl < ng && sl % T::DUP == 0
+                              ? p.scores + (int64_t(s.row) * a.heads + s.g0 + gl) * p.cap
+                              : nullptr;
+    float ref = -INFINITY, l = 0.0f;    // of query head gl, over this lane group's entries
+
+    int in_slot = 0, out_slot = 0;
+    const auto load = [&](int it) {
+        if (it < its) {
+            const uint32_t st = dst0 + in_slot * (2 * T::HALF), vb = v_begin + uint32_t(it) * T::TK + r0;
+            in_slot = in_slot + 1 == T::S ? 0 : in_slot + 1;
+#pragma unroll
+            for (int r = 0; r < T::KT; r += RPI) {
+                const uint32_t v = vb + r, i = v + (v < vis.ns ? 0 : vis.gap);
+                const bool in = v < v_end;
+                const uint64_t at = in ? uint64_t(i) * pitch : 0;
+#pragma unroll
+                for (int c = 0; c < CPR; c += 32) {
+                    static_assert(LPK != 4 || RPI % 2 == 0, "a lane's rows swap their halves alike");
+                    if ((c0 + c) * T::CD < D) {
+                        cp16(st + r * T::PITCH + c * 16, kp + at + c * 16, in);
+                        cp16(st + T::HALF + r * T::PITCH + c * 16, vp + at + c * 16, in);
+                    }
+                }
+            }
+        }
+        cp_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < T::S - 1; ++i) load(i);
+
+    stage_q<T>(s);
+    f32x2 q[NG][T::NP], o[NG][T::NP];
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < T::NP; ++i) {
+            const int d = (i / (T::CD / 2) * LPK + sl) * T::CD + i % (T::CD / 2) * 2;
+            q[g][i] = *reinterpret_cast<const f32x2*>(s.q + g * T::DMAX + d);
+            o[g][i] = 0ull;
+        }
+    for (int it = 0; it < its; ++it) {
+        cp_wait<T::S - 2>();
+        __syncwarp();
+        load(it + T::S - 1);
+        const uint32_t st = ring_s + out_slot * (2 * T::HALF);
+        out_slot = out_slot + 1 == T::S ? 0 : out_slot + 1;
+        const uint32_t vb = v_begin + uint32_t(it) * T::TK;
+        // partial scores over this lane's values, x[g * U + u]
+        float x[T::NV];
+#pragma unroll
+        for (int u = 0; u < T::U; ++u) {
+            f32x2 k[T::NP];
+#pragma unroll
+            for (int c = 0; c < T::NC; ++c)
+                chunk_pairs<KV>(lds128(st + (u * T::KPS + grp) * T::PITCH + ((c * LPK + sl) ^ swz) * 16),
+                                k + c * (T::CD / 2));
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                f32x2 dot = mul2(q[g][0], k[0]);
+#pragma unroll
+                for (int i = 1; i < T::NP; ++i) dot = fma2(q[g][i], k[i], dot);
+                const float2 f = unpack2(dot);
+                x[g * T::U + u] = f.x + f.y;
+            }
+        }
+        // sum over the LPK lanes; lane sl keeps x[R * (sl / DUP) ...], R of them
+        int n = T::NV;
+#pragma unroll
+        for (int mask = LPK / 2; mask; mask >>= 1) {
+            if (n > 1) {
+                n /= 2;
+                const bool up = sl & mask;
+#pragma unroll
+                for (int i = 0; i < T::NV / 2; ++i) {
+                    if (i >= n) break;
+                    const float give = up ? x[i] : x[i + n], mine = up ? x[i + n] : x[i];
+                    x[i] = mine + __shfl_xor_sync(0xffffffffu, give, mask);
+                }
+            } else {
+                x[0] += __shfl_xor_sync(0xffffffffu, x[0], mask);
+            }
+        }
+        bool moves = false;
+#pragma unroll
+        for (int r = 0; r < T::R; ++r) {
+            const uint32_t v = vb + (u0 + r) * T::KPS + grp;
+            if (scores && v < v_end) scores[v] = x[r];
+            x[r] = v < v_end ? x[r] : -INFINITY;
+            moves = moves || x[r] > ref + 8.0f;
+        }
+        if (__any_sync(0xffffffffu, moves)) {
+            float top = ref;
+#pragma unroll
+            for (int r = 0; r < T::R; ++r) top = fmaxf(top, x[r]);
+#pragma unroll
+            for (int mask = T::LG / 2; mask; mask >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, mask));
+            const float f = top == ref ? 1.0f : ex2(ref - top);
+            ref = top;
+            l *= f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float fg = __shfl_sync(0xffffffffu, f, grp0 + g * T::LG);
+#pragma unroll
+                for (int i = 0; i < T::NP; ++i) o[g][i] = mul2(o[g][i], pack2(fg, fg));
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < T::R; ++r) {
+            x[r] = x[r] == -INFINITY ? 0.0f : ex2(x[r] - ref);
+            l += x[r];
+        }
+#pragma unroll
+        for (int u = 0; u < T::U; ++u) {
+            f32x2 v[T::NP];
+#pragma unroll
+            for (int c = 0; c < T::NC; ++c)
+                chunk_pairs<KV>(
+                    lds128(st + T::HALF + (u * T::KPS + grp) * T::PITCH + ((c * LPK + sl) ^ swz) * 16),
+                    v + c * (T::CD / 2));
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float w = __shfl_sync(0xffffffffu, x[u % T::R],
+                                            grp0 + (g * T::U + u) / T::R * T::DUP);
+                const f32x2 ww = pack2(w, w);
+#pragma unroll
+                for (int i = 0; i < T::NP; ++i) o[g][i] = fma2(ww, v[i], o[g][i]);
+            }
+        }
+    }
+    cp_wait<0>();
+    __syncwarp();
+
+    // join the warp's lane groups, then the warps
+    {
+        float top = ref;
+#pragma unroll
+        for (int mask = LPK; mask < 32; mask <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, mask));
+        const float f = ref == -INFINITY ? 0.0f : ex2(ref - top);
+        // (l stays NaN where a score was NaN before any other)
+        l = ref == -INFINITY ? l : l * f;
+        const float fo = ref == -INFINITY ? 1.0f : f;   // o is 0 or NaN there
+#pragma unroll
+        for (int mask = LPK; mask < 32; mask <<= 1) l += __shfl_xor_sync(0xffffffffu, l, mask);
+#pragma unroll
+        for (int mask = T::LG / 2; mask; mask >>= 1) l += __shfl_xor_sync(0xffffffffu, l, mask);
+        l *= 1.0f / T::DUP;
+        if (grp == 0 && sl % T::LG == 0) {
+            s.m[gl] = top;
+            s.l[gl] = l;
+        }
+        f32x2 z[NG * T::NP];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const float fg = __shfl_sync(0xffffffffu, fo, grp0 + g * T::LG);
+#pragma unroll
+            for (int i = 0; i < T::NP; ++i) z[g * T::NP + i] = mul2(o[g][i], pack2(fg, fg));
+        }
+        constexpr int P = NG * T::NP, KEEP = P / T::KPS;
+        int n = P;
+#pragma unroll
+        for (int mask = 16; mask >= LPK; mask >>= 1) {
+            n /= 2;
+            const bool up = lane & mask;
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) {
+                if (i >= n) break;
+                const f32x2 give = up ? z[i] : z[i + n], mine = up ? z[i + n] : z[i];
+                const float2 y = unpack2(__shfl_xor_sync(0xffffffffu, give, mask)), w = unpack2(mine);
+                z[i] = pack2(w.x + y.x, w.y + y.y);
+            }
+        }
+        float* so = reinterpret_cast<float*>(s.ring);     // [NG][DMAX]
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) {
+            const int at = grp * KEEP + i, g = at / T::NP, pr = at % T::NP;
+            const int d = (pr / (T::CD / 2) * LPK + sl) * T::CD + pr % (T::CD / 2) * 2;
+            *reinterpret_cast<float2*>(so + g * T::DMAX + d) = unpack2(z[i]);
+        }
+    }
+}
+
+template <int KV_, int NG_, int LPK_>
+struct AttnLanes {
+    static constexpr int KV = KV_, NG = NG_, LPK = LPK_;
     static constexpr int ELT = KV == Q8_KV_F32 ? 4 : 2;
     static constexpr int CD = 16 / ELT;                       // values a 16-byte chunk
     static constexpr int DPL = NG <= 4 ? 16 : 8;              // values a lane
@@ -166,14 +403,18 @@ struct AttnShape {
     static constexpr int R = NV > LPK ? NV / LPK : 1;         // scores a lane ends with
     static constexpr int DUP = LPK > NV ? LPK / NV : 1;       // lanes holding the same scores
     static constexpr int LG = LPK / NG;                       // lanes a query head
+    static constexpr int LEAST = NG == 8 ? 1 : 2;             // tiles a CTA, at least
     static_assert(S >= 2 && LG >= 1 && U % R == 0 && R * LPK >= NV, "attention tile");
-    static_assert(NG * DMAX * 4 + NG * 8 <= kAttnRing, "a warp's state fits its ring");
+    static_assert(NG * DMAX * 4 <= kAttnRing, "a warp's state fits its ring");
+
+    static __device__ __forceinline__ void states(const Segment& s) { lanes_states<AttnLanes>(s); }
 };
 
-template <int KV, int NG, int LPK>
+template <class T>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams p) {
-    using T = AttnShape<KV, NG, LPK>;
-    extern __shared__ __align__(128) unsigned char ring_all[];
+    constexpr int NG = T::NG;
+    extern __shared__ __align__(256) unsigned char ring_raw[];
+    unsigned char* const ring_all = ring_raw + (256 - (smem_u32(ring_raw) & 255) & 255);   // stages on 256 bytes
     __shared__ uint32_t s_pre[Q8_MAX_ROWS + 1];   // tiles before each row
     __shared__ uint32_t s_warp[kAttnWarps];
     __shared__ int s_pos[Q8_MAX_ROWS];
@@ -182,15 +423,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     __shared__ int s_last;
     const AttnArgs& a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int sl = lane % LPK, grp = lane / LPK, grp0 = lane - sl;
     const int D = int(a.dim), rows = int(a.rows);
     const uint32_t per_row = uint32_t(a.kv_heads) * p.nb;
     const int TT = T::TK * p.tile_its;                     // entries a tile
     unsigned char* ring = ring_all + warp * kAttnRing;
     const uint32_t ring_s = smem_u32(ring);
-    const int gl = sl / T::LG;                             // this lane's query head of the block
-    const int u0 = (sl / T::DUP) * T::R % T::U;            // and its first of R entry steps
-    const int swz = LPK == 4 ? (grp & 1) * 4 : 0;          // rows next to each other on other banks
 
     // values behind D are never copied; they stay zero
     if (D < T::DMAX) {
@@ -231,12 +468,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         __syncthreads();
     }
     // CTA c has tiles [first(c), first(c + 1)): all of them in equal shares, the
-    // first ones one longer.  Small problems: two tiles a CTA (fewer cost more to
-    // join than they save; of eight query heads, whose tiles are half as many bytes
-    // and twice the work, one), or a unit.
+    // first ones one longer.  Small problems: a tile or two a CTA (fewer cost more
+    // to join than they save; one where a tile is fewer bytes and more work), or a
+    // unit.
     const uint32_t real = s_pre[rows], units = uint32_t(rows) * per_row;
     const uint32_t extra = real >= 4 * gridDim.x ? T::EXTRA : 1, W = real + extra * units;
-    const uint32_t ctas = min(max(NG == 8 ? real : real / 2, units), gridDim.x), cta = blockIdx.x;
+    const uint32_t ctas = min(max(real / T::LEAST, units), gridDim.x), cta = blockIdx.x;
     __syncthreads();
     for (int i = tid; i <= rows; i += kAttnThreads) s_pre[i] += extra * i * per_row;
     __syncthreads();
@@ -280,200 +517,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         const uint64_t v_from = uint64_t(t0 - unit0) * TT + warp * T::KT;
         const uint32_t v_begin = uint32_t(v_from);
         const int its = v_end > v_from ? int((v_end - v_begin + T::TK - 1) / T::TK) : 0;
-        // (a lane copies the same 16-byte column of every row it copies)
-        constexpr int CPR = T::PITCH / 16, RPI = CPR < 32 ? 32 / CPR : 1;   // chunks a row, rows at a time
-        const int r0 = CPR < 32 ? lane / CPR : 0, c0 = lane % CPR;
-        const unsigned char* kp = static_cast<const unsigned char*>(a.k) + off + c0 * 16;
-        const unsigned char* vp = static_cast<const unsigned char*>(a.v) + off + c0 * 16;
-        const uint32_t dst0 = ring_s + r0 * T::PITCH + (LPK == 4 ? c0 ^ (r0 & 1) * 4 : c0) * 16;
-
-        // (where the weights are accumulated: one lane of those that hold a score)
-        float* const scores = p.scores && gl < ng && sl % T::DUP == 0
-                                  ? p.scores + (int64_t(m) * a.heads + g0 + gl) * p.cap
-                                  : nullptr;
-        float ref = -INFINITY, l = 0.0f;    // of query head gl, over this lane group's entries
-
-        int in_slot = 0, out_slot = 0;
-        const auto load = [&](int it) {
-            if (it < its) {
-                const uint32_t st = dst0 + in_slot * (2 * T::HALF), vb = v_begin + uint32_t(it) * T::TK + r0;
-                in_slot = in_slot + 1 == T::S ? 0 : in_slot + 1;
-#pragma unroll
-                for (int r = 0; r < T::KT; r += RPI) {
-                    const uint32_t v = vb + r, i = v + (v < vis.ns ? 0 : vis.gap);
-                    const bool in = v < v_end;
-                    const uint64_t at = in ? uint64_t(i) * pitch : 0;
-#pragma unroll
-                    for (int c = 0; c < CPR; c += 32) {
-                        static_assert(LPK != 4 || RPI % 2 == 0, "a lane's rows swap their halves alike");
-                        if ((c0 + c) * T::CD < D) {
-                            cp16(st + r * T::PITCH + c * 16, kp + at + c * 16, in);
-                            cp16(st + T::HALF + r * T::PITCH + c * 16, vp + at + c * 16, in);
-                        }
-                    }
-                }
-            }
-            cp_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < T::S - 1; ++i) load(i);
-
-        // q by way of shared memory, scaled; zero behind D and behind the block's heads
-#pragma unroll 4
-        for (int e = tid; e < NG * T::DMAX; e += kAttnThreads) {
-            const int g = e / T::DMAX, d = e % T::DMAX;
-            s_q[e] = g < ng && d < D ? a.q[m * a.ldq + int64_t(g0 + g) * D + d] * p.qscale : 0.0f;
-        }
-        __syncthreads();
-        f32x2 q[NG][T::NP], o[NG][T::NP];
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int i = 0; i < T::NP; ++i) {
-                const int d = (i / (T::CD / 2) * LPK + sl) * T::CD + i % (T::CD / 2) * 2;
-                q[g][i] = *reinterpret_cast<const f32x2*>(s_q + g * T::DMAX + d);
-                o[g][i] = 0ull;
-            }
-        for (int it = 0; it < its; ++it) {
-            cp_wait<T::S - 2>();
-            __syncwarp();
-            load(it + T::S - 1);
-            const uint32_t st = ring_s + out_slot * (2 * T::HALF);
-            out_slot = out_slot + 1 == T::S ? 0 : out_slot + 1;
-            const uint32_t vb = v_begin + uint32_t(it) * T::TK;
-            // partial scores over this lane's values, x[g * U + u]
-            float x[T::NV];
-#pragma unroll
-            for (int u = 0; u < T::U; ++u) {
-                f32x2 k[T::NP];
-#pragma unroll
-                for (int c = 0; c < T::NC; ++c)
-                    chunk_pairs<KV>(lds128(st + (u * T::KPS + grp) * T::PITCH + ((c * LPK + sl) ^ swz) * 16),
-                                    k + c * (T::CD / 2));
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    f32x2 s = mul2(q[g][0], k[0]);
-#pragma unroll
-                    for (int i = 1; i < T::NP; ++i) s = fma2(q[g][i], k[i], s);
-                    const float2 f = unpack2(s);
-                    x[g * T::U + u] = f.x + f.y;
-                }
-            }
-            // sum over the LPK lanes; lane sl keeps x[R * (sl / DUP) ...], R of them
-            int n = T::NV;
-#pragma unroll
-            for (int mask = LPK / 2; mask; mask >>= 1) {
-                if (n > 1) {
-                    n /= 2;
-                    const bool up = sl & mask;
-#pragma unroll
-                    for (int i = 0; i < T::NV / 2; ++i) {
-                        if (i >= n) break;
-                        const float give = up ? x[i] : x[i + n], mine = up ? x[i + n] : x[i];
-                        x[i] = mine + __shfl_xor_sync(0xffffffffu, give, mask);
-                    }
-                } else {
-                    x[0] += __shfl_xor_sync(0xffffffffu, x[0], mask);
-                }
-            }
-            bool moves = false;
-#pragma unroll
-            for (int r = 0; r < T::R; ++r) {
-                const uint32_t v = vb + (u0 + r) * T::KPS + grp;
-                if (scores && v < v_end) scores[v] = x[r];
-                x[r] = v < v_end ? x[r] : -INFINITY;
-                moves = moves || x[r] > ref + 8.0f;
-            }
-            if (__any_sync(0xffffffffu, moves)) {
-                float top = ref;
-#pragma unroll
-                for (int r = 0; r < T::R; ++r) top = fmaxf(top, x[r]);
-#pragma unroll
-                for (int mask = T::LG / 2; mask; mask >>= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, mask));
-                const float f = top == ref ? 1.0f : ex2(ref - top);
-                ref = top;
-                l *= f;
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const float fg = __shfl_sync(0xffffffffu, f, grp0 + g * T::LG);
-#pragma unroll
-                    for (int i = 0; i < T::NP; ++i) o[g][i] = mul2(o[g][i], pack2(fg, fg));
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < T::R; ++r) {
-                x[r] = x[r] == -INFINITY ? 0.0f : ex2(x[r] - ref);
-                l += x[r];
-            }
-#pragma unroll
-            for (int u = 0; u < T::U; ++u) {
-                f32x2 v[T::NP];
-#pragma unroll
-                for (int c = 0; c < T::NC; ++c)
-                    chunk_pairs<KV>(
-                        lds128(st + T::HALF + (u * T::KPS + grp) * T::PITCH + ((c * LPK + sl) ^ swz) * 16),
-                        v + c * (T::CD / 2));
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const float w = __shfl_sync(0xffffffffu, x[u % T::R],
-                                                grp0 + (g * T::U + u) / T::R * T::DUP);
-                    const f32x2 ww = pack2(w, w);
-#pragma unroll
-                    for (int i = 0; i < T::NP; ++i) o[g][i] = fma2(ww, v[i], o[g][i]);
-                }
-            }
-        }
-        cp_wait<0>();
-        __syncwarp();
-
-        // join the warp's lane groups, then the warps
-        {
-            float top = ref;
-#pragma unroll
-            for (int mask = LPK; mask < 32; mask <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, mask));
-            const float f = ref == -INFINITY ? 0.0f : ex2(ref - top);
-            // (l stays NaN where a score was NaN before any other)
-            l = ref == -INFINITY ? l : l * f;
-            const float fo = ref == -INFINITY ? 1.0f : f;   // o is 0 or NaN there
-#pragma unroll
-            for (int mask = LPK; mask < 32; mask <<= 1) l += __shfl_xor_sync(0xffffffffu, l, mask);
-#pragma unroll
-            for (int mask = T::LG / 2; mask; mask >>= 1) l += __shfl_xor_sync(0xffffffffu, l, mask);
-            l *= 1.0f / T::DUP;
-            if (grp == 0 && sl % T::LG == 0) {
-                s_m[warp][gl] = top;
-                s_l[warp][gl] = l;
-            }
-            f32x2 z[NG * T::NP];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const float fg = __shfl_sync(0xffffffffu, fo, grp0 + g * T::LG);
-#pragma unroll
-                for (int i = 0; i < T::NP; ++i) z[g * T::NP + i] = mul2(o[g][i], pack2(fg, fg));
-            }
-            constexpr int P = NG * T::NP, KEEP = P / T::KPS;
-            int n = P;
-#pragma unroll
-            for (int mask = 16; mask >= LPK; mask >>= 1) {
-                n /= 2;
-                const bool up = lane & mask;
-#pragma unroll
-                for (int i = 0; i < P / 2; ++i) {
-                    if (i >= n) break;
-                    const f32x2 give = up ? z[i] : z[i + n], mine = up ? z[i + n] : z[i];
-                    const float2 y = unpack2(__shfl_xor_sync(0xffffffffu, give, mask)), w = unpack2(mine);
-                    z[i] = pack2(w.x + y.x, w.y + y.y);
-                }
-            }
-            float* so = reinterpret_cast<float*>(ring);       // [NG][DMAX]
-#pragma unroll
-            for (int i = 0; i < KEEP; ++i) {
-                const int at = grp * KEEP + i, g = at / T::NP, pr = at % T::NP;
-                const int d = (pr / (T::CD / 2) * LPK + sl) * T::CD + pr % (T::CD / 2) * 2;
-                *reinterpret_cast<float2*>(so + g * T::DMAX + d) = unpack2(z[i]);
-            }
-        }
+        const Segment seg{p, m, g0, ng, vis, pitch, off, v_end, v_begin, its, ring, s_q, s_m[warp], s_l[warp]};
+        T::states(seg);
         __syncthreads();
 
         // the CTA's state of the segment, and the whole unit's where it is all here
@@ -585,11 +630,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     }
 }
 
-template <int KV, int NG, int LPK>
-cudaError_t launch_attn_shape(const AttnParams& p, const LaunchCtx& ctx) {
+template <class T>
+cudaError_t launch_attn_kernel(const AttnParams& p, const LaunchCtx& ctx) {
     static std::atomic<bool> ready[kMaxDevices];
-    const auto kern = attn_kernel<KV, NG, LPK>;
-    constexpr size_t smem = size_t(kAttnWarps) * kAttnRing;
+    const auto kern = attn_kernel<T>;
+    constexpr size_t smem = size_t(kAttnWarps) * kAttnRing + 256;
     const cudaError_t e = set_smem_once(kern, smem, ctx.dev, ready);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -603,27 +648,23 @@ cudaError_t launch_attn_shape(const AttnParams& p, const LaunchCtx& ctx) {
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// LPK: the lanes that hold an entry's head_dim values, DPL each.
+// LPK, the lanes that hold an entry's values, by head_dim.
 template <int KV, int NG>
-cudaError_t launch_attn_heads(const AttnParams& p, const LaunchCtx& ctx) {
-    constexpr int DPL = AttnShape<KV, NG, 8>::DPL;
-    if constexpr (DPL == 16) {
-        if (p.a.dim <= 64) return launch_attn_shape<KV, NG, 4>(p, ctx);
-        if (p.a.dim <= 128) return launch_attn_shape<KV, NG, 8>(p, ctx);
-        return launch_attn_shape<KV, NG, 16>(p, ctx);
-    } else {
-        if (p.a.dim <= 64) return launch_attn_shape<KV, NG, 8>(p, ctx);
-        if (p.a.dim <= 128) return launch_attn_shape<KV, NG, 16>(p, ctx);
-        return launch_attn_shape<KV, NG, 32>(p, ctx);
+cudaError_t launch_attn_lanes(const AttnParams& p, const LaunchCtx& ctx) {
+    constexpr int SHARE = AttnLanes<KV, NG, 8>::DPL == 16 ? 1 : 2;
+    if constexpr (KV == Q8_KV_F32 || NG <= kAttnLanesHeads) {
+        if (p.a.dim <= 64) return launch_attn_kernel<AttnLanes<KV, NG, 4 * SHARE>>(p, ctx);
+        if (p.a.dim <= 128) return launch_attn_kernel<AttnLanes<KV, NG, 8 * SHARE>>(p, ctx);
     }
+    return launch_attn_kernel<AttnLanes<KV, NG, 16 * SHARE>>(p, ctx);
 }
 
 template <int KV>
 cudaError_t launch_attn_type(const AttnParams& p, const LaunchCtx& ctx) {
-    if (p.gsz == 1) return launch_attn_heads<KV, 1>(p, ctx);
-    if (p.gsz == 2) return launch_attn_heads<KV, 2>(p, ctx);
-    if (p.gsz <= 4) return launch_attn_heads<KV, 4>(p, ctx);
-    return launch_attn_heads<KV, 8>(p, ctx);
+    if (p.gsz == 1) return launch_attn_lanes<KV, 1>(p, ctx);
+    if (p.gsz == 2) return launch_attn_lanes<KV, 2>(p, ctx);
+    if (p.gsz <= 4) return launch_attn_lanes<KV, 4>(p, ctx);
+    return launch_attn_lanes<KV, 8>(p, ctx);
 }
 
 }  // namespace q8

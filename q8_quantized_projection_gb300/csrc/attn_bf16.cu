@@ -1,10 +1,10 @@
 // attn_bf16.cu -- the attention kernels over bf16 caches.
-#include "attn.cuh"
+#include "attn_mma.cuh"
 
 namespace q8 {
 
 cudaError_t launch_attn_bf16(const AttnParams& p, const LaunchCtx& ctx) {
-    return launch_attn_type<Q8_KV_BF16>(p, ctx);
+    return launch_attn_16<Q8_KV_BF16>(p, ctx);
 }
 
 }  // namespace q8

@@ -1,0 +1,358 @@
+// attn_mma.cuh -- the attention kernels over 16-bit caches of heads up to 128
+// values: the products on the matrix instructions (mma.m16n8k16).
+//
+// With the entries of a stage as the n of the first product and the k of the
+// second, a block of at most 8 query heads fills half of m = 16.  The other half
+// takes what the operand's 16-bit rounding lost: rows 0-7 hold q (then p) rounded,
+// rows 8-15 the rest of it rounded, so one instruction gives both parts' products
+// (f16: 22 bits; bf16: 16, and a second instruction adds 8 more).  K and V enter
+// as they are.  The accumulator layout of the scores is the operand layout of the
+// weights, and all that a lane holds belongs to one query head: no exchange
+// between lanes but two shuffles where a reference moves.
+//
+// Precision.  q is brought to [2^13, 2^14) by a power of two a head (f16), p is
+// at most 2^8 and carried as 2^7 p, so that what falls below f16's subnormals is
+// below 2^-32 of the largest weight.  The instruction truncates its sums; chains
+// are kept short (every other step of a score; 64 entries of o) and joined by
+// rounded binary32 additions: measured 2e-7 where one chain of 512 steps is 1e-5
+// off.  A part times infinity is NaN, so a warp whose state is not finite computes
+// its entries again, one by one, by the formula.
+//
+// What bounds it: HBM.  A stage of 16 bf16 entries of 128 values is 64
+// instructions of 2 clocks an SM, 8 clocks an entry against 23 for its bytes
+// (6.6 TB/s); on the lanes' FMA path eight query heads take 40.
+#pragma once
+
+#include <cfloat>
+
+#include "attn.cuh"
+
+namespace q8 {
+
+template <int KV>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (KV == Q8_KV_F16)
+        asm(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    if constexpr (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr));
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr));
+}
+
+// a and b rounded to the cache's type, as one word (a in the low half); a and b
+// become what the rounding lost.
+template <int KV>
+__device__ __forceinline__ uint32_t round_pair(float& a, float& b) {
+    uint32_t w;
+    if constexpr (KV == Q8_KV_F16) {
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        a -= f.x, b -= f.y;
+    } else {
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+        a -= __int_as_float(int(w << 16));
+        b -= __int_as_float(int(w & 0xffff0000u));
+    }
+    return w;
+}
+
+template <int KV>
+__device__ __forceinline__ float from16(const unsigned char* p) {
+    if constexpr (KV == Q8_KV_F16) return __half2float(*reinterpret_cast<const __half*>(p));
+    return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
+}
+
+// A warp's states entry by entry in binary32, lanes over the values.
+template <class T>
+__device__ __noinline__ void plain_states(const Segment& s) {
+    const AttnArgs& a = s.p.a;
+    const int lane = threadIdx.x & 31, D = int(a.dim);
+    constexpr int J = T::DMAX / 32;
+    for (int g = 0; g < s.ng; ++g) {
+        float* const scores = s.p.scores ? s.p.scores + (int64_t(s.row) * a.heads + s.g0 + g) * s.p.cap : nullptr;
+        float top = -INFINITY, l = 0.0f, o[J] = {};
+        for (int it = 0; it < s.its; ++it)
+            for (int r = 0; r < T::KT; ++r) {
+                const uint32_t v = s.v_begin + uint32_t(it) * T::TK + r;
+                if (v >= s.v_end) break;
+                const int64_t at = s.off + int64_t(v + (v < s.vis.ns ? 0 : s.vis.gap)) * s.pitch;
+                float x = 0.0f;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int d = lane + 32 * j;
+                    if (d < D)
+                        x = fmaf(s.q[g * T::DMAX + d], from16<T::KV>(static_cast<const unsigned char*>(a.k) + at + 2 * d), x);
+                }
+#pragma unroll
+                for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+                if (scores && lane == 0) scores[v] = x;
+                const float n = fmaxf(top, x), f = n == top ? 1.0f : ex2(top - n), w = x == -INFINITY ? 0.0f : ex2(x - n);
+                top = n;
+                l = l * f + w;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int d = lane + 32 * j;
+                    if (d < D) o[j] = o[j] * f + w * from16<T::KV>(static_cast<const unsigned char*>(a.v) + at + 2 * d);
+                }
+            }
+        if (lane == 0) {
+            s.m[g] = top;
+            s.l[g] = l;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) reinterpret_cast<float*>(s.ring)[g * T::DMAX + lane + 32 * j] = o[j];
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void mma_states(const Segment& s) {
+    constexpr int KV = T::KV, KS = T::KS, SUB = T::SUB;
+    constexpr bool BF = KV == Q8_KV_BF16;
+    const AttnParams& p = s.p;
+    const AttnArgs& a = p.a;
+    const int lane = threadIdx.x & 31, D = int(a.dim), its = s.its;
+    const int g = lane >> 2, c2 = (lane & 3) * 2;       // this lane's query head, and its entries (or values) of 8
+    const uint32_t ring_s = smem_u32(s.ring);
+    // a lane copies the same 16-byte column of a row in RPI; the row's swap of
+    // chunks is its own (r0) and that of the row it begins at
+    const int r0 = lane / T::CPR, c0 = lane % T::CPR;
+    const bool copies = r0 < T::RPI && c0 * 8 < D;
+    const unsigned char* kp = static_cast<const unsigned char*>(a.k) + s.off + c0 * 16;
+    const unsigned char* vp = static_cast<const unsigned char*>(a.v) + s.off + c0 * 16;
+    const uint32_t to = r0 * T::PITCH + T::swap(c0, r0) * 16, step = T::RPI * s.pitch;
+
+    int in_slot = 0, out_slot = 0;
+    const auto load = [&](int it) {
+        if (it < its && copies) {
+            const uint32_t st = ring_s + in_slot * (2 * T::HALF) + to, vb = s.v_begin + uint32_t(it) * T::TK + r0;
+            const uint32_t vt = s.v_begin + uint32_t(it) * T::TK;
+            if (vt + T::KT <= s.v_end && (vt >= s.vis.ns || vt + T::KT <= s.vis.ns)) {
+                // all of them, with none left out between
+                const uint64_t at = uint64_t(vb + (vt < s.vis.ns ? 0 : s.vis.gap)) * s.pitch;
+                const unsigned char *ka = kp + at, *va = vp + at;
+#pragma unroll
+                for (int r = 0; r < T::KT; r += T::RPI, ka += step, va += step) {
+                    const uint32_t dst = (st ^ T::turn(r)) + r * T::PITCH;
+                    cp16(dst, ka, true);
+                    cp16(dst + T::HALF, va, true);
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < T::KT; r += T::RPI) {
+                    const uint32_t v = vb + r, dst = (st ^ T::turn(r)) + r * T::PITCH;
+                    const bool in = v < s.v_end;
+                    const uint64_t at = in ? uint64_t(v + (v < s.vis.ns ? 0 : s.vis.gap)) * s.pitch : 0;
+                    cp16(dst, kp + at, in);
+                    cp16(dst + T::HALF, vp + at, in);
+                }
+            }
+        }
+        in_slot = in_slot + 1 == T::S ? 0 : in_slot + 1;
+        cp_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < T::S - 1; ++i) load(i);
+
+    stage_q<T>(s);
+    float scale = 1.0f, back = 1.0f;
+    const float* q = s.q + g * T::DMAX + c2;
+    if constexpr (!BF) {
+        float most = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 2 * KS; ++k) most = fmaxf(most, fmaxf(fabsf(q[8 * k]), fabsf(q[8 * k + 1])));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        // powers of two: 2^(13 - the largest's exponent), and its inverse
+        const int e = min(max(267 - (__float_as_int(most) >> 23), 1), 253);
+        scale = __int_as_float(e << 23);
+        back = __int_as_float((254 - e) << 23);
+    }
+    uint32_t qa[KS][4], ql[BF ? KS : 1][2];
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float x = q[16 * k + 8 * h] * scale, y = q[16 * k + 8 * h + 1] * scale;
+            qa[k][2 * h] = round_pair<KV>(x, y);
+            qa[k][2 * h + 1] = round_pair<KV>(x, y);
+            if constexpr (BF) ql[k][h] = round_pair<KV>(x, y);
+        }
+    float o[2 * KS][4] = {}, sum[2 * KS][2] = {};       // chains of o; their sums
+    float ref = -INFINITY, l = 0.0f;
+    float* const scores =
+        p.scores && g < s.ng ? p.scores + (int64_t(s.row) * a.heads + s.g0 + g) * p.cap : nullptr;
+    // where this lane's rows of the matrix loads begin: of K four of entries 0-7 and
+    // 8-15 by values 0-7 and 8-15, of V transposed
+    const int kr = (lane >> 4) * 8 + (lane & 7), vr = (lane >> 3 & 1) * 8 + (lane & 7);
+    const uint32_t k_at = kr * T::PITCH + T::swap(lane >> 3 & 1, kr) * 16;
+    const uint32_t v_at = T::HALF + vr * T::PITCH + T::swap(lane >> 4, vr) * 16;
+    const auto flush = [&] {
+#pragma unroll
+        for (int t = 0; t < 2 * KS; ++t) {
+            sum[t][0] += o[t][0] + o[t][2];
+            sum[t][1] += o[t][1] + o[t][3];
+            o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
+        }
+    };
+
+    for (int it = 0; it < its; ++it) {
+        cp_wait<T::S - 2>();
+        __syncwarp();
+        load(it + T::S - 1);
+        const uint32_t st = ring_s + out_slot * (2 * T::HALF);
+        out_slot = out_slot + 1 == T::S ? 0 : out_slot + 1;
+        const uint32_t vb = s.v_begin + uint32_t(it) * T::TK;
+        float x[SUB][4];                                // entries c2, c2 + 1, 8 + c2, 9 + c2 of each 16
+        bool moves = false;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+            // scores of 16 entries, two chains each
+            float c[2][2][4] = {};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                uint32_t kb[4];
+                ldmatrix4<false>(kb, T::column(st + k_at, 2 * k) + u * 16 * T::PITCH);
+                mma16<KV>(c[0][k & 1], qa[k], kb[0], kb[1]);
+                mma16<KV>(c[1][k & 1], qa[k], kb[2], kb[3]);
+                if constexpr (BF) {
+                    const uint32_t low[4] = {ql[k][0], 0u, ql[k][1], 0u};
+                    mma16<KV>(c[0][k & 1], low, kb[0], kb[1]);
+                    mma16<KV>(c[1][k & 1], low, kb[2], kb[3]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float(&d)[2][4] = c[j >> 1];
+                float y = (d[0][j & 1] + d[1][j & 1]) + (d[0][2 + (j & 1)] + d[1][2 + (j & 1)]);
+                if constexpr (!BF) y *= back;
+                const uint32_t v = vb + 16 * u + (j >> 1) * 8 + c2 + (j & 1);
+                if (scores && v < s.v_end) scores[v] = y;
+                x[u][j] = v < s.v_end ? y : -INFINITY;
+                moves = moves || x[u][j] > ref + 8.0f;
+            }
+        }
+        if (__any_sync(0xffffffffu, moves)) {
+            float top = ref;
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) top = fmaxf(top, fmaxf(fmaxf(x[u][0], x[u][1]), fmaxf(x[u][2], x[u][3])));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float f = top == ref ? 1.0f : ex2(ref - top);
+            ref = top;
+            l *= f;
+#pragma unroll
+            for (int t = 0; t < 2 * KS; ++t) {
+                sum[t][0] *= f, sum[t][1] *= f;
+                o[t][0] *= f, o[t][1] *= f, o[t][2] *= f, o[t][3] *= f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[u][j] = x[u][j] == -INFINITY ? 0.0f : ex2(x[u][j] - ref);
+                l += x[u][j];
+                if constexpr (!BF) x[u][j] *= 128.0f;
+            }
+            uint32_t pa[4], pl[4] = {};
+            pa[0] = round_pair<KV>(x[u][0], x[u][1]);
+            pa[1] = round_pair<KV>(x[u][0], x[u][1]);
+            pa[2] = round_pair<KV>(x[u][2], x[u][3]);
+            pa[3] = round_pair<KV>(x[u][2], x[u][3]);
+            if constexpr (BF) {
+                pl[0] = round_pair<KV>(x[u][0], x[u][1]);
+                pl[2] = round_pair<KV>(x[u][2], x[u][3]);
+            }
+#pragma unroll
+            for (int t = 0; t < KS; ++t) {
+                uint32_t v[4];
+                ldmatrix4<true>(v, T::column(st + v_at, 2 * t) + u * 16 * T::PITCH);
+                mma16<KV>(o[2 * t], pa, v[0], v[1]);
+                mma16<KV>(o[2 * t + 1], pa, v[2], v[3]);
+                if constexpr (BF) {
+                    mma16<KV>(o[2 * t], pl, v[0], v[1]);
+                    mma16<KV>(o[2 * t + 1], pl, v[2], v[3]);
+                }
+            }
+        }
+        if (it % (4 / SUB) == 4 / SUB - 1) flush();
+    }
+    flush();
+    cp_wait<0>();
+    __syncwarp();
+
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    float zero = l * 0.0f;
+#pragma unroll
+    for (int t = 0; t < 2 * KS; ++t) zero += sum[t][0] * 0.0f + sum[t][1] * 0.0f;
+    if (__any_sync(0xffffffffu, !(zero == 0.0f))) {      // something infinite or NaN among what was seen
+        plain_states<T>(s);
+        return;
+    }
+    if ((lane & 3) == 0) {
+        s.m[g] = ref;
+        s.l[g] = l;
+    }
+    float* so = reinterpret_cast<float*>(s.ring) + g * T::DMAX + c2;
+#pragma unroll
+    for (int t = 0; t < 2 * KS; ++t) {
+        constexpr float f = BF ? 1.0f : 1.0f / 128.0f;
+        *reinterpret_cast<float2*>(so + 8 * t) = make_float2(sum[t][0] * f, sum[t][1] * f);
+    }
+}
+
+// KS: steps of 16 values a head.
+template <int KV_, int KS_>
+struct AttnMma {
+    static constexpr int KV = KV_, KS = KS_, NG = 8;
+    static constexpr int ELT = 2, DMAX = 16 * KS, PITCH = 2 * DMAX, CPR = 2 * KS;
+    static constexpr int SUB = KS == 4 ? 2 : 1;               // products of 16 entries a stage
+    static constexpr int KT = 16 * SUB, HALF = KT * PITCH;
+    static constexpr int S0 = kAttnRing / (2 * HALF);
+    static constexpr int S = S0 > 6 ? 6 : S0;
+    static constexpr int TK = kAttnWarps * KT;
+    static constexpr int EXTRA = (128 * 1024 + kAttnWarps * 2 * HALF - 1) / (kAttnWarps * 2 * HALF);
+    static constexpr int LEAST = 1;
+    static_assert(S >= 2 && NG * DMAX * 4 <= kAttnRing && DMAX % 32 == 0, "attention tile");
+
+    static constexpr int RPI = CPR == 8 ? 4 : 2;              // rows a warp copies at a time
+
+    // Chunk c of entry r lies at swap(c, r), so that the eight rows of a matrix load
+    // are on banks of their own (rows of 12 chunks begin on every other half).
+    static __device__ __forceinline__ int swap(int c, int r) { return CPR % 8 ? c ^ (r >> 1 & 3) : c ^ (r & 7); }
+    // What row r (a multiple of RPI) adds to the swap of a place in row r0 < RPI; a
+    // stage begins on a multiple of 128 bytes, and of a row where that is 256.
+    static constexpr uint32_t turn(int r) { return uint32_t(CPR % 8 ? r >> 1 & 3 : r & 7) * 16; }
+    // The place of chunk c more (even) than that at `at`.
+    static __device__ __forceinline__ uint32_t column(uint32_t at, int c) {
+        return CPR % 8 ? (at ^ uint32_t(c & 2) * 16) + uint32_t(c & ~3) * 16 : at ^ uint32_t(c) * 16;
+    }
+    static __device__ __forceinline__ void states(const Segment& s) { mma_states<AttnMma>(s); }
+};
+
+template <int KV>
+cudaError_t launch_attn_16(const AttnParams& p, const LaunchCtx& ctx) {
+    if (p.gsz <= kAttnLanesHeads || p.a.dim > kAttnMmaDim) return launch_attn_type<KV>(p, ctx);
+    if (p.a.dim <= 64) return launch_attn_kernel<AttnMma<KV, 4>>(p, ctx);
+    if (p.a.dim <= 96) return launch_attn_kernel<AttnMma<KV, 6>>(p, ctx);
+    return launch_attn_kernel<AttnMma<KV, 8>>(p, ctx);
+}
+
+}  // namespace q8

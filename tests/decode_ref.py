@@ -22,7 +22,9 @@ def attn(q, k, v, pos, heads, kv_heads, window, sinks, scale, acc=None):
     rounded at most once more (the scale): |ds| <= (D + 4) u sum|q k| scale.
     A weight exp(s - m) then carries a relative 2 |ds|max + 8u (the maximum's
     own error included; the exponential and the steps around it a few u), its
-    sums over n entries n u more, and the same again for the normalising sum."""
+    sums over n entries n u more, and the same again for the normalising sum.
+    (Operands carried as two or three 16-bit parts hold 22 bits at least: 4u of a
+    score's product and 4u of a weight, within the D + 4 and the 8.)"""
     rows, n_pos, _ = k.shape
     dim = k.shape[2] // kv_heads
     group = heads // kv_heads

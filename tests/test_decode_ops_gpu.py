@@ -97,6 +97,64 @@ def test_attn_window_and_sinks(window, sinks):
     Attn("f32", [199, 99, 64, 0, 3], 4, 2, 32, 200, window=window, sinks=sinks, seed=window % 97 + sinks % 89).check()
 
 
+@pytest.mark.parametrize("kv", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [8, 24, 64, 72, 88, 96, 104, 128])
+@pytest.mark.parametrize("group,n", [(5, 17), (6, 1), (7, 64), (8, 300), (16, 65)])
+def test_attn_eight_heads_of_16_bit_caches(kv, dim, group, n):
+    """The products on the matrix instructions: heads padded to whole steps, entries to whole stages."""
+    Attn(kv, [n - 1, n // 2, n // 3], 2 * group, 2, dim, n, window=70, sinks=2, seed=dim + n).check()
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16"])
+def test_attn_eight_heads_of_odd_magnitudes(kv):
+    t = torch()
+    for q_scale, k_scale in ((1e-6, 1.0), (1e-6, 3e4), (30.0, 1.0), (1e4, 1e-3), (1.0, 1e-4), (0.0, 1.0)):
+        a = Attn(kv, [499, 40], 8, 1, 64, 500, seed=3)
+        a.wide.mul_(q_scale)
+        a.q[:, :64] *= t.logspace(-6, 0, 64, device="cuda")        # one head's values far apart
+        a.k.copy_((a.k.float() * k_scale).clamp(-6e4, 6e4).to(a.k.dtype))     # (within f16)
+        a.check()
+    a = Attn(kv, [499, 40], 8, 1, 64, 500, seed=4)                 # masks of the type's lowest value
+    a.q.abs_()
+    a.k[:, ::3] = t.finfo(a.k.dtype).min if kv == "f16" else -1e30
+    a.v[:, ::3] = t.finfo(a.v.dtype).max if kv == "f16" else 1e30
+    a.check()
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 80, 128])
+def test_attn_eight_heads_of_not_finite_values_that_are_seen(kv, dim):
+    """As the formulas say, in the warps that see them and no others."""
+    t = torch()
+    a = Attn(kv, [899, 899, 899, 30], 16, 2, dim, 900, acc=True, seed=8)
+    a.q.abs_()
+    clean = a.want()
+    a.k[0, 450, :dim] = math.nan            # K/V head 0 of row 0
+    a.k[1, 460, dim:] = -math.inf           # head 1 of row 1: drops out
+    a.v[2, 10, 3] = math.inf                # one value of head 0 of row 2
+    a.k[3, 31:], a.v[3, 31:] = math.nan, math.inf     # behind the last entry
+    acc0 = a.acc.clone()
+    kd, vd = a.k.cpu().double().numpy(), a.v.cpu().double().numpy()
+    kd[1, 460, dim:] = -1e30                # what -inf means where q is above 0
+    vd[3, 31:], kd[3, 31:] = 0, 0
+    a.call()
+    got, acc = a.out.cpu().double().numpy(), a.acc.cpu().double().numpy()
+    half = 8 * dim
+    assert np.isnan(got[0, :half]).all() and np.isnan(acc[0, 0]).all()
+    assert np.all(np.abs(got[0, half:] - clean[0][0, half:]) <= clean[1][0, half:])
+    want, tol, want_acc, acc_tol = ref.attn(a.q.cpu().double().numpy()[1:2], kd[1:2], vd[1:2], [899], 16, 2, -1, 0,
+                                            dim ** -0.5, acc0.cpu().double().numpy()[1:2])
+    # (the tolerance's largest |q k| without the entry that drops out)
+    assert np.all(np.abs(got[1] - want[0]) <= clean[1][1] * 2)
+    assert np.all(np.abs(acc[1] - want_acc[0]) <= clean[3][1] * 2)
+    seen = np.arange(16 * dim) % dim == 3
+    seen[half:] = False
+    assert np.isposinf(got[2, seen]).all()
+    assert np.all(np.abs(got[2, ~seen] - clean[0][2, ~seen]) <= clean[1][2, ~seen])
+    assert np.all(np.abs(got[3] - clean[0][3]) <= clean[1][3])
+    no_error()
+
+
 @pytest.mark.parametrize("heads,kv_heads,dim", [(1024, 4, 16), (128, 1, 64), (1024, 1024, 8), (71, 71, 128)])
 def test_attn_many_heads(heads, kv_heads, dim):
     Attn("bf16", [90, 12], heads, kv_heads, dim, 91, window=60, sinks=1, seed=heads).check()
