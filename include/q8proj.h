@@ -322,7 +322,8 @@ size_t head_argmax_noalloc_scratch_bytes(void);
  * the result does not depend on what else runs (no atomics on values).
  * 1 <= rows <= Q8_MAX_ROWS; heads a multiple of kv_heads, heads <= 1024;
  * head_dim a multiple of 8, 8 <= head_dim <= 256; 1 <= n_pos <= 2^31 - 1, each
- * cache at most 2^40 bytes; window >= -1, sinks >= 0; out overlaps no input.
+ * cache at most 2^40 bytes; window >= -1, sinks >= 0; out, acc and the workspace
+ * overlap nothing else (Q8_ERR_ARG).
  *   workspace: attn_decode_workspace(...) bytes for the same arguments (with_acc:
  *   acc is given), zeroed whole before the first call on it; every completed
  *   call leaves what it counts with at zero, so that calls of any sizes, of

@@ -530,10 +530,13 @@ q8_status attn_decode(const float* q, int64_t ldq, const void* k_cache, const vo
         overlaps2(acc, an, q, qn) || overlaps2(acc, an, k_cache, cache) ||
         overlaps2(acc, an, v_cache, cache) || overlaps2(acc, an, pos, pn))
         return Q8_ERR_ARG;
-    if (!workspace ||
-        ws_bytes < attn_workspace_bytes(rows, heads, kv_heads, head_dim, n_pos, window, sinks, acc != nullptr))
-        return Q8_ERR_WORKSPACE;
+    const size_t wn = attn_workspace_bytes(rows, heads, kv_heads, head_dim, n_pos, window, sinks, acc != nullptr);
+    if (!workspace || ws_bytes < wn) return Q8_ERR_WORKSPACE;
     if (!aligned16(workspace)) return Q8_ERR_ALIGN;
+    if (overlaps2(workspace, wn, q, qn) || overlaps2(workspace, wn, k_cache, cache) ||
+        overlaps2(workspace, wn, v_cache, cache) || overlaps2(workspace, wn, pos, pn) ||
+        overlaps2(workspace, wn, out, on) || overlaps2(workspace, wn, acc, an))
+        return Q8_ERR_ARG;
     LaunchCtx ctx;
     if ((st = make_ctx(stream, ctx)) != Q8_OK) return st;
     const AttnArgs a{q,   ldq,    k_cache, v_cache, kv_type, rows, n_pos, heads, kv_heads, head_dim,
@@ -564,18 +567,19 @@ q8_status kv_evict(void* k_cache, void* v_cache, int kv_type, int64_t rows, int6
         return Q8_ERR_ALIGN;
     const size_t an = size_t(rows * kv_heads) * size_t(n_pos) * 4, pn = size_t(rows) * 4;
     const size_t kn = size_t(rows * kv_heads) * size_t(budget) * 4;
+    const size_t wn = evict_workspace_bytes(rows, kv_heads, budget);
+    if (!workspace || ws_bytes < wn) return Q8_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     // every buffer that is written is disjoint from every other one
     const struct { const void* p; size_t n; bool written; } b[] = {
-        {k_cache, cache, true}, {v_cache, cache, true}, {pos, pn, false},    {acc, an, false},
-        {new_pos, pn, true},    {new_acc, an, true},    {kept, kn, true}};
-    for (int i = 0; i < 7; ++i)
+        {k_cache, cache, true}, {v_cache, cache, true}, {pos, pn, false}, {acc, an, false},
+        {new_pos, pn, true},    {new_acc, an, true},    {kept, kn, true}, {workspace, wn, true}};
+    for (int i = 0; i < 8; ++i)
         for (int j = 0; j < i; ++j) {
             if (!b[i].written && !b[j].written) continue;
             if ((i == 4 && j == 2 && new_pos == pos) || (i == 5 && j == 3 && new_acc == acc)) continue;
             if (overlaps2(b[i].p, b[i].n, b[j].p, b[j].n)) return Q8_ERR_ARG;
         }
-    if (!workspace || ws_bytes < evict_workspace_bytes(rows, kv_heads, budget)) return Q8_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     LaunchCtx ctx;
     if ((st = make_ctx(stream, ctx)) != Q8_OK) return st;
     const EvictArgs a{k_cache, v_cache, kv_type, rows,    n_pos,   kv_heads, head_dim, pos,

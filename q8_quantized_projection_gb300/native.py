@@ -271,13 +271,19 @@ def _need_rows(what, t, dtype, rows, least, device):
     return t.data_ptr(), pitch if rows != 1 else t.shape[1]
 
 
+_torch = None
+
+
 def _current(what, t):
     """(torch, the device index of a call's first tensor, which must be the current one)."""
-    import torch
+    global _torch
     device = t.get_device()
-    if device < 0 or device != torch.cuda.current_device():
+    if _torch is None:
+        import torch
+        _torch = torch
+    if device < 0 or device != _torch._C._cuda_getDevice():
         raise ValueError(f"{what} is on {t.device}; calls run on the current CUDA device")
-    return torch, device
+    return _torch, device
 
 
 def _raw_stream(torch, device, stream):
@@ -293,7 +299,7 @@ def _workspace(workspace, device):
 
 
 def _kv_caches(k_cache, v_cache, kv_heads):
-    """(torch, device, kv type, rows, n_pos, head_dim) of a pair of caches
+    """(torch, device, K and V addresses, kv type, rows, n_pos, head_dim) of a pair of caches
     [rows, n_pos, kv_heads * head_dim]."""
     torch, device = _current("k_cache", k_cache)
     dtype, shape = k_cache.dtype, k_cache.shape
@@ -303,17 +309,17 @@ def _kv_caches(k_cache, v_cache, kv_heads):
         raise TypeError(f"k_cache must be float32, float16 or bfloat16, not {dtype}")
     if len(shape) != 3:
         raise ValueError(f"k_cache must have shape (rows, n_pos, kv_dim), not {tuple(shape)}")
-    _need("k_cache", k_cache, dtype, shape, device)
-    _need("v_cache", v_cache, dtype, shape, device)
+    k_at = _need("k_cache", k_cache, dtype, shape, device)
+    v_at = _need("v_cache", v_cache, dtype, shape, device)
     rows, n_pos, kv_dim = shape
     if kv_heads < 1 or kv_dim % kv_heads:
         raise ValueError(f"cache rows of {kv_dim} values do not hold {kv_heads} heads")
-    return torch, device, kv, rows, n_pos, kv_dim // kv_heads
+    return torch, device, k_at, v_at, kv, rows, n_pos, kv_dim // kv_heads
 
 
 def attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window=-1, sinks=0, acc=False) -> int:
-    return int(load().attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window, sinks,
-                                            1 if acc else 0))
+    return int((_lib or load()).attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window,
+                                                          sinks, 1 if acc else 0))
 
 
 def attn_decode(q, k_cache, v_cache, pos, out, workspace, heads, kv_heads, window=-1, sinks=0,
@@ -321,13 +327,13 @@ def attn_decode(q, k_cache, v_cache, pos, out, workspace, heads, kv_heads, windo
     """q, out: [rows, >= heads * head_dim] float32 with any row pitch; caches
     [rows, n_pos, kv_heads * head_dim]; pos int32 [rows]; acc float32
     [rows, kv_heads, n_pos] or None; scale None: 1 / sqrt(head_dim)."""
-    torch, device, kv, rows, n_pos, dim = _kv_caches(k_cache, v_cache, kv_heads)
+    torch, device, k_at, v_at, kv, rows, n_pos, dim = _kv_caches(k_cache, v_cache, kv_heads)
     f32 = torch.float32
     q_at, ldq = _need_rows("q", q, f32, rows, heads * dim, device)
     out_at, ldo = _need_rows("out", out, f32, rows, heads * dim, device)
     ws_at, ws_bytes = _workspace(workspace, device)
-    _check(load().attn_decode(
-        q_at, ldq, k_cache.data_ptr(), v_cache.data_ptr(), kv, rows, n_pos, heads, kv_heads, dim,
+    _check((_lib or load()).attn_decode(
+        q_at, ldq, k_at, v_at, kv, rows, n_pos, heads, kv_heads, dim,
         _need("pos", pos, torch.int32, (rows,), device), window, sinks,
         dim ** -0.5 if scale is None else scale, out_at, ldo,
         _maybe("acc", acc, f32, (rows, kv_heads, n_pos), device), ws_at, ws_bytes,
@@ -335,18 +341,18 @@ def attn_decode(q, k_cache, v_cache, pos, out, workspace, heads, kv_heads, windo
 
 
 def kv_evict_workspace(rows, kv_heads, budget) -> int:
-    return int(load().kv_evict_workspace(rows, kv_heads, budget))
+    return int((_lib or load()).kv_evict_workspace(rows, kv_heads, budget))
 
 
 def kv_evict(k_cache, v_cache, pos, acc, new_pos, new_acc, workspace, kv_heads, budget, sinks=0,
              recent=0, kept=None, stream=None):
     """Caches and acc as attn_decode; new_pos, new_acc may be pos, acc; kept
     int32 [rows, kv_heads, budget] or None."""
-    torch, device, kv, rows, n_pos, dim = _kv_caches(k_cache, v_cache, kv_heads)
+    torch, device, k_at, v_at, kv, rows, n_pos, dim = _kv_caches(k_cache, v_cache, kv_heads)
     f32, i32, weights = torch.float32, torch.int32, (rows, kv_heads, n_pos)
     ws_at, ws_bytes = _workspace(workspace, device)
-    _check(load().kv_evict(
-        k_cache.data_ptr(), v_cache.data_ptr(), kv, rows, n_pos, kv_heads, dim,
+    _check((_lib or load()).kv_evict(
+        k_at, v_at, kv, rows, n_pos, kv_heads, dim,
         _need("pos", pos, i32, (rows,), device), _need("acc", acc, f32, weights, device), budget, sinks,
         recent, _need("new_pos", new_pos, i32, (rows,), device),
         _need("new_acc", new_acc, f32, weights, device),
@@ -362,7 +368,7 @@ def head_sample(logits, u, tok, temperature=None, top_k=None, top_p=None, min_p=
     rows, n = logits.shape
     f32, i32, per_row = torch.float32, torch.int32, (rows,)
     x_at, ldl = _need_rows("logits", logits, f32, rows, n, device)
-    _check(load().head_sample(
+    _check((_lib or load()).head_sample(
         x_at, ldl, rows, n, _need("u", u, f32, per_row, device),
         _maybe("temperature", temperature, f32, per_row, device),
         _maybe("top_k", top_k, i32, per_row, device), _maybe("top_p", top_p, f32, per_row, device),

@@ -49,6 +49,8 @@ def attn(lib, **over):
     (dict(out=Q), 1), (dict(out=off(Q, 1024)), 1), (dict(out=off(K, 64)), 1), (dict(out=V), 1),
     (dict(out=POS), 1), (dict(acc=OUT), 1), (dict(acc=off(K, 16)), 1), (dict(acc=Q), 1), (dict(acc=POS), 1),
     (dict(ws=None), 7), (dict(wsb=16), 7), (dict(ws=off(WS, 8), wsb=BIG), 3),
+    (dict(ws=K, wsb=BIG), 1), (dict(ws=Q, wsb=BIG), 1), (dict(ws=off(OUT, -4096), wsb=BIG), 1),
+    (dict(ws=POS, wsb=BIG), 1), (dict(ws=ACC, acc=ACC, wsb=BIG), 1),
 ])
 def test_attn_decode_refuses(lib, over, status):
     assert attn(lib, **over) == status
@@ -75,6 +77,17 @@ def evict(lib, **over):
     return lib.kv_evict(*a.values())
 
 
+OVERLAPS = [
+    dict(v=off(K, 256)), dict(new_acc=off(ACC, 16)), dict(new_pos=off(POS, -16), rows=8), dict(new_acc=K),
+    dict(kept=V), dict(kept=ACC), dict(kept=NACC), dict(new_pos=KEPT), dict(pos=K), dict(acc=V),
+    dict(ws=K), dict(ws=NACC), dict(ws=off(KEPT, -4096)), dict(ws=POS), dict(ws=ACC), dict(ws=NPOS)]
+
+
+@pytest.mark.parametrize("over", OVERLAPS)
+def test_kv_evict_refuses_buffers_that_overlap(lib, over):
+    assert evict(lib, wsb=BIG, **over) == 1
+
+
 @pytest.mark.parametrize("over,status", [
     (dict(k=None), 1), (dict(v=None), 1), (dict(pos=None), 1), (dict(acc=None), 1), (dict(new_pos=None), 1),
     (dict(new_acc=None), 1), (dict(kv=3), 4), (dict(rows=0), 2), (dict(rows=257), 2), (dict(n_pos=0), 2),
@@ -83,9 +96,6 @@ def evict(lib, **over):
     (dict(sinks=33), 2), (dict(sinks=20, recent=13), 2), (dict(sinks=1, recent=(1 << 63) - 1), 2),
     (dict(k=off(K, 8)), 3), (dict(v=off(V, 8)), 3), (dict(pos=off(POS, 4)), 3), (dict(acc=off(ACC, 4)), 3),
     (dict(new_pos=off(NPOS, 4)), 3), (dict(new_acc=off(NACC, 4)), 3), (dict(kept=off(KEPT, 4)), 3),
-    (dict(v=off(K, 256)), 1), (dict(new_acc=off(ACC, 16)), 1), (dict(new_pos=off(POS, -16), rows=8), 1),
-    (dict(new_acc=K), 1), (dict(kept=V), 1), (dict(kept=ACC), 1), (dict(kept=NACC), 1), (dict(new_pos=KEPT), 1),
-    (dict(pos=K), 1), (dict(acc=V), 1),
     (dict(ws=None), 7), (dict(wsb=16), 7), (dict(ws=off(WS, 4), wsb=BIG), 3),
 ])
 def test_kv_evict_refuses(lib, over, status):

@@ -332,6 +332,25 @@ def test_attn_offsets_past_32_bits():
     no_error()
 
 
+@pytest.mark.parametrize("kv,heads", [("f16", 1024), ("f32", 1024)])
+def test_attn_tiles_of_several_stages(kv, heads):
+    """So many heads over so long a cache that a tile holds several stages (its count stays below 2^31)."""
+    t = torch()
+    n_pos, n, dim = (1 << 28) + 3, 3001, 8
+    k = t.empty(1, n_pos, dim, dtype=dt(kv), device="cuda")
+    v = t.empty(1, n_pos, dim, dtype=dt(kv), device="cuda")
+    g = t.Generator(device="cuda").manual_seed(1)
+    k[:, :n], v[:, :n] = (t.randn(1, n, dim, device="cuda", generator=g).to(dt(kv)) for _ in range(2))
+    q = t.randn(1, heads * dim, device="cuda", generator=g)
+    out = t.empty(1, heads * dim, device="cuda")
+    native.attn_decode(q, k, v, t.tensor([n - 1], dtype=t.int32, device="cuda"), out,
+                       native.attn_workspace(1, heads, 1, dim, n_pos), heads, 1)
+    f = lambda x: x.cpu().double().numpy()  # noqa: E731
+    want, tol, _, _ = ref.attn(f(q), f(k[:, :n]), f(v[:, :n]), [n - 1], heads, 1, -1, 0, dim ** -0.5)
+    assert np.all(np.abs(f(out) - want) <= tol)
+    no_error()
+
+
 # ---------------------------------------------------------------- kv_evict
 
 class Evict:
