@@ -362,7 +362,8 @@ size_t attn_decode_workspace(int64_t rows, int64_t heads, int64_t kv_heads, int6
  * device error 2.  1 <= budget <= n_pos, sinks + recent <= budget, other
  * limits as attn_decode.
  *   workspace: kv_evict_workspace(rows, kv_heads, budget) bytes, of any content
- *   (the first 4096 bytes stay as they are).
+ *   (the first 4096 bytes stay as they are).  Whatever is written overlaps
+ *   nothing else (Q8_ERR_ARG).
  */
 q8_status kv_evict(void* k_cache, void* v_cache, int kv_type, int64_t rows, int64_t n_pos,
                    int64_t kv_heads, int64_t head_dim, const int32_t* pos, const float* acc,

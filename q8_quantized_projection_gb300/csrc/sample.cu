@@ -460,10 +460,10 @@ struct Row {
 // top reaches rough_need in the cut's bin; need_of(sum of all f): the sum that
 // the cut reaches; scale: bins a unit of M - x.  False: not found this way.
 // True: above and above_n are this thread's f and number of the tokens in bins
-// before the cut's, cut_bin.
+// before the cut's; s.mine lists this CTA's in the cut's.
 template <bool RES, typename F, typename R, typename P>
 __device__ __forceinline__ bool cut_by_bins(Row<RES>& row, const Weights& w, float scale, F f, R rough, u64 rough_need,
-                                            P need_of, Cut* cut, u64* above, uint32_t* above_n, int* cut_bin) {
+                                            P need_of, Cut* cut, u64* above, uint32_t* above_n) {
     cg::cluster_group cl = cg::this_cluster();
     Shared& s = sh();
     const int tid = threadIdx.x;
@@ -568,7 +568,6 @@ __device__ __forceinline__ bool cut_by_bins(Row<RES>& row, const Weights& w, flo
         *cut = {s.cut_x, s.cut_i};
         *above = v.b;
         *above_n = v.e;
-        *cut_bin = B;
         return true;
     }
     return false;
@@ -842,15 +841,12 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
     Cut cut{-FLT_MAX, 0xffffffffu};      // everything above -inf
     u64 above = 0;
     uint32_t above_n = 0;
-    int cut_bin = 0;
     if (by_k) {
         const auto counted = [&](float x, uint32_t) { return uint32_t(x > -INFINITY); };
-        if (!cut_by_bins(row, w, k_scale, counted, counted, u64(k), [&](u64) { return u64(k); }, &cut, &above, &above_n,
-                         &cut_bin))
+        if (!cut_by_bins(row, w, k_scale, counted, counted, u64(k), [&](u64) { return u64(k); }, &cut, &above, &above_n))
             cut = row.search(top, counted, u64(k), [&](u64 sum, u64) { return u64(k) - sum; });
     }
-    bool summed = false;                 // above, above_n, cut_bin are the kept weights' before the cut's bin
-    float scale = 0.0f;
+    bool summed = false;                 // above, above_n are the kept weights' before the cut's bin
     if (p < 1.0f) {
         // bins hold masses in units of 2^-31 of the sum, by its estimate
         float est = 0.0f;
@@ -865,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
         // tokens of less than (1 - p) S / N hold less than the share 1 - p
         // together, so the nucleus ends above them: the bins stop there
         const float least = (1.0f - p) * S / float(all.e) * 0.99f;
-        scale = bins_over(-log2f(least) / w.ch);
+        const float scale = bins_over(-log2f(least) / w.ch);
         // (the weight of -inf is 0: without a cut before, every logit may be asked)
         const auto f = [&](float x, uint32_t i) {
             const u64 wx = w(x);
@@ -877,8 +873,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
         };
         u64 need = 0;
         const auto need_of = [&](u64 sum) { return need = share(p, sum, true); };
-        summed = cut_by_bins(row, w, scale, f, rough, u64(share(p, u64(1) << 31, true)), need_of, &cut, &above, &above_n,
-                             &cut_bin);
+        summed = cut_by_bins(row, w, scale, f, rough, u64(share(p, u64(1) << 31, true)), need_of, &cut, &above, &above_n);
         if (!summed)
             // (`need` is of the exact sum by now) the fewest ties that reach the mass
             cut = row.search(top, f, need, [&](u64 sum, u64 tie) { return (need - sum + tie - 1) / tie; });
@@ -891,18 +886,20 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
         return cut.has(x, i) && wx >= floor_w ? wx : 0;
     };
     v = Slot();
-    if (summed && floor_w == 0) {
+    if (summed && floor_w == 0 && u > 0.0f) {
+        // what lies above the cut's bin is summed; of that bin's list, each warp
+        // takes the tokens of its own part
         v.a = above;
         v.e = above_n;
-        row.each([&](float x, uint32_t i) {
-            if (cut.has(x, i)) {
-                if (w.rough(x) > 0.0f) v.d = min(v.d, i);
-                if (w.bin(x, scale) == cut_bin) {
-                    v.a += w(x);
-                    ++v.e;
-                }
+        const uint32_t first = base + (tid >> 5) * of_warp;
+        for (uint32_t j = lane; j < s.listed; j += 32) {
+            const float x = list_x(s.mine[j]);
+            const uint32_t i = list_i(s.mine[j]);
+            if (i - first < of_warp && cut.has(x, i)) {
+                v.a += w(x);
+                ++v.e;
             }
-        });
+        }
     } else {
         row.each([&](float x, uint32_t i) {
             const u64 wx = w(x);
