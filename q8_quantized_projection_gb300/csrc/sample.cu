@@ -57,13 +57,15 @@ constexpr int kShort = 128;                 // a longer list is cut by a histogr
 typedef unsigned long long u64;
 
 // What the CTAs of a cluster exchange: sums a, b, g, e and e2, the largest c
-// and c2, the smallest d.  A slot a CTA, two sets used in turn, so that a slot
+// and c2, the smallest d; s: a sum of weights as a float, of which a logit of
+// key c weighs 1 (0: none).  A slot a CTA, two sets used in turn, so that a slot
 // is written again only after a barrier behind its last reader.
 struct Slot {
     u64 a = 0, b = 0, g = 0;
     uint32_t e = 0, e2 = 0, c = 0, c2 = 0, d = 0xffffffffu;
+    float s = 0.0f;
 };
-enum { kA = 1, kB = 2, kG = 4, kE = 8, kE2 = 16, kC = 32, kC2 = 64, kD = 128 };
+enum { kA = 1, kB = 2, kG = 4, kE = 8, kE2 = 16, kC = 32, kC2 = 64, kD = 128, kS = 256 };
 
 struct Shared {
     Slot slot[2][kMaxCluster];
@@ -96,6 +98,12 @@ __device__ __forceinline__ uint32_t logit_key(float x) {
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+__device__ __forceinline__ float exp2_rough(float y) {      // to about 2^-22; 0 below 2^-126
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+    return r;
 }
 
 // 2^(j/64) in units of 2^-31.
@@ -157,9 +165,7 @@ struct Weights {
     }
     // 2^y to about 2^-21, for the histogram; 0 below 2^-126
     __device__ __forceinline__ float rough(float x) const {
-        float r;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((x * pre - M) * ch));
-        return r;
+        return exp2_rough((x * pre - M) * ch);
     }
 };
 
@@ -221,14 +227,22 @@ __device__ __noinline__ u64 block_scan(u64 v, u64* all) {
     return (warp ? before : 0) + up - v;
 }
 
+// (c: the exponent's factor, for s)
 template <int F>
-__device__ __forceinline__ void warp_reduce(Slot& v) {
+__device__ __forceinline__ void warp_reduce(Slot& v, float c = 0.0f) {
+    if constexpr (F & kS) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, v.c);
+        v.s = v.c == top ? v.s : v.c ? v.s * exp2_rough((key_logit(v.c) - key_logit(top)) * c) : 0.0f;
+        v.c = top;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) v.s += __shfl_xor_sync(0xffffffffu, v.s, d);
+    }
     if constexpr (F & kA) v.a = warp_sum(v.a);
     if constexpr (F & kB) v.b = warp_sum(v.b);
     if constexpr (F & kG) v.g = warp_sum(v.g);
     if constexpr (F & kE) v.e = __reduce_add_sync(0xffffffffu, v.e);
     if constexpr (F & kE2) v.e2 = __reduce_add_sync(0xffffffffu, v.e2);
-    if constexpr (F & kC) v.c = __reduce_max_sync(0xffffffffu, v.c);
+    if constexpr ((F & kC) && !(F & kS)) v.c = __reduce_max_sync(0xffffffffu, v.c);
     if constexpr (F & kC2) v.c2 = __reduce_max_sync(0xffffffffu, v.c2);
     if constexpr (F & kD) v.d = __reduce_min_sync(0xffffffffu, v.d);
 }
@@ -236,12 +250,12 @@ __device__ __forceinline__ void warp_reduce(Slot& v) {
 // The fields F of every thread's Slot over the cluster as one; before (if
 // given) receives the sum of a over the CTAs before this one.
 template <int F>
-__device__ __forceinline__ Slot exchange(Slot v, int& phase, u64* before = nullptr) {
+__device__ __forceinline__ Slot exchange(Slot v, int& phase, u64* before = nullptr, float c = 0.0f) {
     Shared& s = sh();
     cg::cluster_group cl = cg::this_cluster();
     const unsigned rank = cl.block_rank(), size = cl.num_blocks();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    warp_reduce<F>(v);
+    warp_reduce<F>(v, c);
     if (lane == 0) s.warp[warp] = v;
     __syncthreads();
     Slot* const slots = s.slot[phase];
@@ -249,14 +263,14 @@ __device__ __forceinline__ Slot exchange(Slot v, int& phase, u64* before = nullp
     if (warp == 0) {
         v = Slot();
         if (lane < kWarpsN) v = s.warp[lane];
-        warp_reduce<F>(v);
+        warp_reduce<F>(v, c);
         if (lane < int(size)) *cl.map_shared_rank(&slots[rank], lane) = v;
     }
     cluster_sync(size);
     v = Slot();
     if (lane < int(size)) v = slots[lane];
     if (before) *before = warp_sum(lane < int(rank) ? v.a : 0);
-    warp_reduce<F>(v);
+    warp_reduce<F>(v, c);
     return v;
 }
 
@@ -700,11 +714,39 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
     const uint32_t n = base < N ? min(uint32_t(part), N - base) : 0;
     const float* gx = a.x + m * a.ldx + base;
     Row<RES> row{gx, base, n, part / kPart, rank, size, 0};
+    const uint32_t of_warp = uint32_t(row.tiles) * kTile;      // tokens of a warp
+
+    // Seen once while they are loaded: the largest and the smallest that can be
+    // drawn, how many can, and for the nucleus of the whole row the sum of their
+    // weights (a lane's in units of its own largest).
+    const bool early = p < 1.0f && k <= 0 && T <= 1e30f;       // (T: so that no difference overflows but to weight 0)
+    const float early_c = __fdividef(1.44269502f, T);
+    float best = -INFINITY, least = INFINITY, est = 0.0f;
+    uint32_t some = 0;
+    const auto look = [&](float4 q, uint32_t) {
+        const float x[4] = {q.x, q.y, q.z, q.w};
+        const float now = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), best);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (x[j] > -INFINITY) {
+                least = fminf(least, x[j]);
+                ++some;
+            }
+        if (early) {
+            if (now > best) est = best > -INFINITY ? est * exp2_rough((best - now) * early_c) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (x[j] > -INFINITY) est += exp2_rough((x[j] - now) * early_c);
+        }
+        best = now;
+    };
     if constexpr (RES) {
         float* x = sh_x();
         if ((reinterpret_cast<uintptr_t>(gx) & 15) == 0) {
+            // each warp its own tiles
+            const int end = (tid >> 5) * int(of_warp) + int(of_warp);
 #pragma unroll 8
-            for (int e = tid * 4; e < part; e += kThreads * 4) {
+            for (int e = end - int(of_warp) + lane * 4; e < end; e += kTile) {
                 float4 v;
                 if (e + 3 < int(n)) {
                     v = __ldg(reinterpret_cast<const float4*>(gx + e));
@@ -714,8 +756,11 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
                     v.z = e + 2 < int(n) ? __ldg(gx + e + 2) : -INFINITY;
                     v.w = -INFINITY;
                 }
-                *reinterpret_cast<float4*>(x + e) = make_float4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+                v = make_float4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+                *reinterpret_cast<float4*>(x + e) = v;
+                look(v, 0);
             }
+            __syncthreads();
         } else {
             // a row that begins off a 16-byte boundary: whole words, stored a float at
             // a time (behind the first row only, so the word before it is the row before's)
@@ -734,24 +779,21 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
                 for (int j = 0; j < 4; ++j)
                     if (e + j >= 0 && e + j < part) x[e + j] = clean(f[j]);
             }
+            __syncthreads();
+            row.quads(look);
         }
-        __syncthreads();
+    } else {
+        row.quads(look);
     }
-
-    // the largest and the smallest that can be drawn, and how many can
     Slot v;
-    float best = -INFINITY;
-    row.each([&](float x, uint32_t) {
-        best = fmaxf(best, x);
-        const uint32_t key = logit_key(x);
-        v.d = min(v.d, key - 1);               // (0, never drawn: the largest)
-        v.e += key != 0;
-    });
     v.c = logit_key(best);
+    v.d = least < INFINITY ? logit_key(least) - 1 : 0xffffffffu;
+    v.e = some;
+    v.s = est;
     // with top-k: a logit that at least k reach, from the lanes' maxima: the
     // q-th largest of each full warp, the smallest of those over the warps
     uint32_t reach = 0xffffffffu;
-    const uint32_t of_warp = uint32_t(row.tiles) * kTile, full = N / of_warp;     // warps whose logits all exist
+    const uint32_t full = N / of_warp;      // warps whose logits all exist
     const uint32_t q = k > 0 && full ? (uint32_t(k) + full - 1) / full : 0;
     if (q >= 1 && q <= 32 && base / of_warp + (tid >> 5) < full) {
         uint32_t key = v.c;
@@ -764,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
     }
     v.c2 = ~reach;
     cluster_sync(size);      // every CTA has begun before another writes to it
-    const Slot all = exchange<kE | kC | kC2 | kD>(v, row.phase);
+    const Slot all = exchange<kE | kC | kC2 | kD | kS>(v, row.phase, nullptr, early_c);
     const uint32_t top = all.c, low = all.d + 1;
     reach = ~all.c2;
     if (top == 0) {
@@ -849,19 +891,22 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
     bool summed = false;                 // above, above_n are the kept weights' before the cut's bin
     if (p < 1.0f) {
         // bins hold masses in units of 2^-31 of the sum, by its estimate
-        float est = 0.0f;
         const Cut before = cut;
-        row.each([&](float x, uint32_t i) {
-            if (before.has(x, i)) est += w.rough(x);
-        });
-        v = Slot();
-        v.a = u64(est * 16777216.0f);
-        const float S = float(exchange<kA>(v, row.phase).a) * 0x1p-24f;      // at least 1: M itself
+        float S = all.s;                 // at least 1: M itself
+        if (!early) {
+            est = 0.0f;
+            row.each([&](float x, uint32_t i) {
+                if (before.has(x, i)) est += w.rough(x);
+            });
+            v = Slot();
+            v.a = u64(est * 16777216.0f);
+            S = float(exchange<kA>(v, row.phase).a) * 0x1p-24f;
+        }
         const float unit = 2147483648.0f / S;
         // tokens of less than (1 - p) S / N hold less than the share 1 - p
         // together, so the nucleus ends above them: the bins stop there
-        const float least = (1.0f - p) * S / float(all.e) * 0.99f;
-        const float scale = bins_over(-log2f(least) / w.ch);
+        const float lowest = (1.0f - p) * S / float(all.e) * 0.99f;
+        const float scale = bins_over(-log2f(lowest) / w.ch);
         // (the weight of -inf is 0: without a cut before, every logit may be asked)
         const auto f = [&](float x, uint32_t i) {
             const u64 wx = w(x);
