@@ -139,13 +139,16 @@ __device__ __forceinline__ void named_bar(int id, int count) {
 // A barrier over a cluster's threads that publishes their shared memory; over
 // the CTA's alone in a cluster of one (measured: 0.4 against 1.8 thousand
 // cycles).  Every thread calls it with the cluster's size.
+__device__ __forceinline__ void cluster_arrive(unsigned size) {
+    if (size > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait(unsigned size) {
+    if (size > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    else __syncthreads();
+}
 __device__ __forceinline__ void cluster_sync(unsigned size) {
-    if (size > 1) {
-        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-    } else {
-        __syncthreads();
-    }
+    cluster_arrive(size);
+    cluster_wait(size);
 }
 
 // ---------------------------------------------- programmatic dependent launch

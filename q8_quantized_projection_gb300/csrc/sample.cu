@@ -53,6 +53,7 @@ constexpr int kTile = 128;                  // logits a warp takes at a time, fo
 constexpr int kPart = kWarpsN * kTile;      // a CTA's part is a multiple of this
 constexpr int kMaxPart = 46 * 1024;         // logits of a part held in shared memory
 constexpr int kBins = 1024, kList = 2048, kMaxCluster = 8;
+constexpr uint32_t kPairs = kBins / 2, kPairsOne = 128;   // lists up to these are compared pair by pair (one CTA a row)
 constexpr int kShort = 128;                 // a longer list is cut by a histogram before it is sorted
 typedef unsigned long long u64;
 
@@ -160,8 +161,9 @@ struct Weights {
     }
     // the histogram's bin: (M - x) * scale, the last one for all that lies lower
     __device__ __forceinline__ int bin(float x, float scale) const {
-        const float y = depth(x, scale);
-        return y < float(kBins - 1) ? int(y) : kBins - 1;
+        // (added to 2^23 rounded down: whole units; a quarter of the time of a conversion)
+        const float y = fminf(depth(x, scale), float(kBins - 1));
+        return __float_as_int(__fadd_rd(y, 8388608.0f)) - 0x4b000000;
     }
     // 2^y to about 2^-21, for the histogram; 0 below 2^-126
     __device__ __forceinline__ float rough(float x) const {
@@ -380,17 +382,20 @@ struct Row {
             }
         return true;
     }
-    // First CTA, behind the exchange (of e2: tokens listed) that ended the
-    // listing: the parts as one list of n <= kList tokens.  The other CTAs keep
-    // theirs until the next barrier.
-    __device__ __forceinline__ void gather(uint32_t n) {
+    // Behind the exchange (of e2: tokens listed) that ended the listing: the
+    // parts as one list of n <= kList tokens, got(place, token) for each.  The
+    // CTAs keep their parts until the next barrier.
+    template <typename G>
+    __device__ __forceinline__ void gather(uint32_t n, G got) {
         Shared& s = sh();
         cg::cluster_group cl = cg::this_cluster();
         for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
             uint32_t at = i;
             unsigned r = 0;
             for (; r + 1 < size && at >= s.slot[phase ^ 1][r].e2; ++r) at -= s.slot[phase ^ 1][r].e2;
-            s.list[i] = cl.map_shared_rank(s.mine, r)[at];
+            const u64 t = cl.map_shared_rank(s.mine, r)[at];
+            s.list[i] = t;
+            got(i, t);
         }
         __syncthreads();
     }
@@ -401,22 +406,25 @@ struct Row {
     template <typename W>
     __device__ __forceinline__ uint32_t pick(u64 e, u64 before, W w) {
         Shared& s = sh();
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         u64 run = before;
-        for (int k = 0; k < warp; ++k) run += s.warp[k].a;
-        if (run < e && run + s.warp[warp].a >= e) {
-#pragma unroll 1
-            for (int k = 0; k < tiles; ++k) {
-                const uint32_t el = (warp * tiles + k) * kTile + lane * 4, i = base + el;
-                const float4 v = quad(el);
-                const u64 w0 = w(v.x, i), w1 = w0 + w(v.y, i + 1), w2 = w1 + w(v.z, i + 2), w3 = w2 + w(v.w, i + 3);
-                const u64 sum = warp_sum(w3);
+        int k = 0;       // the warp whose tokens hold it, if one of this CTA's does
+        while (k < kWarpsN && run + s.warp[k].a < e) run += s.warp[k++].a;
+        if (run < e && k < kWarpsN) {
+            const uint32_t of_warp = uint32_t(tiles) * kTile;
+            // that warp's tokens, over the whole CTA
+            for (uint32_t at0 = 0; at0 < of_warp; at0 += kThreads * 4) {
+                const uint32_t at = at0 + threadIdx.x * 4, el = k * of_warp + at, i = base + el;
+                u64 w0 = 0, w1 = 0, w2 = 0, w3 = 0, sum;
+                if (at < of_warp) {
+                    const float4 v = quad(el);
+                    w0 = w(v.x, i), w1 = w0 + w(v.y, i + 1), w2 = w1 + w(v.z, i + 2), w3 = w2 + w(v.w, i + 3);
+                }
+                const u64 lo = run + block_scan(w3, &sum);
                 if (run + sum < e) {
                     run += sum;
                     continue;
                 }
-                const u64 up = run + warp_scan(w3), lo = up - w3;
-                if (lo < e && up >= e) {
+                if (lo < e && lo + w3 >= e) {
                     const uint32_t hit = lo + w0 >= e ? 0 : lo + w1 >= e ? 1 : lo + w2 >= e ? 2 : 3;
                     cg::cluster_group cl = cg::this_cluster();
                     for (unsigned r = 0; r < size; ++r) *cl.map_shared_rank(&s.found, r) = i + hit;
@@ -473,11 +481,12 @@ struct Row {
 // not among the tokens); rough(x, i): f for the histogram, whose sum from the
 // top reaches rough_need in the cut's bin; need_of(sum of all f): the sum that
 // the cut reaches; scale: bins a unit of M - x.  False: not found this way.
-// True: above and above_n are this thread's f and number of the tokens in bins
-// before the cut's; s.mine lists this CTA's in the cut's.
+// True: s.cut_x and s.cut_i hold the cut behind the next cluster barrier, and
+// kept and kept_n are a thread's part of the sum and number of the tokens that
+// it keeps (summed over a warp: those of its own part of the row).
 template <bool RES, typename F, typename R, typename P>
 __device__ __forceinline__ bool cut_by_bins(Row<RES>& row, const Weights& w, float scale, F f, R rough, u64 rough_need,
-                                            P need_of, Cut* cut, u64* above, uint32_t* above_n) {
+                                            P need_of, u64* kept, uint32_t* kept_n) {
     cg::cluster_group cl = cg::this_cluster();
     Shared& s = sh();
     const int tid = threadIdx.x;
@@ -558,30 +567,75 @@ __device__ __forceinline__ bool cut_by_bins(Row<RES>& row, const Weights& w, flo
             continue;
         }
         if (all.e2 > kList) return false;
-        if (row.rank == 0) {
-            const int n = int(all.e2);
-            row.gather(all.e2);
-            sort_down(s.list, n);
-            // the first place whose sum, itself included, is enough
-            const int per = (n + kThreads - 1) / kThreads, at0 = tid * per, at1 = min(at0 + per, n);
-            u64 part = 0, sum;
-            for (int j = at0; j < at1; ++j) part += f(list_x(s.list[j]), list_i(s.list[j]));
-            u64 run = all.b + block_scan(part, &sum);
-            for (int j = at0; j < at1; ++j) {
-                const u64 fx = f(list_x(s.list[j]), list_i(s.list[j]));
-                if (run < need && run + fx >= need) {
-                    for (unsigned r = 0; r < row.size; ++r) {
-                        *cl.map_shared_rank(&s.cut_x, r) = list_x(s.list[j]);
-                        *cl.map_shared_rank(&s.cut_i, r) = list_i(s.list[j]);
-                    }
+        const uint32_t n = all.e2;
+        const int lane = tid & 31, warp = tid >> 5;
+        const uint32_t of_warp = uint32_t(row.tiles) * kTile;
+        if (n <= (row.size == 1 ? kPairsOne : kPairs)) {
+            // every CTA takes the whole list; a token of its own is kept if what
+            // goes before it falls short, and is the cut if it makes that up
+            u64* const fs = reinterpret_cast<u64*>(s.hist);
+            if (tid < kWarpsN) s.scan[tid] = 0;
+            row.gather(n, [&](uint32_t i, u64 t) { fs[i] = f(list_x(t), list_i(t)); });
+            // eight lanes a token
+            const uint32_t own = s.listed, sub = lane & 7;
+            for (uint32_t j0 = 0; j0 < own; j0 += kThreads / 8) {
+                const uint32_t j = j0 + tid / 8;
+                const u64 t = j < own ? s.mine[j] : ~u64(0);
+                u64 sum = 0;
+#pragma unroll 4
+                for (uint32_t i = sub; i < n; i += 8) sum += s.list[i] > t ? fs[i] : 0;
+#pragma unroll
+                for (int d = 4; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                sum += all.b;
+                if (sub == 0 && j < own && sum < need) {
+                    const float x = list_x(t);
+                    const uint32_t at = list_i(t);
+                    const u64 fx = f(x, at);
+                    atomicAdd(&s.scan[(at - row.base) / of_warp], fx);
+                    ++v.e;
+                    if (sum + fx >= need)
+                        for (unsigned r = 0; r < row.size; ++r) {
+                            *cl.map_shared_rank(&s.cut_x, r) = x;
+                            *cl.map_shared_rank(&s.cut_i, r) = at;
+                        }
                 }
-                run += fx;
+            }
+            __syncthreads();
+            if (lane == 0) v.b += s.scan[warp];
+        } else {
+            if (row.rank == 0) {
+                row.gather(n, [](uint32_t, u64) {});
+                sort_down(s.list, int(n));
+                // the first place whose sum, itself included, is enough
+                const int per = (n + kThreads - 1) / kThreads, at0 = tid * per, at1 = min(at0 + per, int(n));
+                u64 part = 0, sum;
+                for (int j = at0; j < at1; ++j) part += f(list_x(s.list[j]), list_i(s.list[j]));
+                u64 run = all.b + block_scan(part, &sum);
+                for (int j = at0; j < at1; ++j) {
+                    const u64 fx = f(list_x(s.list[j]), list_i(s.list[j]));
+                    if (run < need && run + fx >= need) {
+                        for (unsigned r = 0; r < row.size; ++r) {
+                            *cl.map_shared_rank(&s.cut_x, r) = list_x(s.list[j]);
+                            *cl.map_shared_rank(&s.cut_i, r) = list_i(s.list[j]);
+                        }
+                    }
+                    run += fx;
+                }
+            }
+            cluster_sync(row.size);
+            const Cut cut{s.cut_x, s.cut_i};
+            const uint32_t first = row.base + warp * of_warp;
+            for (uint32_t j = lane; j < s.listed; j += 32) {
+                const float x = list_x(s.mine[j]);
+                const uint32_t i = list_i(s.mine[j]);
+                if (i - first < of_warp && cut.has(x, i)) {
+                    v.b += f(x, i);
+                    ++v.e;
+                }
             }
         }
-        cluster_sync(row.size);
-        *cut = {s.cut_x, s.cut_i};
-        *above = v.b;
-        *above_n = v.e;
+        *kept = v.b;
+        *kept_n = v.e;
         return true;
     }
     return false;
@@ -709,6 +763,8 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
         return;
     }
 
+    cluster_arrive(size);    // (waited for below: every CTA has begun before another writes to it)
+
     // the part: [base, base + n) of the row
     const uint32_t base = rank * uint32_t(part), N = uint32_t(a.N);
     const uint32_t n = base < N ? min(uint32_t(part), N - base) : 0;
@@ -805,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
         reach = __reduce_max_sync(0xffffffffu, key);
     }
     v.c2 = ~reach;
-    cluster_sync(size);      // every CTA has begun before another writes to it
+    cluster_wait(size);
     const Slot all = exchange<kE | kC | kC2 | kD | kS>(v, row.phase, nullptr, early_c);
     const uint32_t top = all.c, low = all.d + 1;
     reach = ~all.c2;
@@ -869,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
         const uint32_t listed = exchange<kE2>(v, row.phase).e2;
         if (listed <= kList) {
             if (rank == 0) {
-                row.gather(listed);
+                row.gather(listed, [](uint32_t, u64) {});
                 uint32_t tok, kept;
                 u64 S;
                 draw_from_list(w, set, int(listed), k_scale, &tok, &S, &kept);
@@ -881,14 +937,20 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
     }
 
     Cut cut{-FLT_MAX, 0xffffffffu};      // everything above -inf
-    u64 above = 0;
-    uint32_t above_n = 0;
+    const auto cut_found = [&] {
+        cluster_sync(size);
+        cut = {s.cut_x, s.cut_i};
+    };
+    u64 kept = 0;
+    uint32_t kept_n = 0;
     if (by_k) {
         const auto counted = [&](float x, uint32_t) { return uint32_t(x > -INFINITY); };
-        if (!cut_by_bins(row, w, k_scale, counted, counted, u64(k), [&](u64) { return u64(k); }, &cut, &above, &above_n))
+        if (cut_by_bins(row, w, k_scale, counted, counted, u64(k), [&](u64) { return u64(k); }, &kept, &kept_n))
+            cut_found();
+        else
             cut = row.search(top, counted, u64(k), [&](u64 sum, u64) { return u64(k) - sum; });
     }
-    bool summed = false;                 // above, above_n are the kept weights' before the cut's bin
+    bool summed = false;                 // kept, kept_n are the nucleus's
     if (p < 1.0f) {
         // bins hold masses in units of 2^-31 of the sum, by its estimate
         const Cut before = cut;
@@ -918,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
         };
         u64 need = 0;
         const auto need_of = [&](u64 sum) { return need = share(p, sum, true); };
-        summed = cut_by_bins(row, w, scale, f, rough, u64(share(p, u64(1) << 31, true)), need_of, &cut, &above, &above_n);
+        summed = cut_by_bins(row, w, scale, f, rough, u64(share(p, u64(1) << 31, true)), need_of, &kept, &kept_n);
         if (!summed)
             // (`need` is of the exact sum by now) the fewest ties that reach the mass
             cut = row.search(top, f, need, [&](u64 sum, u64 tie) { return (need - sum + tie - 1) / tie; });
@@ -931,21 +993,12 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
         return cut.has(x, i) && wx >= floor_w ? wx : 0;
     };
     v = Slot();
-    if (summed && floor_w == 0 && u > 0.0f) {
-        // what lies above the cut's bin is summed; of that bin's list, each warp
-        // takes the tokens of its own part
-        v.a = above;
-        v.e = above_n;
-        const uint32_t first = base + (tid >> 5) * of_warp;
-        for (uint32_t j = lane; j < s.listed; j += 32) {
-            const float x = list_x(s.mine[j]);
-            const uint32_t i = list_i(s.mine[j]);
-            if (i - first < of_warp && cut.has(x, i)) {
-                v.a += w(x);
-                ++v.e;
-            }
-        }
+    const bool whole = summed && floor_w == 0 && u > 0.0f;
+    if (whole) {
+        v.a = kept;
+        v.e = kept_n;
     } else {
+        if (summed) cut_found();
         row.each([&](float x, uint32_t i) {
             const u64 wx = w(x);
             const bool in = cut.has(x, i) && wx >= floor_w;
@@ -956,6 +1009,7 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
     }
     u64 before;
     const Slot fin = exchange<kA | kE | kD>(v, row.phase, &before);
+    if (whole) cut = {s.cut_x, s.cut_i};
     uint32_t tok = fin.d;
     if (u > 0.0f) {
         // the first sum above u * S
