@@ -558,6 +558,23 @@ def test_sample_few_levels():
     check_draw(x, u, k=[500, 3000, 0, 100, 30000, 10], p=[0.9, 0.5, 0.95, 0.99, 0.8, 0.3], mp=[0.0, 0.01, 0.1, 0.05, 0.0, 0.2])
 
 
+@pytest.mark.parametrize("n", [1900, 15000, 40000])
+@pytest.mark.parametrize("many", [60, 300, 1000, 2000])
+@pytest.mark.parametrize("sort", [False, True])
+def test_sample_cuts_among_equal_logits(n, many, sort):
+    """Equal logits by tens to thousands where the cut falls, scattered and side by side."""
+    t = torch()
+    g = t.Generator(device="cuda").manual_seed(n + many)
+    x = (t.rand(6, n, device="cuda", generator=g) * (n / many)).floor() * (4.0 * many / n)
+    if sort:
+        x = x.sort(dim=1, descending=True).values.contiguous()
+    u = [0.0, 0.317, 0.513, 0.0, 0.913, 0.9917]
+    p = [0.117, 0.317, 0.517, 0.717, 0.917, 0.9917]
+    check_draw(x, u, p=p)
+    check_draw(x, u, p=p, mp=[0.0, 0.1, 0.01, 0.2, 0.0, 0.3], t=[1.0, 2.0, 0.5, 1.5, 3.0, 1.0])
+    check_draw(x, u, k=[1700, 1234, 1500, 1801, 1111, 1899], p=p)
+
+
 def test_sample_shares_next_to_a_border():
     """Nuclei that end a few steps of binary32 beside a token's border, tokens far apart."""
     t = torch()
