@@ -470,10 +470,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     // CTA c has tiles [first(c), first(c + 1)): all of them in equal shares, the
     // first ones one longer.  Small problems: a tile or two a CTA (fewer cost more
     // to join than they save; one where a tile is fewer bytes and more work), or a
-    // unit.
+    // unit.  Few units: of T tiles cut in P parts, one CTA's tiles take T / P and
+    // the join P, so P grows with the root of T (one row's K/V head with 8 query
+    // heads, on all CTAs and so: 48000 bf16 entries of 128 values 67 and 28 us, 3408
+    // f32 entries of 80 values 34 and 16 us; factors of 2 to 20 tried).
     const uint32_t real = s_pre[rows], units = uint32_t(rows) * per_row;
     const uint32_t extra = real >= 4 * gridDim.x ? T::EXTRA : 1, W = real + extra * units;
-    const uint32_t ctas = min(max(real / T::LEAST, units), gridDim.x), cta = blockIdx.x;
+    constexpr float ROOT = NG * T::DMAX > 512 ? 5.0f : 8.0f;
+    const uint32_t best = uint32_t(__fsqrt_rn(ROOT * float(real) * float(units)));
+    const uint32_t ctas = min(max(min(real / T::LEAST, best), units), gridDim.x), cta = blockIdx.x;
     __syncthreads();
     for (int i = tid; i <= rows; i += kAttnThreads) s_pre[i] += extra * i * per_row;
     __syncthreads();
@@ -577,7 +582,25 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                 const auto state = [&](int i, int g) {      // reference and sum of part i
                     return __ldcg(reinterpret_cast<const float2*>(from(i) + NG * D + 2 * g));
                 };
-                float* s_f = reinterpret_cast<float*>(ring_all);   // (the states there have been read)
+                // (the states in the ring have been read) the factors, then as many
+                // parts' o at a time as fit, copied by all threads: one CTA's plain
+                // loads in turn would be the time of a unit that many share
+                float* const s_f = reinterpret_cast<float*>(ring_all);
+                constexpr int FACTORS = kAttnMaxCtas * NG * 4;
+                constexpr int FIT = (kAttnWarps * kAttnRing - FACTORS) / (NG * T::DMAX * 4);
+                const float4* const s_x = reinterpret_cast<const float4*>(ring_all + FACTORS);
+                const int E = ng * D4;
+                const auto fetch = [&](int i0) {
+                    const int end = min(i0 + FIT, n);
+                    for (int i = i0 + warp; i < end; i += kAttnWarps) {
+                        const float* src = from(i);
+                        const uint32_t dst = smem_u32(s_x + (i - i0) * E);
+#pragma unroll 4
+                        for (int e = lane; e < E; e += 32) cp16(dst + 16 * e, src + 4 * e, true);
+                    }
+                    cp_commit();
+                };
+                fetch(0);
                 // one warp a query head: factors 2^(r_i - r), the sum and 1 / sum
                 for (int g = warp; g < ng; g += kAttnWarps) {
                     const float2 mine = lane < n ? state(lane, g) : make_float2(-INFINITY, 0.0f);
@@ -598,32 +621,58 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                         if (p.ml) p.ml[int64_t(m) * a.heads + g0 + g] = make_float2(top, 1.0f / sum);
                     }
                 }
-                __syncthreads();
-                for (int e = tid; e < ng * D4; e += kAttnThreads) {
-                    const int g = e / D4, d = (e - g * D4) * 4;
-                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    constexpr int AHEAD = 8;                       // parts in flight
-                    for (int i0 = 0; i0 < n; i0 += AHEAD) {
-                        float4 x[AHEAD];
+                // where there are at most half as many float4 as threads, several threads
+                // share one, each every share-th part
+                constexpr int NE = (NG * T::DMAX / 4 + kAttnThreads - 1) / kAttnThreads;
+                const int bits = E <= kAttnThreads / 2 ? 32 - __clz(E - 1) : 31;    // (E >= 2)
+                const int share = E <= kAttnThreads / 2 ? kAttnThreads >> bits : 1, sub = tid >> bits;
+                const int mine = tid - (sub << bits);
+                float4 v[NE];
 #pragma unroll
-                        for (int i = 0; i < AHEAD; ++i)
-                            if (i0 + i < n) x[i] = __ldcg(reinterpret_cast<const float4*>(from(i0 + i) + g * D + d));
+                for (int j = 0; j < NE; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int i0 = 0; i0 < n; i0 += FIT) {
+                    if (i0) fetch(i0);
+                    cp_wait<0>();
+                    __syncthreads();
+                    const int end = min(FIT, n - i0);
 #pragma unroll
-                        for (int i = 0; i < AHEAD; ++i)
-                            if (i0 + i < n) {
-                                const float f = s_f[(i0 + i) * NG + g];
-                                v.x += x[i].x * f, v.y += x[i].y * f, v.z += x[i].z * f, v.w += x[i].w * f;
-                            }
+                    for (int j = 0; j < NE; ++j) {
+                        const int e = mine + j * kAttnThreads;
+                        if (e >= E) continue;
+                        const int g = e / D4;
+#pragma unroll 4
+                        for (int i = sub; i < end; i += share) {
+                            const float4 x = s_x[i * E + e];
+                            const float f = s_f[(i0 + i) * NG + g];
+                            v[j].x += x.x * f, v[j].y += x.y * f, v[j].z += x.z * f, v[j].w += x.w * f;
+                        }
                     }
-                    put(g, d, v, s_l[0][g], true);
+                    __syncthreads();
+                }
+                if (share > 1) {
+                    float4* const s_v = reinterpret_cast<float4*>(ring_all + FACTORS);
+                    s_v[tid] = v[0];
+                    __syncthreads();
+                    for (int k = 1; tid < E && k < share; ++k) {
+                        const float4 x = s_v[tid + (k << bits)];
+                        v[0].x += x.x, v[0].y += x.y, v[0].z += x.z, v[0].w += x.w;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < NE; ++j) {
+                    const int e = tid + j * kAttnThreads;
+                    if (e < E) put(e / D4, e % D4 * 4, v[j], s_l[0][e / D4], true);
+                }
+                if (D < T::DMAX) {     // values behind D are zero again
+                    __syncthreads();
+                    for (int i = tid; i < kAttnWarps * kAttnRing / 16; i += kAttnThreads)
+                        reinterpret_cast<int4*>(ring_all)[i] = int4{0, 0, 0, 0};
                 }
             }
         }
         __syncthreads();
-        if (D < T::DMAX) {   // the states (and factors) overwrote values behind D
-            constexpr int DIRTY = NG * (T::DMAX > kAttnMaxCtas ? T::DMAX : kAttnMaxCtas);
-            static_assert(DIRTY * 4 <= kAttnRing, "states and factors fit a warp's ring");
-            for (int i = lane; i < DIRTY / 4; i += 32) reinterpret_cast<int4*>(ring)[i] = int4{0, 0, 0, 0};
+        if (D < T::DMAX) {   // the states overwrote values behind D
+            for (int i = lane; i < NG * T::DMAX / 4; i += 32) reinterpret_cast<int4*>(ring)[i] = int4{0, 0, 0, 0};
             __syncwarp();
         }
         t0 = t1;

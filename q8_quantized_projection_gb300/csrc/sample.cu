@@ -52,6 +52,7 @@ constexpr int kThreads = 512, kWarpsN = kThreads / 32;
 constexpr int kTile = 128;                  // logits a warp takes at a time, four a lane
 constexpr int kPart = kWarpsN * kTile;      // a CTA's part is a multiple of this
 constexpr int kMaxPart = 46 * 1024;         // logits of a part held in shared memory
+constexpr int kPairPart = 18 * 1024;        // the same with two CTAs an SM
 constexpr int kBins = 1024, kList = 2048, kMaxCluster = 8;
 constexpr uint32_t kPairs = kBins / 2, kPairsOne = 128;   // lists up to these are compared pair by pair (one CTA a row)
 constexpr int kShort = 128;                 // a longer list is cut by a histogram before it is sorted
@@ -87,6 +88,7 @@ extern __shared__ __align__(16) unsigned char smem[];
 __device__ __forceinline__ Shared& sh() { return *reinterpret_cast<Shared*>(smem); }
 __device__ __forceinline__ float* sh_x() { return reinterpret_cast<float*>(smem + sizeof(Shared)); }
 static_assert(sizeof(Shared) % 16 == 0 && sizeof(Shared) + 4 * kMaxPart <= 227 * 1024, "shared memory");
+static_assert(2 * (sizeof(Shared) + 4 * kPairPart + 1024) <= 228 * 1024, "two CTAs an SM");
 
 // A logit as it is taken: NaN as -inf (never drawn), +inf as the largest float.
 __device__ __forceinline__ float clean(float v) { return v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY; }
@@ -1051,10 +1053,11 @@ cudaError_t launch_sample(const SampleArgs& a, const LaunchCtx& ctx) {
         const int64_t tiles = (a.N + int64_t(size) * kPart - 1) / (int64_t(size) * kPart);
         return int(tiles * kPart);
     };
-    // CTAs a row: parts of at most 16 K logits where 8 CTAs reach that; more,
-    // down to parts of one tile a warp, while the GPU has SMs to spare
+    // CTAs a row: parts of which an SM holds two where 8 CTAs reach that (248 rows
+    // of 33098: 2 of 18 K 80 us, 4 of 10 K 101 us); more, down to parts of one tile
+    // a warp, while the GPU has SMs to spare
     int size = 1;
-    while (size < kMaxCluster && (part_of(size) > 16 * 1024 ||
+    while (size < kMaxCluster && (part_of(size) > kPairPart ||
                                   (a.rows * size * 2 <= ctx.num_sms && part_of(size) > kPart)))
         size *= 2;
     const int part = part_of(size);

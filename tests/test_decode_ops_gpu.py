@@ -166,6 +166,16 @@ def test_attn_ragged_batches(rows):
     Attn("f16", pos, 8, 2, 64, 400, window=150, sinks=5, seed=rows, pad=5).check()
 
 
+@pytest.mark.parametrize("kv,heads,dim,n", [
+    ("f32", 8, 256, 9000), ("f32", 8, 72, 20000), ("f32", 5, 8, 30000), ("f32", 1, 64, 60000), ("f32", 1, 8, 70000),
+    ("f32", 2, 200, 20000), ("bf16", 8, 128, 30000), ("bf16", 3, 24, 60000), ("bf16", 1, 256, 40000),
+    ("f16", 7, 40, 30000), ("f16", 4, 200, 20000), ("f16", 6, 256, 15000)])
+def test_attn_one_head_cut_in_many_parts(kv, heads, dim, n):
+    """More parts of a K/V head than are joined at a time, of few values and of many."""
+    Attn(kv, [n - 1], heads, 1, dim, n, seed=n + dim).check()
+    Attn(kv, [n - 1, n // 9], heads, 1, dim, n, window=n // 2, sinks=5, seed=n - dim).check()
+
+
 def test_attn_strided_rows():
     a = Attn("bf16", [50, 20, 63], 6, 3, 24, 64, seed=5, pad=13)
     a.check()
