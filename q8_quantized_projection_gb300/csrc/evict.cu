@@ -35,7 +35,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32, kThreads = 512;
+constexpr int kThreads = 512;
 constexpr int kDigit = 256, kMaxCluster = 8;
 constexpr int kHeld = 8;                      // keys a lane holds at a time
 constexpr int kBatch = 4;                     // pieces a thread has in a batch of moves
@@ -56,7 +56,10 @@ __device__ __forceinline__ int32_t* kept_list(const EvictArgs& a, int64_t unit) 
     return first_moved(a) + (a.rows * a.kv_heads + 63) / 64 * 64 + unit * a.budget;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a, int* err) {
+template <int kSelThreads>
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_kernel(const EvictArgs a, int* err) {
+    constexpr int kSelWarps = kSelThreads / 32;
+    static_assert(kSelThreads >= kDigit && kSelWarps <= 32, "a thread a bin, a lane a warp");
     __shared__ uint32_t s_hist[2][kDigit], s_scan[kSelWarps], s_digit, s_above;
     __shared__ uint2 s_warp[kSelWarps];                 // sure ones and ties by warp
     __shared__ uint2 s_cta[kMaxCluster];             // and by CTA
@@ -174,8 +177,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     if (need == 0) cluster_sync(size);                            // (every CTA runs, else the passes' barriers say so)
     __syncthreads();
     // kept ones before this warp: of the CTA's warps, then of the CTAs before
-    static_assert(kSelWarps == 32, "one lane a warp");
-    const uint2 of = s_warp[lane];
+    const uint2 of = lane < kSelWarps ? s_warp[lane] : make_uint2(0, 0);
     uint2 up = of;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -302,6 +304,27 @@ __global__ void __launch_bounds__(kThreads, 2)
                         col < row_bytes, rank, size);
 }
 
+template <int THREADS>
+cudaError_t launch_select(const EvictArgs& a, const LaunchCtx& ctx) {
+    // CTAs a row and head: so many that lanes hold their keys, where 8 reach that
+    // (a barrier of one CTA costs 0.4 thousand cycles, of a cluster 1.8)
+    int size = 1;
+    while (size < kMaxCluster && a.n_pos > int64_t(size) * THREADS * kHeld) size *= 2;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attrs[2];
+    cfg.stream = ctx.stream;
+    cfg.numAttrs = pdl_attrs(ctx, attrs);
+    attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attrs[cfg.numAttrs].val.clusterDim.x = unsigned(size);
+    attrs[cfg.numAttrs].val.clusterDim.y = 1;
+    attrs[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+    cfg.attrs = attrs;
+    cfg.gridDim = dim3(unsigned(a.rows * a.kv_heads * size));
+    cfg.blockDim = dim3(THREADS);
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<THREADS>, a, ctx.dev_err);
+}
+
 template <bool CLUSTER>
 cudaError_t launch_move(const EvictArgs& a, int size, int elt, int lanes_log, int slices, const LaunchCtx& ctx) {
     cudaLaunchConfig_t cfg{};
@@ -330,23 +353,9 @@ size_t evict_workspace_bytes(int64_t rows, int64_t kv_heads, int64_t budget) {
 
 cudaError_t launch_evict(const EvictArgs& a, const LaunchCtx& ctx) {
     const int64_t units = a.rows * a.kv_heads;
-    // CTAs a row and head: so many that lanes hold their keys, where 8 reach that
-    // (a barrier of one CTA costs 0.4 thousand cycles, of a cluster 1.8)
-    int size = 1;
-    while (size < kMaxCluster && a.n_pos > int64_t(size) * kSelThreads * kHeld) size *= 2;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attrs[2];
-    cfg.stream = ctx.stream;
-    cfg.numAttrs = pdl_attrs(ctx, attrs);
-    attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attrs[cfg.numAttrs].val.clusterDim.x = unsigned(size);
-    attrs[cfg.numAttrs].val.clusterDim.y = 1;
-    attrs[cfg.numAttrs].val.clusterDim.z = 1;
-    ++cfg.numAttrs;
-    cfg.attrs = attrs;
-    cfg.gridDim = dim3(unsigned(units * size));
-    cfg.blockDim = dim3(kSelThreads);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ctx.dev_err);
+    const cudaError_t e = a.n_pos <= 256 * kHeld   ? launch_select<256>(a, ctx)
+                          : a.n_pos <= 512 * kHeld ? launch_select<512>(a, ctx)
+                                                   : launch_select<1024>(a, ctx);
     if (e != cudaSuccess) return e;
     // the widest slice that leaves a CTA an SM, 64 bytes at least
     const int elt = a.kv_type == Q8_KV_F32 ? 4 : 2, chunks = int(a.dim) * elt / 16;      // 16-byte pieces an entry
@@ -360,7 +369,7 @@ cudaError_t launch_evict(const EvictArgs& a, const LaunchCtx& ctx) {
     // of 64 f16 values, 41475 of 55887 entries: 123 us alone, 57 in eights; 16 x 8
     // heads of 128, two CTAs an SM: 76 alone, 96 in pairs)
     const int64_t ctas = units * 2 * slices, batch = int64_t(kThreads >> lanes_log) * kBatch;
-    size = 1;
+    int size = 1;
     while (size < kMaxCluster && ctas <= ctx.num_sms + ctx.num_sms / 10 && ctas * size * 2 <= 5 * int64_t(ctx.num_sms) &&
            a.budget >= 3 * batch * size * 2)
         size *= 2;
