@@ -8,8 +8,11 @@
 // every warp counts and lists the kept entries of its own range in order.  A
 // lane holds its keys in registers where a warp's range is at most 256 entries
 // and reads them again (4 bytes against the caches' hundreds) where it is
-// longer.  Bound by the latency of its steps: 11 us at 4096 entries a row and
-// head, 12 at 8192, 16 at 32768.
+// longer; the CTA has a lane for eight keys of a row where 256 or 512 threads do
+// (2048 of 4096 entries of 8 heads of 128 f32 values, moves included: 1024 threads
+// 16.2 us, 512 14.4; 150 of 300 of 64 x 8 heads of 64: 1024 49, 256 30).  Bound by
+// the latency of its steps: 8 us at 4096 entries a row and head, 12 at 8192, 16 at
+// 32768.
 //
 // evict_move_kernel: K, V and acc to the front, in place and in order.  Entry
 // j of the result comes from an entry idx[j] >= j.  A CTA owns a column slice
@@ -35,7 +38,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
 constexpr int kDigit = 256, kMaxCluster = 8;
 constexpr int kHeld = 8;                      // keys a lane holds at a time
 constexpr int kBatch = 4;                     // pieces a thread has in a batch of moves
@@ -264,8 +266,8 @@ __device__ __forceinline__ void move_items(const unsigned char* src, unsigned ch
 
 // Cluster: acc of one row and K/V head (the first ones), or its K or V in one
 // column slice of 16 << lanes_log bytes.
-template <bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, 2)
+template <bool CLUSTER, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     evict_move_kernel(const EvictArgs a, int elt, int lanes_log, int slices) {
     const unsigned rank = CLUSTER ? cg::this_cluster().block_rank() : 0;
     const unsigned size = CLUSTER ? cg::this_cluster().num_blocks() : 1;
@@ -325,7 +327,7 @@ cudaError_t launch_select(const EvictArgs& a, const LaunchCtx& ctx) {
     return cudaLaunchKernelEx(&cfg, evict_select_kernel<THREADS>, a, ctx.dev_err);
 }
 
-template <bool CLUSTER>
+template <bool CLUSTER, int kThreads>
 cudaError_t launch_move(const EvictArgs& a, int size, int elt, int lanes_log, int slices, const LaunchCtx& ctx) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attrs[2];
@@ -341,7 +343,7 @@ cudaError_t launch_move(const EvictArgs& a, int size, int elt, int lanes_log, in
         ++cfg.numAttrs;
     }
     cfg.attrs = attrs;
-    return cudaLaunchKernelEx(&cfg, evict_move_kernel<CLUSTER>, a, elt, lanes_log, slices);
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel<CLUSTER, kThreads>, a, elt, lanes_log, slices);
 }
 
 }  // namespace
@@ -368,13 +370,18 @@ cudaError_t launch_evict(const EvictArgs& a, const LaunchCtx& ctx) {
     // together: up to 5 CTAs an SM in all, three batches each at least (1 x 8 heads
     // of 64 f16 values, 41475 of 55887 entries: 123 us alone, 57 in eights; 16 x 8
     // heads of 128, two CTAs an SM: 76 alone, 96 in pairs)
-    const int64_t ctas = units * 2 * slices, batch = int64_t(kThreads >> lanes_log) * kBatch;
+    const int64_t ctas = units * 2 * slices, batch = int64_t(512 >> lanes_log) * kBatch;
     int size = 1;
     while (size < kMaxCluster && ctas <= ctx.num_sms + ctx.num_sms / 10 && ctas * size * 2 <= 5 * int64_t(ctx.num_sms) &&
            a.budget >= 3 * batch * size * 2)
         size *= 2;
-    if (size > 1) return launch_move<true>(a, size, elt, lanes_log, slices, ctx);
-    return launch_move<false>(a, size, elt, lanes_log, slices, ctx);
+    if (size > 1) return launch_move<true, 512>(a, size, elt, lanes_log, slices, ctx);
+    // short walks of more CTAs than two an SM: 256 threads, four an SM (256 x 8 heads
+    // of 128 bf16 values, 150 of 300: 104 us with 512, 85 with 256, 80 with 128;
+    // 16 x 8, 1000 of 2000: 33, 35)
+    if (a.budget <= 512 && ctas > 2 * int64_t(ctx.num_sms))
+        return launch_move<false, 256>(a, size, elt, lanes_log, slices, ctx);
+    return launch_move<false, 512>(a, size, elt, lanes_log, slices, ctx);
 }
 
 }  // namespace q8

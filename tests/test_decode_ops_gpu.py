@@ -450,6 +450,16 @@ def test_evict_weights(what):
     Evict("f16", [n - 1, n - 40], 2, 16, n, 600, sinks=0, recent=0, acc=a.clone()).check(in_place=True)
 
 
+@pytest.mark.parametrize("n,budget", [(300, 140), (2049, 1000), (3900, 3001), (6000, 2500), (30000, 9000)])
+@pytest.mark.parametrize("levels", [1, 3, 40])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_ties_at_every_length(n, budget, levels, in_place):
+    """Weights of few values: the last place falls among equals, of which the first ones stay."""
+    e = Evict("f16", [n - 1, n - 2], 40 if n < 400 else 2, 8, n, budget, sinks=3, recent=20, seed=n)
+    e.acc.mul_(levels).floor_().div_(levels)
+    e.check(in_place)
+
+
 def test_evict_position_out_of_range():
     t = torch()
     e = Evict("f32", [11, 11, 11], 2, 16, 12, 6)
