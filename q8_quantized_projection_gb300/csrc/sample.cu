@@ -55,7 +55,7 @@ constexpr int kMaxPart = 46 * 1024;         // logits of a part held in shared m
 constexpr int kPairPart = 18 * 1024;        // the same with two CTAs an SM
 constexpr int kBins = 1024, kList = 2048, kMaxCluster = 8;
 constexpr uint32_t kPairs = kBins / 2, kPairsOne = 128;   // lists up to these are compared pair by pair (one CTA a row)
-constexpr int kShort = 128;                 // a longer list is cut by a histogram before it is sorted
+constexpr int kShort = kThreads / 4;        // a longer list is cut by a histogram, and what is longer then is sorted
 typedef unsigned long long u64;
 
 // What the CTAs of a cluster exchange: sums a, b, g, e and e2, the largest c
@@ -650,6 +650,62 @@ struct Settings {
     int k;
 };
 
+// The same on at most kShort tokens a, every pair of them compared, four threads
+// a token, in place of two sorts (wt: n words of shared memory).
+__device__ __noinline__ void draw_from_pairs(const Weights& w, const Settings& g, const u64* a, u64* wt, int n,
+                                             uint32_t* tok, u64* mass, uint32_t* kept) {
+    Shared& s = sh();
+    const int i = threadIdx.x >> 2, sub = threadIdx.x & 3;
+    const bool has = i < n, writes = has && sub == 0;
+    const u64 t = has ? a[i] : 0, wi = has ? w(list_x(t)) : 0;
+    if (writes) wt[i] = wi;
+    __syncthreads();
+    // what goes before it: the k-th says the k's mass, and who falls short of p of that stays
+    u64 above = 0;
+    int rank = 0;
+    for (int j = sub; j < n; j += 4) {
+        const bool more = a[j] > t;
+        above += more ? wt[j] : 0;
+        rank += more;
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+        above += __shfl_xor_sync(0xffffffffu, above, d);
+        rank += __shfl_xor_sync(0xffffffffu, rank, d);
+    }
+    if (writes && rank == 0) s.found = list_i(t);
+    if (writes && rank == g.k - 1) s.scan[0] = above + wi;
+    __syncthreads();
+    const u64 need = g.p < 1.0f ? share(g.p, s.scan[0], true) : ~u64(0);
+    const bool in = has && rank < g.k && above < need && (rank == 0 || wi >= g.floor_w);
+    // (a weight is at most 2^61 here; bit 62: not 0 in binary32)
+    const u64 positive = w.rough(list_x(t)) > 0.0f ? u64(1) << 62 : 0;
+    if (writes) wt[i] = in ? wi | positive | u64(1) << 63 : 0;
+    __syncthreads();
+    const auto counts = [&](u64 v) { return g.u > 0.0f ? v & ((u64(1) << 62) - 1) : v >> 62 & 1; };
+    u64 sum = 0, run = 0;
+    uint32_t cnt = 0;
+    for (int j = sub; j < n; j += 4) {
+        const u64 v = wt[j];
+        sum += v & ((u64(1) << 62) - 1);
+        cnt += uint32_t(v >> 63);
+        run += list_i(a[j]) < list_i(t) ? counts(v) : 0;
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        run += __shfl_xor_sync(0xffffffffu, run, d);
+        cnt += __shfl_xor_sync(0xffffffffu, cnt, d);
+    }
+    // the first sum above u * S; u = 0: the first whose weight is not 0
+    const u64 e = g.u >= 1.0f ? sum : g.u > 0.0f ? share(g.u, sum, false) + 1 : 1;
+    if (writes && in && run < e && run + counts(wi | positive) >= e) s.found = list_i(t);
+    __syncthreads();
+    *tok = s.found;
+    *mass = sum;
+    *kept = cnt;
+}
+
 // The first CTA alone, on a list of n tokens that holds the row's k largest
 // (k <= n): the filters and the draw.  scale: bins over the list's logits.
 __device__ __noinline__ void draw_from_list(const Weights& w, const Settings& g, int n, float scale, uint32_t* tok,
@@ -678,6 +734,7 @@ __device__ __noinline__ void draw_from_list(const Weights& w, const Settings& g,
         a = s.mine;
         wt = s.list;
     }
+    if (n <= kShort) return draw_from_pairs(w, g, a, wt, n, tok, mass, kept);
     sort_down(a, n);
     const int per = (k + kThreads - 1) / kThreads, at0 = tid * per, at1 = min(at0 + per, k);
     u64 part = 0;

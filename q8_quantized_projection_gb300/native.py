@@ -318,8 +318,8 @@ def _kv_caches(k_cache, v_cache, kv_heads):
 
 
 def attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window=-1, sinks=0, acc=False) -> int:
-    return int((_lib or load()).attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window,
-                                                          sinks, 1 if acc else 0))
+    return int((_lib or load()).attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window, sinks,
+                                                      1 if acc else 0))
 
 
 def attn_decode(q, k_cache, v_cache, pos, out, workspace, heads, kv_heads, window=-1, sinks=0,
