@@ -33,8 +33,8 @@
 //
 // Measured (32 query and 8 K/V heads of 128 values; device time): 64 rows of
 // 4100 to 8192 bf16 entries 241 us, 6.7 TB/s; 16 rows of up to 2052 visible
-// f32 entries 41 us, 5.6 TB/s; one row of 130001 bf16 entries 90 us, 5.9 TB/s,
-// and 105 us with the weights accumulated; one row of 613 f32 entries 8.7 us,
+// f32 entries 42 us, 5.5 TB/s; one row of 130001 bf16 entries 90 us, 5.9 TB/s,
+// and 104 us with the weights accumulated; one row of 613 f32 entries 8.1 us,
 // of one entry 3.8 us: there the launch, three dependent reads (positions, q
 // and the entries, the partial states) and the ticket are the time.  A unit cut between CTAs leaves
 // partial states in the workspace; the CTA that finishes it last (a ticket)
@@ -55,11 +55,10 @@ constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnRing = 24 * 1024;                  // bytes a warp
 constexpr int kAttnMaxCtas = 512;
 // 16-bit caches take the matrix instructions (attn_mma.cuh) from five query heads
-// a block and up to heads of 128 values on.  (32 rows of 4096 bf16 entries, 8 K/V
-// heads of 128 values: 4 query heads each 91 us on the lanes, 96 on the matrix
-// instructions; 8 query heads 145 and 101; of 256 values their states would not
-// fit the registers.)
-constexpr int kAttnLanesHeads = 4, kAttnMmaDim = 128;
+// a block on.  (32 rows of 4096 bf16 entries, 8 K/V heads of 128 values: 4 query
+// heads each 91 us on the lanes, 96 on the matrix instructions; 8 query heads 145
+// and 100.)
+constexpr int kAttnLanesHeads = 4;
 static_assert(4 * kAttnMaxCtas <= kCounterBytes, "one ticket a CTA");
 
 // Floats of a partial state, whole 16-byte words.
@@ -161,6 +160,7 @@ struct Segment {
     int64_t off;             // of the row and K/V head in the caches
     uint32_t v_end, v_begin;
     int its;                 // stages
+    int half;                // of V's values, where two warps share them
     unsigned char* ring;
     float* q;                // shared: the block's query heads [NG][DMAX]
     float *m, *l;            // the warp's references and sums; its o goes to the ring [NG][DMAX]
@@ -389,7 +389,7 @@ struct AttnLanes {
     static constexpr int DPL = NG <= 4 ? 16 : 8;              // values a lane
     static constexpr int NC = DPL / CD;                       // chunks a lane
     static constexpr int NP = DPL / 2;                        // pairs a lane
-    static constexpr int DMAX = DPL * LPK;
+    static constexpr int DMAX = DPL * LPK, DV = DMAX, SPLIT = 1;
     static constexpr int PITCH = DMAX * ELT;                  // bytes an entry in a stage
     static constexpr int KPS = 32 / LPK;                      // entries a warp takes at a time
     static constexpr int U = KV == Q8_KV_F32 ? 2 : 4;
@@ -412,9 +412,9 @@ struct AttnLanes {
 
 template <class T>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams p) {
-    constexpr int NG = T::NG;
+    constexpr int NG = T::NG, WARPS = kAttnWarps / T::SPLIT;      // warps that share a stage's entries
     extern __shared__ __align__(256) unsigned char ring_raw[];
-    unsigned char* const ring_all = ring_raw + (256 - (smem_u32(ring_raw) & 255) & 255);   // stages on 256 bytes
+    unsigned char* const ring_all = ring_raw + (512 - (smem_u32(ring_raw) & 511) & 511);   // stages on whole rows
     __shared__ uint32_t s_pre[Q8_MAX_ROWS + 1];   // tiles before each row
     __shared__ uint32_t s_warp[kAttnWarps];
     __shared__ int s_pos[Q8_MAX_ROWS];
@@ -519,10 +519,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         // visible, so 32 bits hold every index and a tile more.
         const uint64_t upto = uint64_t(t1 - unit0) * TT;
         const uint32_t v_end = uint32_t(vis.nvis < upto ? vis.nvis : upto);
-        const uint64_t v_from = uint64_t(t0 - unit0) * TT + warp * T::KT;
+        const int half = warp / WARPS;
+        const uint64_t v_from = uint64_t(t0 - unit0) * TT + (warp - half * WARPS) * T::KT;
         const uint32_t v_begin = uint32_t(v_from);
         const int its = v_end > v_from ? int((v_end - v_begin + T::TK - 1) / T::TK) : 0;
-        const Segment seg{p, m, g0, ng, vis, pitch, off, v_end, v_begin, its, ring, s_q, s_m[warp], s_l[warp]};
+        const Segment seg{p, m, g0, ng, vis, pitch, off, v_end, v_begin, its, half, ring, s_q, s_m[warp], s_l[warp]};
         T::states(seg);
         __syncthreads();
 
@@ -546,10 +547,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
             for (int w = 1; w < kAttnWarps; ++w) top = fmaxf(top, s_m[w][g]);
             float sum = 0.0f;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const int h0 = d / T::DV * WARPS;                     // the first warp that holds these values
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
+            for (int i = 0; i < WARPS; ++i) {
+                const int w = h0 + i;
                 const float f = s_m[w][g] == -INFINITY ? 1.0f : ex2(s_m[w][g] - top);   // l and o: 0 or NaN
-                const float4 o4 = *reinterpret_cast<const float4*>(ring_all + w * kAttnRing + (g * T::DMAX + d) * 4);
+                const float4 o4 =
+                    *reinterpret_cast<const float4*>(ring_all + w * kAttnRing + (g * T::DV + d % T::DV) * 4);
                 sum += s_l[w][g] * f;
                 v.x += o4.x * f, v.y += o4.y * f, v.z += o4.z * f, v.w += o4.w * f;
             }
@@ -683,7 +687,7 @@ template <class T>
 cudaError_t launch_attn_kernel(const AttnParams& p, const LaunchCtx& ctx) {
     static std::atomic<bool> ready[kMaxDevices];
     const auto kern = attn_kernel<T>;
-    constexpr size_t smem = size_t(kAttnWarps) * kAttnRing + 256;
+    constexpr size_t smem = size_t(kAttnWarps) * kAttnRing + 512;
     const cudaError_t e = set_smem_once(kern, smem, ctx.dev, ready);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -701,10 +705,8 @@ cudaError_t launch_attn_kernel(const AttnParams& p, const LaunchCtx& ctx) {
 template <int KV, int NG>
 cudaError_t launch_attn_lanes(const AttnParams& p, const LaunchCtx& ctx) {
     constexpr int SHARE = AttnLanes<KV, NG, 8>::DPL == 16 ? 1 : 2;
-    if constexpr (KV == Q8_KV_F32 || NG <= kAttnLanesHeads) {
-        if (p.a.dim <= 64) return launch_attn_kernel<AttnLanes<KV, NG, 4 * SHARE>>(p, ctx);
-        if (p.a.dim <= 128) return launch_attn_kernel<AttnLanes<KV, NG, 8 * SHARE>>(p, ctx);
-    }
+    if (p.a.dim <= 64) return launch_attn_kernel<AttnLanes<KV, NG, 4 * SHARE>>(p, ctx);
+    if (p.a.dim <= 128) return launch_attn_kernel<AttnLanes<KV, NG, 8 * SHARE>>(p, ctx);
     return launch_attn_kernel<AttnLanes<KV, NG, 16 * SHARE>>(p, ctx);
 }
 
@@ -712,8 +714,9 @@ template <int KV>
 cudaError_t launch_attn_type(const AttnParams& p, const LaunchCtx& ctx) {
     if (p.gsz == 1) return launch_attn_lanes<KV, 1>(p, ctx);
     if (p.gsz == 2) return launch_attn_lanes<KV, 2>(p, ctx);
-    if (p.gsz <= 4) return launch_attn_lanes<KV, 4>(p, ctx);
-    return launch_attn_lanes<KV, 8>(p, ctx);
+    if constexpr (KV == Q8_KV_F32)
+        if (p.gsz > kAttnLanesHeads) return launch_attn_lanes<KV, 8>(p, ctx);
+    return launch_attn_lanes<KV, 4>(p, ctx);
 }
 
 }  // namespace q8

@@ -1,5 +1,5 @@
-// attn_mma.cuh -- the attention kernels over 16-bit caches of heads up to 128
-// values: the products on the matrix instructions (mma.m16n8k16).
+// attn_mma.cuh -- the attention kernels over 16-bit caches: the products on the
+// matrix instructions (mma.m16n8k16).
 //
 // With the entries of a stage as the n of the first product and the k of the
 // second, a block of at most 8 query heads fills half of m = 16.  The other half
@@ -20,7 +20,9 @@
 //
 // What bounds it: HBM.  A stage of 16 bf16 entries of 128 values is 64
 // instructions of 2 clocks an SM, 8 clocks an entry against 23 for its bytes
-// (6.6 TB/s); on the lanes' FMA path eight query heads take 40.
+// (6.6 TB/s); on the lanes' FMA path eight query heads take 40.  Heads of 256
+// values: 16 rows of 4096 entries, 8 K/V heads of 8 query heads, bf16 113 us, f16
+// 109 (4.8 and 4.9 TB/s; on the lanes 146 and 151).
 #pragma once
 
 #include <cfloat>
@@ -83,10 +85,11 @@ template <class T>
 __device__ __noinline__ void plain_states(const Segment& s) {
     const AttnArgs& a = s.p.a;
     const int lane = threadIdx.x & 31, D = int(a.dim);
-    constexpr int J = T::DMAX / 32;
+    constexpr int J = T::DMAX / 32, JV = T::DV / 32;
+    const int v0 = s.half * T::DV;                      // this warp's values of V
     for (int g = 0; g < s.ng; ++g) {
-        float* const scores = s.p.scores ? s.p.scores + (int64_t(s.row) * a.heads + s.g0 + g) * s.p.cap : nullptr;
-        float top = -INFINITY, l = 0.0f, o[J] = {};
+        float* const scores = s.p.scores && s.half == 0 ? s.p.scores + (int64_t(s.row) * a.heads + s.g0 + g) * s.p.cap : nullptr;
+        float top = -INFINITY, l = 0.0f, o[JV] = {};
         for (int it = 0; it < s.its; ++it)
             for (int r = 0; r < T::KT; ++r) {
                 const uint32_t v = s.v_begin + uint32_t(it) * T::TK + r;
@@ -106,8 +109,8 @@ __device__ __noinline__ void plain_states(const Segment& s) {
                 top = n;
                 l = l * f + w;
 #pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const int d = lane + 32 * j;
+                for (int j = 0; j < JV; ++j) {
+                    const int d = v0 + lane + 32 * j;
                     if (d < D) o[j] = o[j] * f + w * from16<T::KV>(static_cast<const unsigned char*>(a.v) + at + 2 * d);
                 }
             }
@@ -116,50 +119,77 @@ __device__ __noinline__ void plain_states(const Segment& s) {
             s.l[g] = l;
         }
 #pragma unroll
-        for (int j = 0; j < J; ++j) reinterpret_cast<float*>(s.ring)[g * T::DMAX + lane + 32 * j] = o[j];
+        for (int j = 0; j < JV; ++j) reinterpret_cast<float*>(s.ring)[g * T::DV + lane + 32 * j] = o[j];
     }
 }
 
 template <class T>
 __device__ __forceinline__ void mma_states(const Segment& s) {
-    constexpr int KV = T::KV, KS = T::KS, SUB = T::SUB;
+    constexpr int KV = T::KV, KS = T::KS, VS = T::VS, SUB = T::SUB;
     constexpr bool BF = KV == Q8_KV_BF16;
     const AttnParams& p = s.p;
     const AttnArgs& a = p.a;
     const int lane = threadIdx.x & 31, D = int(a.dim), its = s.its;
     const int g = lane >> 2, c2 = (lane & 3) * 2;       // this lane's query head, and its entries (or values) of 8
     const uint32_t ring_s = smem_u32(s.ring);
-    // a lane copies the same 16-byte column of a row in RPI; the row's swap of
+    // a lane copies the same 16-byte column of a row in RPI (VRPI); the row's swap of
     // chunks is its own (r0) and that of the row it begins at
-    const int r0 = lane / T::CPR, c0 = lane % T::CPR;
-    const bool copies = r0 < T::RPI && c0 * 8 < D;
+    const int r0 = lane / T::CPR, c0 = lane % T::CPR, rv = lane / T::VCPR, cv = lane % T::VCPR;
+    const bool copies = r0 < T::RPI && c0 * 8 < D, v_copies = rv < T::VRPI && s.half * T::DV + cv * 8 < D;
     const unsigned char* kp = static_cast<const unsigned char*>(a.k) + s.off + c0 * 16;
-    const unsigned char* vp = static_cast<const unsigned char*>(a.v) + s.off + c0 * 16;
+    const unsigned char* vp = static_cast<const unsigned char*>(a.v) + s.off + s.half * (2 * T::DV) + cv * 16;
     const uint32_t to = r0 * T::PITCH + T::swap(c0, r0) * 16, step = T::RPI * s.pitch;
+    const uint32_t v_to = T::HALF + rv * T::VPITCH + T::swap(cv, rv) * 16, v_step = T::VRPI * s.pitch;
 
     int in_slot = 0, out_slot = 0;
     const auto load = [&](int it) {
-        if (it < its && copies) {
-            const uint32_t st = ring_s + in_slot * (2 * T::HALF) + to, vb = s.v_begin + uint32_t(it) * T::TK + r0;
-            const uint32_t vt = s.v_begin + uint32_t(it) * T::TK;
+        // (where K and V are alike, so are their lanes' columns: one pass for both)
+        constexpr bool ALIKE = T::SPLIT == 1;
+        if (it < its && (copies || (!ALIKE && v_copies))) {
+            const uint32_t slot = ring_s + in_slot * T::STAGE, st = slot + to, sv = slot + v_to;
+            const uint32_t vt = s.v_begin + uint32_t(it) * T::TK, vb = vt + r0, vbv = vt + rv;
             if (vt + T::KT <= s.v_end && (vt >= s.vis.ns || vt + T::KT <= s.vis.ns)) {
                 // all of them, with none left out between
-                const uint64_t at = uint64_t(vb + (vt < s.vis.ns ? 0 : s.vis.gap)) * s.pitch;
-                const unsigned char *ka = kp + at, *va = vp + at;
+                const uint32_t gap = vt < s.vis.ns ? 0 : s.vis.gap;
+                const uint64_t at = uint64_t(vb + gap) * s.pitch;
+                const unsigned char *ka = kp + at, *va = vp + (ALIKE ? at : uint64_t(vbv + gap) * s.pitch);
+                if (ALIKE || copies) {
 #pragma unroll
-                for (int r = 0; r < T::KT; r += T::RPI, ka += step, va += step) {
-                    const uint32_t dst = (st ^ T::turn(r)) + r * T::PITCH;
-                    cp16(dst, ka, true);
-                    cp16(dst + T::HALF, va, true);
+                    for (int r = 0; r < T::KT; r += T::RPI, ka += step) {
+                        const uint32_t dst = (st ^ T::turn(r)) + r * T::PITCH;
+                        cp16(dst, ka, true);
+                        if constexpr (ALIKE) {
+                            cp16(dst + T::HALF, va, true);
+                            va += step;
+                        }
+                    }
+                }
+                if (!ALIKE && v_copies) {
+#pragma unroll
+                    for (int r = 0; r < T::KT; r += T::VRPI, va += v_step)
+                        cp16((sv ^ T::turn(r)) + r * T::VPITCH, va, true);
                 }
             } else {
+                const auto from = [&](uint32_t v, bool in) {
+                    return in ? uint64_t(v + (v < s.vis.ns ? 0 : s.vis.gap)) * s.pitch : 0;
+                };
+                if (ALIKE || copies) {
 #pragma unroll
-                for (int r = 0; r < T::KT; r += T::RPI) {
-                    const uint32_t v = vb + r, dst = (st ^ T::turn(r)) + r * T::PITCH;
-                    const bool in = v < s.v_end;
-                    const uint64_t at = in ? uint64_t(v + (v < s.vis.ns ? 0 : s.vis.gap)) * s.pitch : 0;
-                    cp16(dst, kp + at, in);
-                    cp16(dst + T::HALF, vp + at, in);
+                    for (int r = 0; r < T::KT; r += T::RPI) {
+                        const uint32_t v = vb + r, dst = (st ^ T::turn(r)) + r * T::PITCH;
+                        const bool in = v < s.v_end;
+                        const uint64_t at = from(v, in);
+                        cp16(dst, kp + at, in);
+                        if constexpr (ALIKE) cp16(dst + T::HALF, vp + at, in);
+                    }
+                }
+                if (!ALIKE && v_copies) {
+#pragma unroll
+                    for (int r = 0; r < T::KT; r += T::VRPI) {
+                        const uint32_t v = vbv + r;
+                        const bool in = v < s.v_end;
+                        cp16((sv ^ T::turn(r)) + r * T::VPITCH, vp + from(v, in), in);
+                    }
                 }
             }
         }
@@ -183,7 +213,10 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
         scale = __int_as_float(e << 23);
         back = __int_as_float((254 - e) << 23);
     }
-    uint32_t qa[KS][4], ql[BF ? KS : 1][2];
+    // (the third part of 256 values lies in shared memory, each lane's its own)
+    constexpr bool LOW = BF && T::SPLIT > 1;
+    __shared__ uint2 s_low[LOW ? KS * 32 : 1];
+    uint32_t qa[KS][4], ql[BF && !LOW ? KS : 1][2];
 #pragma unroll
     for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -191,20 +224,26 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
             float x = q[16 * k + 8 * h] * scale, y = q[16 * k + 8 * h + 1] * scale;
             qa[k][2 * h] = round_pair<KV>(x, y);
             qa[k][2 * h + 1] = round_pair<KV>(x, y);
-            if constexpr (BF) ql[k][h] = round_pair<KV>(x, y);
+            if constexpr (LOW) {
+                const uint32_t low = round_pair<KV>(x, y);
+                if (threadIdx.x < 32) (h ? s_low[32 * k + lane].y : s_low[32 * k + lane].x) = low;
+            } else if constexpr (BF) {
+                ql[k][h] = round_pair<KV>(x, y);
+            }
         }
-    float o[2 * KS][4] = {}, sum[2 * KS][2] = {};       // chains of o; their sums
+    if constexpr (LOW) __syncthreads();
+    float o[2 * VS][4] = {}, sum[2 * VS][2] = {};       // chains of o; their sums
     float ref = -INFINITY, l = 0.0f;
     float* const scores =
-        p.scores && g < s.ng ? p.scores + (int64_t(s.row) * a.heads + s.g0 + g) * p.cap : nullptr;
+        p.scores && g < s.ng && s.half == 0 ? p.scores + (int64_t(s.row) * a.heads + s.g0 + g) * p.cap : nullptr;
     // where this lane's rows of the matrix loads begin: of K four of entries 0-7 and
     // 8-15 by values 0-7 and 8-15, of V transposed
     const int kr = (lane >> 4) * 8 + (lane & 7), vr = (lane >> 3 & 1) * 8 + (lane & 7);
     const uint32_t k_at = kr * T::PITCH + T::swap(lane >> 3 & 1, kr) * 16;
-    const uint32_t v_at = T::HALF + vr * T::PITCH + T::swap(lane >> 4, vr) * 16;
+    const uint32_t v_at = T::HALF + vr * T::VPITCH + T::swap(lane >> 4, vr) * 16;
     const auto flush = [&] {
 #pragma unroll
-        for (int t = 0; t < 2 * KS; ++t) {
+        for (int t = 0; t < 2 * VS; ++t) {
             sum[t][0] += o[t][0] + o[t][2];
             sum[t][1] += o[t][1] + o[t][3];
             o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
@@ -215,7 +254,7 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
         cp_wait<T::S - 2>();
         __syncwarp();
         load(it + T::S - 1);
-        const uint32_t st = ring_s + out_slot * (2 * T::HALF);
+        const uint32_t st = ring_s + out_slot * T::STAGE;
         out_slot = out_slot + 1 == T::S ? 0 : out_slot + 1;
         const uint32_t vb = s.v_begin + uint32_t(it) * T::TK;
         float x[SUB][4];                                // entries c2, c2 + 1, 8 + c2, 9 + c2 of each 16
@@ -231,7 +270,8 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
                 mma16<KV>(c[0][k & 1], qa[k], kb[0], kb[1]);
                 mma16<KV>(c[1][k & 1], qa[k], kb[2], kb[3]);
                 if constexpr (BF) {
-                    const uint32_t low[4] = {ql[k][0], 0u, ql[k][1], 0u};
+                    const uint2 lw = LOW ? s_low[32 * k + lane] : make_uint2(ql[LOW ? 0 : k][0], ql[LOW ? 0 : k][1]);
+                    const uint32_t low[4] = {lw.x, 0u, lw.y, 0u};
                     mma16<KV>(c[0][k & 1], low, kb[0], kb[1]);
                     mma16<KV>(c[1][k & 1], low, kb[2], kb[3]);
                 }
@@ -257,7 +297,7 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
             ref = top;
             l *= f;
 #pragma unroll
-            for (int t = 0; t < 2 * KS; ++t) {
+            for (int t = 0; t < 2 * VS; ++t) {
                 sum[t][0] *= f, sum[t][1] *= f;
                 o[t][0] *= f, o[t][1] *= f, o[t][2] *= f, o[t][3] *= f;
             }
@@ -280,9 +320,9 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
                 pl[2] = round_pair<KV>(x[u][2], x[u][3]);
             }
 #pragma unroll
-            for (int t = 0; t < KS; ++t) {
+            for (int t = 0; t < VS; ++t) {
                 uint32_t v[4];
-                ldmatrix4<true>(v, T::column(st + v_at, 2 * t) + u * 16 * T::PITCH);
+                ldmatrix4<true>(v, T::column(st + v_at, 2 * t) + u * 16 * T::VPITCH);
                 mma16<KV>(o[2 * t], pa, v[0], v[1]);
                 mma16<KV>(o[2 * t + 1], pa, v[2], v[3]);
                 if constexpr (BF) {
@@ -301,7 +341,7 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     float zero = l * 0.0f;
 #pragma unroll
-    for (int t = 0; t < 2 * KS; ++t) zero += sum[t][0] * 0.0f + sum[t][1] * 0.0f;
+    for (int t = 0; t < 2 * VS; ++t) zero += sum[t][0] * 0.0f + sum[t][1] * 0.0f;
     if (__any_sync(0xffffffffu, !(zero == 0.0f))) {      // something infinite or NaN among what was seen
         plain_states<T>(s);
         return;
@@ -310,29 +350,33 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
         s.m[g] = ref;
         s.l[g] = l;
     }
-    float* so = reinterpret_cast<float*>(s.ring) + g * T::DMAX + c2;
+    float* so = reinterpret_cast<float*>(s.ring) + g * T::DV + c2;
 #pragma unroll
-    for (int t = 0; t < 2 * KS; ++t) {
+    for (int t = 0; t < 2 * VS; ++t) {
         constexpr float f = BF ? 1.0f : 1.0f / 128.0f;
         *reinterpret_cast<float2*>(so + 8 * t) = make_float2(sum[t][0] * f, sum[t][1] * f);
     }
 }
 
-// KS: steps of 16 values a head.
-template <int KV_, int KS_>
+// KS: steps of 16 values a head.  SPLIT 2: two warps take the same entries, all of
+// K and half of V's values each (the states of 256 values would not fit a warp's
+// registers); K comes from L2 the second time.
+template <int KV_, int KS_, int SPLIT_ = 1>
 struct AttnMma {
-    static constexpr int KV = KV_, KS = KS_, NG = 8;
-    static constexpr int ELT = 2, DMAX = 16 * KS, PITCH = 2 * DMAX, CPR = 2 * KS;
+    static constexpr int KV = KV_, KS = KS_, SPLIT = SPLIT_, VS = KS / SPLIT, NG = 8;
+    static constexpr int ELT = 2, DMAX = 16 * KS, DV = 16 * VS;
+    static constexpr int PITCH = 2 * DMAX, CPR = 2 * KS, VPITCH = 2 * DV, VCPR = 2 * VS;
     static constexpr int SUB = KS == 4 ? 2 : 1;               // products of 16 entries a stage
-    static constexpr int KT = 16 * SUB, HALF = KT * PITCH;
-    static constexpr int S0 = kAttnRing / (2 * HALF);
+    static constexpr int KT = 16 * SUB, HALF = KT * PITCH, STAGE = HALF + KT * VPITCH;
+    static constexpr int S0 = kAttnRing / STAGE;
     static constexpr int S = S0 > 6 ? 6 : S0;
-    static constexpr int TK = kAttnWarps * KT;
-    static constexpr int EXTRA = (128 * 1024 + kAttnWarps * 2 * HALF - 1) / (kAttnWarps * 2 * HALF);
+    static constexpr int TK = kAttnWarps / SPLIT * KT;
+    static constexpr int EXTRA = (128 * 1024 + TK * 2 * PITCH - 1) / (TK * 2 * PITCH);
     static constexpr int LEAST = 1;
-    static_assert(S >= 2 && NG * DMAX * 4 <= kAttnRing && DMAX % 32 == 0, "attention tile");
+    static_assert(S >= 2 && NG * DMAX * 4 <= kAttnRing && DV % 32 == 0, "attention tile");
 
-    static constexpr int RPI = CPR == 8 ? 4 : 2;              // rows a warp copies at a time
+    static constexpr int RPI = CPR == 8 ? 4 : CPR == 32 ? 1 : 2;       // rows a warp copies at a time
+    static constexpr int VRPI = VCPR == 8 ? 4 : 2;
 
     // Chunk c of entry r lies at swap(c, r), so that the eight rows of a matrix load
     // are on banks of their own (rows of 12 chunks begin on every other half).
@@ -349,10 +393,11 @@ struct AttnMma {
 
 template <int KV>
 cudaError_t launch_attn_16(const AttnParams& p, const LaunchCtx& ctx) {
-    if (p.gsz <= kAttnLanesHeads || p.a.dim > kAttnMmaDim) return launch_attn_type<KV>(p, ctx);
+    if (p.gsz <= kAttnLanesHeads) return launch_attn_type<KV>(p, ctx);
     if (p.a.dim <= 64) return launch_attn_kernel<AttnMma<KV, 4>>(p, ctx);
     if (p.a.dim <= 96) return launch_attn_kernel<AttnMma<KV, 6>>(p, ctx);
-    return launch_attn_kernel<AttnMma<KV, 8>>(p, ctx);
+    if (p.a.dim <= 128) return launch_attn_kernel<AttnMma<KV, 8>>(p, ctx);
+    return launch_attn_kernel<AttnMma<KV, 16, 2>>(p, ctx);
 }
 
 }  // namespace q8

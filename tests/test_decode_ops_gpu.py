@@ -155,6 +155,39 @@ def test_attn_eight_heads_of_not_finite_values_that_are_seen(kv, dim):
     no_error()
 
 
+@pytest.mark.parametrize("kv", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [136, 160, 192, 200, 248, 256])
+@pytest.mark.parametrize("group,n", [(5, 17), (6, 1), (7, 64), (8, 300), (16, 65), (8, 4000)])
+def test_attn_eight_long_heads_of_16_bit_caches(kv, dim, group, n):
+    """Two warps share V's values: heads padded to whole steps, entries to whole stages."""
+    Attn(kv, [n - 1, n // 2, n // 3], 2 * group, 2, dim, n, window=n // 2 + 20, sinks=2, seed=dim + n).check()
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [136, 192, 256])
+def test_attn_eight_long_heads_of_not_finite_values_that_are_seen(kv, dim):
+    test_attn_eight_heads_of_not_finite_values_that_are_seen(kv, dim)
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16"])
+@pytest.mark.parametrize("at", [0, 127, 128, 199])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_attn_one_value_of_v_not_finite_in_either_half(kv, at, bad):
+    """It reaches its own output only, whichever of the two warps holds it."""
+    t = torch()
+    a = Attn(kv, [499, 250], 16, 2, 200, 500, seed=at)
+    a.v[0, 77, at] = bad
+    want = a.want()
+    a.call()
+    got, w, tol = a.out.cpu().double().numpy(), *want[:2]
+    hit = np.zeros_like(w, dtype=bool)
+    hit[0, [g * 200 + at for g in range(8)]] = True
+    assert not np.isfinite(got[hit]).any() and not np.isfinite(w[hit]).any()
+    assert np.all(np.abs(got[~hit] - w[~hit]) <= tol[~hit])
+    assert np.all(np.abs(a.acc.cpu().double().numpy() - want[2]) <= want[3])
+    no_error()
+
+
 @pytest.mark.parametrize("heads,kv_heads,dim", [(1024, 4, 16), (128, 1, 64), (1024, 1024, 8), (71, 71, 128)])
 def test_attn_many_heads(heads, kv_heads, dim):
     Attn("bf16", [90, 12], heads, kv_heads, dim, 91, window=60, sinks=1, seed=heads).check()
