@@ -25,20 +25,21 @@
 // Split.  A unit is a row's K/V head (and block of at most 8 query heads); its
 // visible entries are tiles of 4 warps x KT (several such where the tiles would
 // not fit 32 bits), and it counts some tiles more for what it costs to begin
-// and end (128 KB of loads where CTAs have long shares: of 64,
-// 128, 192 and 256 KB the best on long and ragged batches).  The tiles of all units in one line are cut evenly over the CTAs, so
-// ragged batches balance and one long sequence fills the GPU; lengths are read
-// on the device, so one captured graph serves every step.  Two CTAs of four
+// and end (128 KB of loads where CTAs have long shares: of 64, 128, 192 and 256 KB
+// the best on long and ragged batches).  The tiles of all units in one line are
+// cut evenly over the CTAs, so ragged batches balance and one long sequence fills
+// the GPU (few units, fewer CTAs: the join of many parts would be the time);
+// lengths are read on the device, so one captured graph serves every step.  Two CTAs of four
 // warps an SM: one streams while the other ends a unit.
 //
 // Measured (32 query and 8 K/V heads of 128 values; device time): 64 rows of
 // 4100 to 8192 bf16 entries 241 us, 6.7 TB/s; 16 rows of up to 2052 visible
 // f32 entries 42 us, 5.5 TB/s; one row of 130001 bf16 entries 90 us, 5.9 TB/s,
-// and 104 us with the weights accumulated; one row of 613 f32 entries 8.1 us,
+// and 104 us with the weights accumulated; one row of 613 f32 entries 8.5 us,
 // of one entry 3.8 us: there the launch, three dependent reads (positions, q
-// and the entries, the partial states) and the ticket are the time.  A unit cut between CTAs leaves
-// partial states in the workspace; the CTA that finishes it last (a ticket)
-// joins them in CTA order, so results repeat bit for bit.
+// and the entries, the partial states) and the ticket are the time.  A unit cut
+// between CTAs leaves partial states in the workspace; the CTA that finishes it
+// last (a ticket) joins them in CTA order, so results repeat bit for bit.
 #pragma once
 
 #include <cuda_bf16.h>

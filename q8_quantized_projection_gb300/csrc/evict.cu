@@ -11,8 +11,7 @@
 // longer; the CTA has a lane for eight keys of a row where 256 or 512 threads do
 // (2048 of 4096 entries of 8 heads of 128 f32 values, moves included: 1024 threads
 // 16.2 us, 512 14.4; 150 of 300 of 64 x 8 heads of 64: 1024 49, 256 30).  Bound by
-// the latency of its steps: 8 us at 4096 entries a row and head, 12 at 8192, 16 at
-// 32768.
+// the latency of its steps: 12 us at 8192 entries a row and head, 16 at 32768.
 //
 // evict_move_kernel: K, V and acc to the front, in place and in order.  Entry
 // j of the result comes from an entry idx[j] >= j.  A CTA owns a column slice

@@ -14,27 +14,32 @@
 //
 // Top-k of up to some hundreds: the lanes' maxima give a logit (`reach`) that
 // at least k tokens reach; the tokens that reach it, 600 of 128256 for k = 50,
-// are listed, and the first CTA does the rest on the list alone.
+// are listed, and the first CTA does the rest on the list alone (what a
+// histogram leaves of it, up to 128 tokens, by comparing every pair).
 //
 // Otherwise a cut (the k-th largest; the end of the nucleus) is found without
 // sorting the row: a histogram of 1024 bins linear in x (counts, or masses to
 // 2^-21) names the bin that holds it; an exact pass sums what lies above that
-// bin and lists the bin's tokens, which the first CTA sorts (some hundreds).
+// bin and lists the bin's tokens (some hundreds); every CTA takes the whole list,
+// and each of its own tokens adds up what goes before it, which says whether it
+// stays and whether it is the cut.  Longer lists are sorted by the first CTA.
 // Where the list is too long (thousands of equal logits), a binary search over
 // the 32 bits of the ordered logits finds the cut instead, with exact sums at
 // each step.
 //
 // What bounds it.  One row: latency, of exchanges and of code that runs once
 // (no arithmetic of 64-bit floats: at 2 lanes a clock and SM, one division in
-// every thread cost 5 us).  A batch: instructions, 45 for an exact weight and
-// about 200 a token in all against 4 bytes read, at 0.45 issued a clock and
-// scheduler; barriers are most of the rest.
+// every thread cost 5 us).  A batch: the same latency, 17 of a CTA's 39 us, in two
+// waves of clusters (64 rows of 128256, two CTAs an SM), then the instructions, 45
+// for an exact weight and about 170 a token in all against 4 bytes read, at 0.49
+// issued a clock and scheduler, and the histogram's shared atomics, 5 of the 39.
+// (An exponent of 5 instructions in place of 16 gained 0.2 us of the 84.)
 //
-// Measured (device time): 3 rows of 1001 tokens 11 us, one of 128256 with every
-// filter 18 us, 64 of 128256 with top-p 100 us, 256 of 32003 with settings of
-// their own 75 us.  CTAs of 512 threads and parts of 16 K tokens, two CTAs an
-// SM: 256 threads and 8 K (clusters of 16) 137 us, 1024 and 32 K 103 us on the
-// 64 rows, 86 and 93 on the 256.
+// Measured (device time): 3 rows of 1001 tokens 9 us, one of 128256 with every
+// filter 15 us, 64 of 128256 with top-p 85 us, 256 of 32003 with settings of
+// their own 69 us.  CTAs of 512 threads and two CTAs an SM: on an earlier form at
+// 100 us for the 64 rows, 256 threads and parts of 8 K (clusters of 16) took 137
+// us, 1024 and 32 K 103 us, and 86 and 93 on the 256 rows at 75 us.
 #include <cooperative_groups.h>
 #include <float.h>
 #include <math.h>
