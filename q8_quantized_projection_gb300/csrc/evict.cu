@@ -22,7 +22,7 @@
 // leaves a CTA an SM, 64 bytes at least (8 heads of 24576 of 32768 f32 entries
 // in 4 rows: 128 bytes 246 us; 64 bytes 40 us and 256 bytes 60 us more).  Where
 // that leaves few CTAs (few rows and heads) and long walks, a cluster of up to 8
-// walks a slice together, with a cluster barrier a batch.
+// walks a slice together, with a cluster barrier a batch, and slices are wider.
 // Bound: HBM, each moved byte read and written once; measured there 6.6 TB/s
 // (read and write), and 9 us for 2048 of 4096 entries of one row.
 #include <cooperative_groups.h>
@@ -364,14 +364,22 @@ cudaError_t launch_evict(const EvictArgs& a, const LaunchCtx& ctx) {
     const auto slices_at = [&](int log) { return (chunks + (1 << log) - 1) >> log; };
     while (lanes_log > 2 && ((1 << (lanes_log - 1)) >= chunks || units * 2 * slices_at(lanes_log) < ctx.num_sms))
         --lanes_log;
-    const int slices = slices_at(lanes_log);
     // where even those leave an SM one CTA and a long walk, clusters walk
     // together: up to 5 CTAs an SM in all, three batches each at least (1 x 8 heads
     // of 64 f16 values, 41475 of 55887 entries: 123 us alone, 57 in eights; 16 x 8
-    // heads of 128, two CTAs an SM: 76 alone, 96 in pairs)
-    const int64_t ctas = units * 2 * slices, batch = int64_t(512 >> lanes_log) * kBatch;
+    // heads of 128, two CTAs an SM: 76 alone, 96 in pairs); and wider slices then,
+    // while eights of them leave five CTAs to four SMs (3 x 2 heads of 128 f32 values,
+    // 16144 of 47256: 64 bytes 66 us, 128 64, 256, 192 CTAs, 59, 512, 96 CTAs, 93)
+    const auto few = [&](int log) { return units * 2 * slices_at(log) <= ctx.num_sms + ctx.num_sms / 10; };
+    const auto batch_at = [&](int log) { return int64_t(512 >> log) * kBatch; };
+    while (few(lanes_log) && lanes_log < 5 && (1 << lanes_log) < chunks &&
+           units * 2 * slices_at(lanes_log + 1) * kMaxCluster * 4 >= 5 * int64_t(ctx.num_sms) &&
+           a.budget >= 3 * batch_at(lanes_log + 1) * kMaxCluster)
+        ++lanes_log;
+    const int slices = slices_at(lanes_log);
+    const int64_t ctas = units * 2 * slices, batch = batch_at(lanes_log);
     int size = 1;
-    while (size < kMaxCluster && ctas <= ctx.num_sms + ctx.num_sms / 10 && ctas * size * 2 <= 5 * int64_t(ctx.num_sms) &&
+    while (size < kMaxCluster && few(lanes_log) && ctas * size * 2 <= 5 * int64_t(ctx.num_sms) &&
            a.budget >= 3 * batch * size * 2)
         size *= 2;
     if (size > 1) return launch_move<true, 512>(a, size, elt, lanes_log, slices, ctx);

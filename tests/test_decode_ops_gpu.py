@@ -459,6 +459,15 @@ def test_evict_long_rows(n, budget, sinks, recent, in_place):
     Evict("bf16", [n - 1, n // 2], 1, 8, n, budget, sinks, recent, seed=n).check(in_place)
 
 
+@pytest.mark.parametrize("kv,rows,heads,dim,n,budget", [
+    ("f16", 1, 8, 256, 9000, 7000), ("f32", 3, 2, 128, 12000, 5000), ("bf16", 2, 8, 80, 8000, 6501),
+    ("f32", 1, 8, 24, 9000, 4000), ("bf16", 1, 2, 200, 20000, 12345)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_walks_of_clusters(kv, rows, heads, dim, n, budget, in_place):
+    """Few slices, narrow and wide ones, whose clusters walk together."""
+    Evict(kv, [n - 1 - 700 * m for m in range(rows)], heads, dim, n, budget, 4, 900, seed=n + dim).check(in_place)
+
+
 def test_evict_rows_at_most_the_budget_stay():
     e = Evict("f32", [9, 0, -1, 5], 2, 16, 12, 10, sinks=2, recent=2)
     k = e.k.clone()
