@@ -259,16 +259,21 @@ def _maybe(what, t, dtype, shape, device):
 
 def _need_rows(what, t, dtype, rows, least, device):
     """A 2-D tensor of dense rows of at least `least` values: its address and row pitch."""
+    shape = t.shape
+    if t.dtype is dtype and len(shape) == 2 and shape[0] == rows and t.get_device() == device:
+        pitch, step = t.stride()
+        if step == 1 and shape[1] >= least:
+            return t.data_ptr(), pitch if rows != 1 else shape[1]
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < least:
-        raise ValueError(f"{what} must have {rows} rows of at least {least} values, not {tuple(t.shape)}")
+    if len(shape) != 2 or shape[0] != rows or shape[1] < least:
+        raise ValueError(f"{what} must have {rows} rows of at least {least} values, not {tuple(shape)}")
     if t.get_device() != device:
         raise ValueError(f"{what} must be on cuda:{device}, not {t.device}")
     pitch, step = t.stride()
-    if step != 1 and t.shape[1] != 1:
+    if step != 1 and shape[1] != 1:
         raise ValueError(f"{what} must have dense rows")
-    return t.data_ptr(), pitch if rows != 1 else t.shape[1]
+    return t.data_ptr(), pitch if rows != 1 else shape[1]
 
 
 _torch = None
@@ -304,17 +309,18 @@ def _kv_caches(k_cache, v_cache, kv_heads):
     torch, device = _current("k_cache", k_cache)
     dtype, shape = k_cache.dtype, k_cache.shape
     kv = (Q8_KV_F32 if dtype is torch.float32 else Q8_KV_F16 if dtype is torch.float16
-          else Q8_KV_BF16 if dtype is torch.bfloat16 else -1)
-    if kv < 0:
+          else Q8_KV_BF16 if dtype is torch.bfloat16 else None)
+    if kv is None:
         raise TypeError(f"k_cache must be float32, float16 or bfloat16, not {dtype}")
     if len(shape) != 3:
         raise ValueError(f"k_cache must have shape (rows, n_pos, kv_dim), not {tuple(shape)}")
-    k_at = _need("k_cache", k_cache, dtype, shape, device)
+    if not k_cache.is_contiguous():
+        raise ValueError("k_cache must be contiguous")
     v_at = _need("v_cache", v_cache, dtype, shape, device)
     rows, n_pos, kv_dim = shape
     if kv_heads < 1 or kv_dim % kv_heads:
         raise ValueError(f"cache rows of {kv_dim} values do not hold {kv_heads} heads")
-    return torch, device, k_at, v_at, kv, rows, n_pos, kv_dim // kv_heads
+    return torch, device, k_cache.data_ptr(), v_at, kv, rows, n_pos, kv_dim // kv_heads
 
 
 def attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window=-1, sinks=0, acc=False) -> int:
