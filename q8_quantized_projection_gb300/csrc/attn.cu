@@ -14,22 +14,30 @@ constexpr int kAccThreads = 256, kAccPer = 4;
 
 // acc[m][h][i] += the sum over K/V head h's query heads of 2^(s - r) / sum.
 // Scores and weights once each: 4 bytes a head and entry against the cache's
-// hundreds.  One thread an entry, so nothing is added atomically.
+// hundreds.  One thread an entry, so nothing is added atomically.  Positions and
+// the first old values are read before the wait: the attention kernel, whose
+// scores it waits for, lets this one begin behind its own wait, so whatever wrote
+// those is done.
 __global__ void __launch_bounds__(kAccThreads) attn_acc_kernel(const AttnParams p) {
-    pdl_wait();
-    pdl_launch_dependents();
     const AttnArgs& a = p.a;
     const int64_t m = blockIdx.x / a.kv_heads, h = blockIdx.x % a.kv_heads, group = a.heads / a.kv_heads;
-    const Visible vis = visible(a.pos[m], a.n_pos, a.window, a.sinks);
+    const Visible vis = visible(__ldcg(a.pos + m), a.n_pos, a.window, a.sinks);
     float* acc = a.acc + int64_t(blockIdx.x) * a.n_pos;
     const int64_t step = int64_t(gridDim.y) * kAccThreads * kAccPer;
-    for (int64_t v0 = int64_t(blockIdx.y) * kAccThreads * kAccPer + threadIdx.x; v0 < vis.nvis; v0 += step) {
-        float w[kAccPer] = {}, old[kAccPer];
+    int64_t v0 = int64_t(blockIdx.y) * kAccThreads * kAccPer + threadIdx.x;
+    float old[kAccPer];
+    const auto fetch = [&] {
 #pragma unroll
         for (int j = 0; j < kAccPer; ++j) {
             const int64_t v = v0 + j * kAccThreads;
-            if (v < vis.nvis) old[j] = acc[v + (v < vis.ns ? 0 : vis.gap)];
+            if (v < vis.nvis) old[j] = __ldcg(acc + v + (v < vis.ns ? 0 : vis.gap));
         }
+    };
+    fetch();
+    pdl_wait();
+    pdl_launch_dependents();
+    while (v0 < vis.nvis) {
+        float w[kAccPer] = {};
 #pragma unroll 4
         for (int64_t g = m * a.heads + h * group; g < m * a.heads + (h + 1) * group; ++g) {
             const float2 ml = p.ml[g];
@@ -45,6 +53,8 @@ __global__ void __launch_bounds__(kAccThreads) attn_acc_kernel(const AttnParams 
             const int64_t v = v0 + j * kAccThreads;
             if (v < vis.nvis) acc[v + (v < vis.ns ? 0 : vis.gap)] = old[j] + w[j];
         }
+        v0 += step;
+        fetch();
     }
 }
 
