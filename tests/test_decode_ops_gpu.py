@@ -637,6 +637,21 @@ def test_sample_cuts_among_equal_logits(n, many, sort):
     check_draw(x, u, k=[1700, 1234, 1500, 1801, 1111, 1899], p=p)
 
 
+@pytest.mark.parametrize("n", [2, 127, 128, 129, 6000, 128256])
+@pytest.mark.parametrize("allowed", [1, 2, 17, 128, 129])
+def test_sample_few_tokens_allowed(n, allowed):
+    """A mask that leaves few tokens of a row, as a grammar does."""
+    t = torch()
+    x = logits(6, n, spread=2.5, seed=n + allowed)
+    if allowed < n:
+        order = t.rand(6, n, device="cuda", generator=t.Generator(device="cuda").manual_seed(n)).argsort(dim=1)
+        x = x.scatter(1, order[:, allowed:], -math.inf).contiguous()
+    u = [0.0, 0.21, 0.5, 0.77, 0.93, 0.9999]
+    check_draw(x, u)
+    check_draw(x, u, p=[0.3, 0.6, 0.9, 0.95, 0.99, 0.5], t=[1.0, 0.5, 2.0, 3.0, 0.7, 1.3])
+    check_draw(x, u, k=[3, 0, 50, 127, 1, 128], p=[0.9, 0.8, 1.0, 0.7, 0.6, 0.99], mp=[0.0, 0.2, 0.05, 0.0, 0.1, 0.01])
+
+
 def test_sample_shares_next_to_a_border():
     """Nuclei that end a few steps of binary32 beside a token's border, tokens far apart."""
     t = torch()
