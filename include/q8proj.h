@@ -398,7 +398,8 @@ size_t kv_evict_workspace(int64_t rows, int64_t kv_heads, int64_t budget);
  * value before that, and their sums are exact: a row's token depends on
  * nothing but its own row and settings.
  * 1 <= rows <= Q8_MAX_ROWS, 1 <= N <= 2^20, logits 16-byte aligned, the
- * others 4-byte.  No workspace.
+ * others 4-byte; tok, prob and kept overlap nothing else (Q8_ERR_ARG).  No
+ * workspace.
  */
 q8_status head_sample(const float* logits, int64_t ldl, int64_t rows, int64_t N, const float* u,
                       const float* temperature, const int32_t* top_k, const float* top_p,

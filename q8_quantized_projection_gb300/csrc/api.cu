@@ -598,6 +598,14 @@ q8_status head_sample(const float* logits, int64_t ldl, int64_t rows, int64_t N,
     for (const void* p : per_row)
         if (reinterpret_cast<uintptr_t>(p) & 3u) return Q8_ERR_ALIGN;
     if (!aligned16(logits)) return Q8_ERR_ALIGN;
+    // every output is disjoint from every other buffer: a row's first CTA may write its
+    // results while the others have not read the row's settings yet
+    const size_t rn = size_t(rows) * 4;
+    for (int i = 5; i < 8; ++i) {
+        if (overlaps2(per_row[i], rn, logits, size_t((rows - 1) * ldl + N) * 4)) return Q8_ERR_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlaps2(per_row[i], rn, per_row[j], rn)) return Q8_ERR_ARG;
+    }
     LaunchCtx ctx;
     q8_status st = make_ctx(stream, ctx);
     if (st != Q8_OK) return st;

@@ -129,6 +129,17 @@ def test_head_sample_refuses(lib, over, status):
     assert sample(lib, **over) == status
 
 
+@pytest.mark.parametrize("over", [
+    dict(prob=P(12)), dict(prob=off(P(12), 4)), dict(prob=off(P(11), -4)), dict(prob=P(14)), dict(prob=P(15)),
+    dict(tok=P(13)), dict(tok=P(12)), dict(tok=P(11)), dict(kept=P(13)), dict(kept=P(12)),
+    dict(prob=P(16)), dict(kept=P(16)), dict(kept=off(P(17), 4)),
+    dict(tok=Q), dict(prob=off(Q, 4 * 199)), dict(kept=off(Q, 400)), dict(prob=off(Q, -4)),
+    dict(tok=P(13), prob=None, kept=None), dict(ldl=1 << 20, tok=off(Q, 4 << 20))])
+def test_head_sample_refuses_outputs_that_overlap(lib, over):
+    """In place: one CTA of a row could read settings that another has written over."""
+    assert sample(lib, **over) == 1
+
+
 def test_binding_refuses_host_tensors():
     torch = pytest.importorskip("torch")
     x = torch.zeros(1, 8)
