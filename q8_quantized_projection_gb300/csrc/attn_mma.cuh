@@ -1,25 +1,30 @@
 // attn_mma.cuh -- the attention kernels over 16-bit caches: the products on the
-// matrix instructions (mma.m16n8k16).
+// matrix instructions (mma.m16n8k16; m16n8k8 for f16's second product).
 //
 // With the entries of a stage as the n of the first product and the k of the
 // second, a block of at most 8 query heads fills half of m = 16.  The other half
-// takes what the operand's 16-bit rounding lost: rows 0-7 hold q (then p) rounded,
-// rows 8-15 the rest of it rounded, so one instruction gives both parts' products
-// (f16: 22 bits; bf16: 16, and a second instruction adds 8 more).  K and V enter
-// as they are.  The accumulator layout of the scores is the operand layout of the
-// weights, and all that a lane holds belongs to one query head: no exchange
-// between lanes but two shuffles where a reference moves.
+// takes what the operand's rounding lost: rows 0-7 hold q (then p) rounded, rows
+// 8-15 the rest of it rounded, so one instruction gives both parts' products (f16:
+// 22 bits; bf16: 16, and a second instruction adds 8 more).  K and V enter as they
+// are.  The accumulator layout of the scores is the operand layout of the weights,
+// and all that a lane holds belongs to one query head: no exchange between lanes
+// but two shuffles where a reference moves.
 //
-// Precision.  q is brought to [2^13, 2^14) by a power of two a head (f16), p is
-// at most 2^8 and carried as 2^7 p, so that what falls below f16's subnormals is
-// below 2^-32 of the largest weight.  The instruction truncates its sums; chains
-// are kept short (every other step of a score; 64 entries of o) and joined by
-// rounded binary32 additions: measured 2e-7 where one chain of 512 steps is 1e-5
-// off.  A part times infinity is NaN, so a warp whose state is not finite computes
-// its entries again, one by one, by the formula.
+// Precision.  Over f16 caches q is brought to [2^13, 2^14) by a power of two a
+// head.  Weights span more than f16 holds, and where the largest stand on entries
+// of no value (as a row's first tokens often are) the output is made of the small
+// ones alone; so p enters the second product in two parts of tf32, 11 bits each
+// and binary32's exponents, and V converted to it, exactly: m16n8k8, twice as many
+// instructions (32 rows of 4096 entries, 8 K/V heads of 64, 128 and 256 values (16
+// rows): 59.9, 98.7 and 109 us; with p in two parts of f16, which lost bits below
+// 2^-16 of the largest weight, 58.7, 97.4 and 108).  The instruction truncates its
+// sums; chains are kept short (every other step of a score; 64 entries of o) and
+// joined by rounded binary32 additions: measured 2e-7 where one chain of 512 steps
+// is 1e-5 off.  A part times infinity is NaN, so a warp whose state is not finite
+// computes its entries again, one by one, by the formula.
 //
-// What bounds it: HBM.  A stage of 16 bf16 entries of 128 values is 64
-// instructions of 2 clocks an SM, 8 clocks an entry against 23 for its bytes
+// What bounds it: HBM.  A stage of 16 entries of 128 values is 64 instructions
+// (bf16; 48 of f16) of 2 clocks an SM, 8 clocks an entry against 23 for its bytes
 // (6.6 TB/s); on the lanes' FMA path eight query heads take 40.  Heads of 256
 // values: 16 rows of 4096 entries, 8 K/V heads of 8 query heads, bf16 113 us, f16
 // 109 (4.8 and 4.9 TB/s; on the lanes 146 and 151).
@@ -43,6 +48,22 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// m16n8k8: a 10-bit mantissa and binary32's exponents (what f16 holds, exactly).
+__device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// x rounded to that format; x becomes what the rounding lost.
+__device__ __forceinline__ uint32_t round_tf32(float& x) {
+    uint32_t w;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(w) : "f"(x));
+    x -= __uint_as_float(w);
+    return w;
 }
 
 template <bool TRANS>
@@ -308,26 +329,37 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
             for (int j = 0; j < 4; ++j) {
                 x[u][j] = x[u][j] == -INFINITY ? 0.0f : ex2(x[u][j] - ref);
                 l += x[u][j];
-                if constexpr (!BF) x[u][j] *= 128.0f;
             }
-            uint32_t pa[4], pl[4] = {};
-            pa[0] = round_pair<KV>(x[u][0], x[u][1]);
-            pa[1] = round_pair<KV>(x[u][0], x[u][1]);
-            pa[2] = round_pair<KV>(x[u][2], x[u][3]);
-            pa[3] = round_pair<KV>(x[u][2], x[u][3]);
+            uint32_t pa[4], pl[4] = {};      // f16: of entries 0-7 and 8-15
             if constexpr (BF) {
+                pa[0] = round_pair<KV>(x[u][0], x[u][1]);
+                pa[1] = round_pair<KV>(x[u][0], x[u][1]);
+                pa[2] = round_pair<KV>(x[u][2], x[u][3]);
+                pa[3] = round_pair<KV>(x[u][2], x[u][3]);
                 pl[0] = round_pair<KV>(x[u][0], x[u][1]);
                 pl[2] = round_pair<KV>(x[u][2], x[u][3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    pa[j] = round_tf32(x[u][j >> 1]);
+                    pl[j] = round_tf32(x[u][2 + (j >> 1)]);
+                }
             }
 #pragma unroll
             for (int t = 0; t < VS; ++t) {
                 uint32_t v[4];
                 ldmatrix4<true>(v, T::column(st + v_at, 2 * t) + u * 16 * T::VPITCH);
-                mma16<KV>(o[2 * t], pa, v[0], v[1]);
-                mma16<KV>(o[2 * t + 1], pa, v[2], v[3]);
                 if constexpr (BF) {
+                    mma16<KV>(o[2 * t], pa, v[0], v[1]);
+                    mma16<KV>(o[2 * t + 1], pa, v[2], v[3]);
                     mma16<KV>(o[2 * t], pl, v[0], v[1]);
                     mma16<KV>(o[2 * t + 1], pl, v[2], v[3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {        // (a lane's two entries as k and k + 4)
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
+                        mma8(o[2 * t + (j >> 1)], j & 1 ? pl : pa, __float_as_uint(f.x), __float_as_uint(f.y));
+                    }
                 }
             }
         }
@@ -352,10 +384,7 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
     }
     float* so = reinterpret_cast<float*>(s.ring) + g * T::DV + c2;
 #pragma unroll
-    for (int t = 0; t < 2 * VS; ++t) {
-        constexpr float f = BF ? 1.0f : 1.0f / 128.0f;
-        *reinterpret_cast<float2*>(so + 8 * t) = make_float2(sum[t][0] * f, sum[t][1] * f);
-    }
+    for (int t = 0; t < 2 * VS; ++t) *reinterpret_cast<float2*>(so + 8 * t) = make_float2(sum[t][0], sum[t][1]);
 }
 
 // KS: steps of 16 values a head.  SPLIT 2: two warps take the same entries, all of

@@ -1,0 +1,39 @@
+"""The precision checks of attn_decode find what they are there to find: arithmetic of
+fewer bits, and parts of a row that are lost, fall outside their bounds (CPU, numpy)."""
+import numpy as np
+import pytest
+
+import attn_precision as ap
+
+
+def out_of(p, v, w):
+    """out from weights w (of any precision) over the sum of exact ones p."""
+    return np.einsum("mgn,mnd->mgd", w, v) / p.sum(-1)[..., None]
+
+
+def unscaled(q, k):
+    s = np.einsum("mgd,mnd->mgn", q, k)
+    return np.exp2(s - s.max(-1, keepdims=True))
+
+
+def two_parts(x, to):
+    hi = to(x)
+    return hi + to(x - hi)
+
+
+def test_scale_takes_scores_to_units_of_log_2():
+    assert np.float32(float(np.float32(ap.SCALE)) * 1.4426950408889634) == 1.0
+
+
+@pytest.mark.parametrize("n,at", [(16, 0), (300, 5)])
+def test_small_weights_need_more_than_two_parts_of_f16(n, at):
+    q, k, v = ap.small_weights(8, 64, n, at)
+    want, _ = ap.exact(q, k, v)
+    p, tol = unscaled(q, k), ap.small_weights_bound(want, n)
+    got = out_of(p, v, two_parts(p * 128, ap.to_f16) / 128)        # 22 bits of the largest weights only
+    bad = (np.abs(got - want) > tol).any(axis=(1, 2))
+    assert bad[3:].all()                                            # from 2^-12 to 2^-24 on
+    hi = p * 128
+    lo = ap.to_f16((hi - ap.to_f16(hi)) * 2048) / 2048              # the second part 2^11 lower
+    assert (np.abs(out_of(p, v, (ap.to_f16(hi) + lo) / 128) - want) > tol).any()
+    assert np.all(np.abs(out_of(p, v, p.astype(np.float32).astype(np.float64)) - want) <= tol)

@@ -1,0 +1,43 @@
+"""GPU tests of attn_decode's precision: inputs whose result hangs on low bits or on small
+weights (attn_precision.py has them and their bounds)."""
+import numpy as np
+import pytest
+
+import attn_precision as ap
+from q8_quantized_projection_gb300 import native
+
+pytestmark = pytest.mark.gpu
+KVS, DIMS = ["f32", "f16", "bf16"], [64, 80, 128, 200, 256]
+
+
+def run(kv, q, k, v, scale=ap.SCALE):
+    """attn_decode of q [rows][heads][D] on one K/V head's k, v [rows][n][D]: out, weights."""
+    import torch as t
+    rows, heads, dim = q.shape
+    n = k.shape[1]
+    ty = {"f32": t.float32, "f16": t.float16, "bf16": t.bfloat16}[kv]
+    dev = lambda x, ty: t.from_numpy(np.ascontiguousarray(x)).to("cuda").to(ty)  # noqa: E731
+    out, acc = t.empty(rows, heads * dim, device="cuda"), t.zeros(rows, 1, n, device="cuda")
+    kd, vd = dev(k, ty), dev(v, ty)
+    assert np.array_equal(vd.double().cpu().numpy(), v)
+    native.attn_decode(dev(q.reshape(rows, -1), t.float32), kd, vd, t.full((rows,), n - 1, dtype=t.int32, device="cuda"),
+                       out, native.attn_workspace(rows, heads, 1, dim, n, acc=True), heads, 1, scale=scale, acc=acc)
+    assert native.q8_device_error() == 0
+    return out.double().cpu().numpy().reshape(rows, heads, dim), acc.double().cpu().numpy()[:, 0], kd.double().cpu().numpy()
+
+
+def check(got, want, tol):
+    assert np.all(np.abs(got - want) <= tol), float(np.max(np.abs(got - want) / np.maximum(tol, 1e-300)))
+
+
+@pytest.mark.parametrize("kv", KVS)
+@pytest.mark.parametrize("heads", [2, 4, 5, 8])
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("n,at", [(16, 0), (300, 5)])
+def test_small_weights_beside_large_ones_of_no_value(kv, heads, dim, n, at):
+    q, k, v = ap.small_weights(heads, dim, n, at)
+    want, p = ap.exact(q, k, v)
+    got, acc, _ = run(kv, q, k, v)
+    check(got, want, ap.small_weights_bound(want, n))
+    # (acc: the heads' sum, one rounding a head and one into acc)
+    check(acc, p.sum(1), ap.small_weights_bound(p.sum(1), n) + (heads + 1) * ap.U * p.sum(1))
