@@ -318,7 +318,9 @@ size_t head_argmax_noalloc_scratch_bytes(void);
  * same and sets device error 2.  What an entry that is not visible holds
  * (NaN, infinity) does not matter.  Scores, weights and sums are binary32
  * (the sums before they are divided, of up to 2^8 a visible entry: cache values
- * below 2^88 cannot overflow them);
+ * below 2^88 cannot overflow them).  Over 16-bit caches with five query heads a
+ * K/V head and more, q and the weights enter the products with 22 bits at least,
+ * and sums of up to 128 products are truncated where binary32 would round;
  * the result does not depend on what else runs (no atomics on values).
  * 1 <= rows <= Q8_MAX_ROWS; heads a multiple of kv_heads, heads <= 1024;
  * head_dim a multiple of 8, 8 <= head_dim <= 256; 1 <= n_pos <= 2^31 - 1, each

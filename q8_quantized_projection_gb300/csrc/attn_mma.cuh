@@ -234,6 +234,9 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
         scale = __int_as_float(e << 23);
         back = __int_as_float((254 - e) << 23);
     }
+    // (the second part is 2^-11 of the first at most: brought up by that, so that f16's
+    // subnormals cost values down to 2^-28 of the largest none of their 22 bits)
+    constexpr float LOW_SCALE = BF ? 1.0f : 2048.0f;
     // (the third part of 256 values lies in shared memory, each lane's its own)
     constexpr bool LOW = BF && T::SPLIT > 1;
     __shared__ uint2 s_low[LOW ? KS * 32 : 1];
@@ -244,6 +247,7 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
         for (int h = 0; h < 2; ++h) {
             float x = q[16 * k + 8 * h] * scale, y = q[16 * k + 8 * h + 1] * scale;
             qa[k][2 * h] = round_pair<KV>(x, y);
+            x *= LOW_SCALE, y *= LOW_SCALE;
             qa[k][2 * h + 1] = round_pair<KV>(x, y);
             if constexpr (LOW) {
                 const uint32_t low = round_pair<KV>(x, y);
@@ -300,7 +304,7 @@ __device__ __forceinline__ void mma_states(const Segment& s) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float(&d)[2][4] = c[j >> 1];
-                float y = (d[0][j & 1] + d[1][j & 1]) + (d[0][2 + (j & 1)] + d[1][2 + (j & 1)]);
+                float y = fmaf(d[0][2 + (j & 1)] + d[1][2 + (j & 1)], 1.0f / LOW_SCALE, d[0][j & 1] + d[1][j & 1]);
                 if constexpr (!BF) y *= back;
                 const uint32_t v = vb + 16 * u + (j >> 1) * 8 + c2 + (j & 1);
                 if (scores && v < s.v_end) scores[v] = y;

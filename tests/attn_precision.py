@@ -53,3 +53,20 @@ def small_weights(heads, dim, n, at):
 def small_weights_bound(want, n):
     # positive terms: the exponential and the parts, n truncated additions, the division
     return (4 + 4 + 2 * n + 4 + n + 4) * U * want
+
+
+def small_values_of_q(heads, dim):
+    """A first value of 2^12 that meets keys of 0 (it sets what a head's q is measured by), the
+    others some 2^-14, that meet keys of 2^15 one by one: scores of 2 to 4.  V: the unit matrix."""
+    r = np.random.default_rng(dim + 1)
+    q = 2.0 ** -14 * (1 + r.integers(0, 1 << 23, (1, heads, dim)) * 2.0 ** -23)
+    q[:, :, 0] = 2.0 ** 12
+    k, v = np.zeros((1, dim - 1, dim)), np.zeros((1, dim - 1, dim))
+    i = np.arange(dim - 1)
+    k[0, i, i + 1], v[0, i, i] = 2.0 ** 15, 1
+    return q, k, v
+
+
+def small_values_of_q_bound(want, dim):
+    # scores of at most 4 off by 2^-22 (q's parts) and u (a difference), ln2 each
+    return (2 * (16 * U + 4 * U + 8 * U) + (3 * dim + 8) * U) * want

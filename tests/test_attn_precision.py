@@ -37,3 +37,15 @@ def test_small_weights_need_more_than_two_parts_of_f16(n, at):
     lo = ap.to_f16((hi - ap.to_f16(hi)) * 2048) / 2048              # the second part 2^11 lower
     assert (np.abs(out_of(p, v, (ap.to_f16(hi) + lo) / 128) - want) > tol).any()
     assert np.all(np.abs(out_of(p, v, p.astype(np.float32).astype(np.float64)) - want) <= tol)
+
+
+@pytest.mark.parametrize("dim", [64, 80, 256])
+def test_scores_need_the_small_values_of_q(dim):
+    q, k, v = ap.small_values_of_q(8, dim)
+    want, _ = ap.exact(q, k, v)
+    tol = ap.small_values_of_q_bound(want, dim)
+    x = two_parts(q * 2, ap.to_f16) / 2                    # (brought to 2^13)
+    assert (np.abs(ap.exact(x, k, v)[0] - want) > tol).any(-1).all()
+    hi = ap.to_f16(q * 2)
+    x = (hi + ap.to_f16((q * 2 - hi) * 2048) / 2048) / 2   # the second part 2^11 lower
+    assert np.all(np.abs(ap.exact(x, k, v)[0] - want) <= tol)

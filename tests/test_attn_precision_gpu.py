@@ -41,3 +41,12 @@ def test_small_weights_beside_large_ones_of_no_value(kv, heads, dim, n, at):
     check(got, want, ap.small_weights_bound(want, n))
     # (acc: the heads' sum, one rounding a head and one into acc)
     check(acc, p.sum(1), ap.small_weights_bound(p.sum(1), n) + (heads + 1) * ap.U * p.sum(1))
+
+
+@pytest.mark.parametrize("kv", KVS)
+@pytest.mark.parametrize("heads", [4, 7, 8])
+@pytest.mark.parametrize("dim", DIMS)
+def test_small_values_of_q_beside_a_large_one(kv, heads, dim):
+    q, k, v = ap.small_values_of_q(heads, dim)
+    want, _ = ap.exact(q, k, v)
+    check(run(kv, q, k, v)[0], want, ap.small_values_of_q_bound(want, dim))
