@@ -55,6 +55,45 @@ def small_weights_bound(want, n):
     return (4 + 4 + 2 * n + 4 + n + 4) * U * want
 
 
+def cancelling_weights(heads, dim, n):
+    """Values of +1 and -1 in turn, weights of 1 and 1 - d in turn (n even), where d is one of
+    2^-10 (1 + (2j + 1) 2^-8): 1 - d needs 18 bits, and out is d / (2 - d)."""
+    d = 2.0 ** -10 * (1 + (2 * (np.arange(heads) % 8) + 1) * 2.0 ** -8)
+    q, k, v = np.zeros((1, heads, dim)), np.zeros((1, n, dim)), np.ones((1, n, dim))
+    q[0, :, 1] = (-np.log2(1 - d)).astype(np.float32)
+    k[:, 1::2, 1] = -1
+    v[:, 1::2] = -1
+    return q, k, v
+
+
+def cancelling_weights_bound(want, n):
+    # half of the entries are off by the exponential (4u) and the parts (4u), and a pair's
+    # two additions by 2u of its weight, 1: each counts half of that in out; and out's own part
+    return 6 * U + (n + 16) * U * np.abs(want)
+
+
+def low_parts_of_q(kv, heads, dim):
+    """Entry i has keys K and -K at values i and i + 1, where q is 1 + m 2^-15 + a 2^-23, with
+    m the head's (130 to 186) and |a| <= 64 each value's own: the leading 16 bits cancel, and
+    the score is K 2^-23 (a_i - a_i+1) without an error.  V is the unit matrix: out is p."""
+    r = np.random.default_rng(dim)
+    K = 2.0 ** 15 if kv == "f16" else 2.0 ** 19            # (f16 ends at 2^16)
+    m, a = 130 + 8 * (np.arange(heads) % 8), r.integers(-64, 65, (heads, dim))
+    q = (1 + m[:, None] * 2.0 ** -15 + a * 2.0 ** -23)[None]
+    k, v = np.zeros((1, dim - 1, dim)), np.zeros((1, dim - 1, dim))
+    i = np.arange(dim - 1)
+    k[0, i, i], k[0, i, i + 1], v[0, i, i] = K, -K, 1
+    return q, k, v
+
+
+def low_parts_of_q_bound(want, kv, heads, dim):
+    # scores below 2^3.1 and exact, a difference of two rounded: 16 ln2 u; all of that once
+    # more in the sum.  An f16 cache's q holds 22 bits of each value at least when eight
+    # heads share it: two values off by 2^-23, times K, ln2.
+    ds = 2 * 2.0 ** -23 * 2.0 ** 15 * math.log(2) if kv == "f16" and heads > 4 else 0
+    return (2 * (1.01 * ds + 12 * U + 8 * U) + (3 * dim + 8) * U) * want + 2.0 ** -100
+
+
 def small_values_of_q(heads, dim):
     """A first value of 2^12 that meets keys of 0 (it sets what a head's q is measured by), the
     others some 2^-14, that meet keys of 2^15 one by one: scores of 2 to 4.  V: the unit matrix."""

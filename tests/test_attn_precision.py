@@ -39,6 +39,34 @@ def test_small_weights_need_more_than_two_parts_of_f16(n, at):
     assert np.all(np.abs(out_of(p, v, p.astype(np.float32).astype(np.float64)) - want) <= tol)
 
 
+@pytest.mark.parametrize("n", [64, 600])
+def test_cancelling_weights_need_18_bits(n):
+    q, k, v = ap.cancelling_weights(8, 64, n)
+    want, _ = ap.exact(q, k, v)
+    p, tol = unscaled(q, k), ap.cancelling_weights_bound(want, n)
+    for w in (ap.to_bf16(p), two_parts(p, ap.to_bf16), ap.to_f16(p)):
+        assert (np.abs(out_of(p, v, w) - want) > tol).any(-1).all()             # in every head
+    assert np.all(np.abs(out_of(p, v, p.astype(np.float32).astype(np.float64)) - want) <= tol)
+
+
+@pytest.mark.parametrize("dim", [64, 80, 200, 256])
+def test_scores_need_the_low_parts_of_q(dim):
+    for kv, to in (("bf16", ap.to_bf16), ("f16", ap.to_f16)):
+        q, k, v = ap.low_parts_of_q(kv, 8, dim)
+        assert np.array_equal(q, q.astype(np.float32))
+        want, _ = ap.exact(q, k, v)
+        tol = ap.low_parts_of_q_bound(want, kv, 8, dim)
+        less = [to(q)] if kv == "f16" else [to(q), two_parts(q, to)]
+        if kv == "bf16":          # one step of 16 values without its third part, or with its neighbour's
+            low = q - two_parts(q, to)
+            for step in range((dim + 15) // 16):
+                other = low.copy()
+                other[:, :, 16 * step:16 * step + 16] = 0
+                less.append(two_parts(q, to) + other)
+        for x in less:
+            assert (np.abs(ap.exact(x, k, v)[0] - want) > tol).any(-1).all()
+
+
 @pytest.mark.parametrize("dim", [64, 80, 256])
 def test_scores_need_the_small_values_of_q(dim):
     q, k, v = ap.small_values_of_q(8, dim)

@@ -44,6 +44,28 @@ def test_small_weights_beside_large_ones_of_no_value(kv, heads, dim, n, at):
 
 
 @pytest.mark.parametrize("kv", KVS)
+@pytest.mark.parametrize("heads", [4, 8])
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("n", [64, 600])
+def test_weights_that_cancel(kv, heads, dim, n):
+    q, k, v = ap.cancelling_weights(heads, dim, n)
+    want, _ = ap.exact(q, k, v)
+    check(run(kv, q, k, v)[0], want, ap.cancelling_weights_bound(want, n))
+
+
+@pytest.mark.parametrize("kv", KVS)
+@pytest.mark.parametrize("heads", [4, 7, 8])
+@pytest.mark.parametrize("dim", DIMS)
+def test_low_parts_of_q(kv, heads, dim):
+    q, k, v = ap.low_parts_of_q(kv, heads, dim)
+    want, p = ap.exact(q, k, v)
+    got, acc, kd = run(kv, q, k, v)
+    assert np.array_equal(kd, k)
+    check(got, want, ap.low_parts_of_q_bound(want, kv, heads, dim))
+    check(acc, p.sum(1), ap.low_parts_of_q_bound(p.sum(1), kv, heads, dim) + (heads + 1) * ap.U * p.sum(1))
+
+
+@pytest.mark.parametrize("kv", KVS)
 @pytest.mark.parametrize("heads", [4, 7, 8])
 @pytest.mark.parametrize("dim", DIMS)
 def test_small_values_of_q_beside_a_large_one(kv, heads, dim):
