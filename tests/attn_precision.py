@@ -109,3 +109,21 @@ def small_values_of_q(heads, dim):
 def small_values_of_q_bound(want, dim):
     # scores of at most 4 off by 2^-22 (q's parts) and u (a difference), ln2 each
     return (2 * (16 * U + 4 * U + 8 * U) + (3 * dim + 8) * U) * want
+
+
+def sliced_values(n, dim):
+    """Values that are 1 in one slice of the n entries a column, 0 elsewhere: a column is its
+    slice's weight, and a part of the entries that is lost is a large part of some column."""
+    v = np.zeros((n, dim))
+    v[np.arange(n), np.arange(n) * dim // n] = 1
+    return v
+
+
+def long_row_bound(q, k, want, scale):
+    """Of a column of sliced_values.  A score: (D + 4) u sum |q k| scale at most; a weight and
+    the sum of all each carry twice that and the exponential.  Sums of positive terms: the
+    roundings of n additions are independent, 8 sqrt(n) u covers more than eight of their
+    standard deviations; the matrix instructions' truncation, in chains of 8 at most, 16u."""
+    n, dim = k.shape
+    ds = (dim + 4) * U * (np.abs(k) @ np.abs(q).T).max(0) * abs(scale)       # [heads]
+    return (2 * (2 * ds + 8 * U + 8 * math.sqrt(n) * U + 16 * U))[:, None] * want

@@ -5,6 +5,8 @@ import pytest
 
 import attn_precision as ap
 
+rng = np.random.default_rng
+
 
 def out_of(p, v, w):
     """out from weights w (of any precision) over the sum of exact ones p."""
@@ -77,3 +79,21 @@ def test_scores_need_the_small_values_of_q(dim):
     hi = ap.to_f16(q * 2)
     x = (hi + ap.to_f16((q * 2 - hi) * 2048) / 2048) / 2   # the second part 2^11 lower
     assert np.all(np.abs(ap.exact(x, k, v)[0] - want) <= tol)
+
+
+@pytest.mark.parametrize("heads,dim,n", [(1, 64, 60000), (1, 8, 70000), (3, 24, 60000), (1, 256, 40000), (8, 128, 30000)])
+def test_a_part_lost_from_a_long_row_is_seen(heads, dim, n):
+    """Any of 304 parts (two CTAs an SM) that the join of values leaves out, or weighs 1% wrong
+    where a column has few of them."""
+    r = rng(dim + n)
+    q, k = r.standard_normal((heads, dim)), r.standard_normal((n, dim))
+    v = ap.sliced_values(n, dim)
+    _, p = ap.exact(q[None] * dim ** -0.5 / ap.SCALE, k[None], v[None])
+    want = p[0] @ v
+    tol = ap.long_row_bound(q, k, want, dim ** -0.5)
+    for part in range(0, 304, 7):
+        a, b = n * part // 304, n * (part + 1) // 304
+        lost = p[0][:, a:b] @ v[a:b]
+        assert (lost > 4 * tol).any(-1).all()
+        if dim >= 64:
+            assert (0.01 * lost > tol).any(-1).all()

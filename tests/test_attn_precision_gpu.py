@@ -1,5 +1,5 @@
-"""GPU tests of attn_decode's precision: inputs whose result hangs on low bits or on small
-weights (attn_precision.py has them and their bounds)."""
+"""GPU tests of attn_decode's precision: inputs whose result hangs on low bits, on small
+weights or on every part of a long row (attn_precision.py has them and their bounds)."""
 import numpy as np
 import pytest
 
@@ -72,3 +72,21 @@ def test_small_values_of_q_beside_a_large_one(kv, heads, dim):
     q, k, v = ap.small_values_of_q(heads, dim)
     want, _ = ap.exact(q, k, v)
     check(run(kv, q, k, v)[0], want, ap.small_values_of_q_bound(want, dim))
+
+
+@pytest.mark.parametrize("kv,heads,dim,n", [
+    ("f32", 8, 256, 9000), ("f32", 8, 72, 20000), ("f32", 5, 8, 30000), ("f32", 1, 64, 60000), ("f32", 1, 8, 70000),
+    ("f32", 2, 200, 20000), ("bf16", 8, 128, 30000), ("bf16", 3, 24, 60000), ("bf16", 1, 256, 40000),
+    ("f16", 7, 40, 30000), ("f16", 4, 200, 20000), ("f16", 6, 256, 15000)])
+def test_every_part_of_a_long_row_counts(kv, heads, dim, n):
+    """V is 1 in one slice of the row a column, so that a part lost or misweighed in the join moves a column."""
+    r = np.random.default_rng(n + dim)
+    q = r.standard_normal((1, heads, dim)).astype(np.float32).astype(np.float64)
+    to = {"f32": lambda x: x.astype(np.float32).astype(np.float64), "f16": ap.to_f16, "bf16": ap.to_bf16}[kv]
+    k, v = to(r.standard_normal((1, n, dim))), ap.sliced_values(n, dim)[None]
+    scale = dim ** -0.5
+    want, p = ap.exact(q * scale / np.log(2), k, v)
+    got, acc, kd = run(kv, q, k, v, scale)
+    assert np.array_equal(kd, k)
+    check(got[0], want[0], ap.long_row_bound(q[0], k[0], want[0], scale))
+    check(acc[0], p[0].sum(0), ap.long_row_bound(q[0], k[0], p[0], scale).sum(0) + (heads + 1) * ap.U * p[0].sum(0))
