@@ -324,7 +324,7 @@ size_t head_argmax_noalloc_scratch_bytes(void);
  * the result does not depend on what else runs (no atomics on values).
  * 1 <= rows <= Q8_MAX_ROWS; heads a multiple of kv_heads, heads <= 1024;
  * head_dim a multiple of 8, 8 <= head_dim <= 256; 1 <= n_pos <= 2^31 - 1, each
- * cache at most 2^40 bytes; window >= -1, sinks >= 0; out, acc and the workspace
+ * cache at most 2^39 values; window >= -1, sinks >= 0; out, acc and the workspace
  * overlap nothing else (Q8_ERR_ARG).
  *   workspace: attn_decode_workspace(...) bytes for the same arguments (with_acc:
  *   acc is given), zeroed whole before the first call on it; every completed
@@ -332,7 +332,7 @@ size_t head_argmax_noalloc_scratch_bytes(void);
  *   kv_evict and of head_argmax too, may follow one another on one workspace
  *   (nothing else may write its first 4096 bytes).  Calls sharing it must not
  *   overlap.
- *   (0 bytes: arguments that attn_decode refuses.)
+ *   (0 bytes: sizes that attn_decode refuses.)
  */
 q8_status attn_decode(const float* q, int64_t ldq, const void* k_cache, const void* v_cache,
                       int kv_type, int64_t rows, int64_t n_pos, int64_t heads, int64_t kv_heads,

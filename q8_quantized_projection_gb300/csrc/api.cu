@@ -479,7 +479,8 @@ static q8_status check_cache(int kv_type, int64_t rows, int64_t n_pos, int64_t k
     if (rows < 1 || rows > Q8_MAX_ROWS || n_pos < 1 || n_pos > INT32_MAX) return Q8_ERR_SHAPE;
     if (kv_heads < 1 || kv_heads > kMaxHeads || dim < 8 || dim > 256 || dim % 8) return Q8_ERR_SHAPE;
     const int64_t elt = kv_type == Q8_KV_F32 ? 4 : 2;
-    if (n_pos > (int64_t(1) << 40) / (rows * kv_heads * dim * elt)) return Q8_ERR_SHAPE;
+    // (in values, so that attn_decode_workspace, which is given no type, refuses the same)
+    if (n_pos > (int64_t(1) << 39) / (rows * kv_heads * dim)) return Q8_ERR_SHAPE;
     *bytes = size_t(rows) * size_t(n_pos) * size_t(kv_heads * dim * elt);
     return Q8_OK;
 }

@@ -70,6 +70,17 @@ def test_attn_decode_workspace_sizes(lib):
         assert f(*bad) == 0
 
 
+@pytest.mark.parametrize("kv", [0, 1, 2])
+def test_attn_decode_workspace_knows_the_largest_cache(lib, kv):
+    """The workspace's size has no cache type: it is 0 exactly where the call refuses the sizes."""
+    far = dict(kv=kv, rows=256, wsb=0, **{n: C.c_void_p((i + 1) << 45) for i, n in
+                                          enumerate(("q", "k", "v", "pos", "out", "ws"))})
+    most = 1 << 25                                             # 2^39 values
+    for n_pos, status in ((most // 2 + 1, 7), (most, 7), (most + 1, 2)):
+        assert attn(lib, n_pos=n_pos, **far) == status
+        assert (lib.attn_decode_workspace(256, 8, 2, 32, n_pos, 64, 0, 0) == 0) == (status == 2)
+
+
 def evict(lib, **over):
     a = dict(k=K, v=V, kv=0, rows=2, n_pos=64, kv_heads=2, dim=32, pos=POS, acc=ACC, budget=32, sinks=2,
              recent=4, new_pos=NPOS, new_acc=NACC, kept=KEPT, ws=WS, wsb=0, stream=None)
