@@ -309,7 +309,9 @@ size_t head_argmax_noalloc_scratch_bytes(void);
  *            cache entry.  Visible are the entries i in [0, pos[m]] with
  *            i < sinks or i > pos[m] - window; window = -1: all of them.
  *   out[m][g] = sum_i p_i v_i, p = softmax_i(scale * q_g . k_i) over the
- *            visible i; row m at out + m * ldo, ldo >= heads * head_dim
+ *            visible i; row m at out + m * ldo, ldo >= heads * head_dim.  scale is
+ *            0 or 2^-126 to 2^127 either way; it and log2(e) multiply q first, in
+ *            binary32
  *   acc      float [rows][kv_heads][n_pos] or NULL: acc[m][h][i] += the sum
  *            over the query heads of K/V head h of p_i (what kv_evict ranks);
  *            entries that are not visible keep their values

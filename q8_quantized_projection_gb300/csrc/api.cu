@@ -520,7 +520,8 @@ q8_status attn_decode(const float* q, int64_t ldq, const void* k_cache, const vo
     if (st != Q8_OK) return st;
     const int64_t width = heads * head_dim, max_ld = int64_t(1) << 31;
     if (ldq < width || ldo < width || ldq > max_ld || ldo > max_ld) return Q8_ERR_SHAPE;
-    if (!(fabsf(scale) <= FLT_MAX)) return Q8_ERR_ARG;
+    // (its product with log2(e) is to be a normal binary32)
+    if (scale != 0.0f && !(fabsf(scale) >= FLT_MIN && fabsf(scale) <= 0x1p127f)) return Q8_ERR_ARG;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(pos) ||
         !aligned16(out) || (acc && !aligned16(acc)))
         return Q8_ERR_ALIGN;

@@ -56,6 +56,14 @@ def test_attn_decode_refuses(lib, over, status):
     assert attn(lib, **over) == status
 
 
+@pytest.mark.parametrize("scale,status", [
+    (3e38, 1), (-3.4e38, 1), (1.8e38, 1), (1e-38, 1), (-1e-45, 1),
+    (0.0, 7), (-0.0, 7), (2.0 ** 127, 7), (-2.0 ** 127, 7), (2.0 ** -126, 7), (-2.0 ** -126, 7)])
+def test_attn_decode_scale(lib, scale, status):
+    """Refused where its product with log2(e) would overflow (0 times infinity is NaN) or lose bits."""
+    assert attn(lib, scale=scale) == status
+
+
 def test_attn_decode_workspace_sizes(lib):
     f = lib.attn_decode_workspace
     plain, with_acc = f(2, 8, 2, 32, 64, -1, 0, 0), f(2, 8, 2, 32, 64, -1, 0, 1)
