@@ -372,7 +372,7 @@ struct Row {
         return make_float4(at(e), at(e + 1), at(e + 2), at(e + 3));
     }
     __device__ __forceinline__ float at(uint32_t e) const {
-        return e < n ? clean(__ldg(x + e)) : -INFINITY;
+        return e < n ? clean(x[e]) : -INFINITY;
     }
 
     // Lists those of a lane's four tokens that `in` names (all lanes call);
@@ -836,6 +836,9 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
     Row<RES> row{gx, base, n, part / kPart, rank, size, 0};
     const uint32_t of_warp = uint32_t(row.tiles) * kTile;      // tokens of a warp
 
+    // (Ordinary loads, here and where rows are read again: this grid may have begun while
+    // the one that writes the logits ran, and the read-only path is for what nobody writes
+    // while a grid runs.)
     // Seen once while they are loaded: the largest and the smallest that can be
     // drawn, how many can, and for the nucleus of the whole row the sum of their
     // weights (a lane's in units of its own largest).
@@ -869,11 +872,11 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
             for (int e = end - int(of_warp) + lane * 4; e < end; e += kTile) {
                 float4 v;
                 if (e + 3 < int(n)) {
-                    v = __ldg(reinterpret_cast<const float4*>(gx + e));
+                    v = *reinterpret_cast<const float4*>(gx + e);
                 } else {
-                    v.x = e < int(n) ? __ldg(gx + e) : -INFINITY;
-                    v.y = e + 1 < int(n) ? __ldg(gx + e + 1) : -INFINITY;
-                    v.z = e + 2 < int(n) ? __ldg(gx + e + 2) : -INFINITY;
+                    v.x = e < int(n) ? gx[e] : -INFINITY;
+                    v.y = e + 1 < int(n) ? gx[e + 1] : -INFINITY;
+                    v.z = e + 2 < int(n) ? gx[e + 2] : -INFINITY;
                     v.w = -INFINITY;
                 }
                 v = make_float4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
@@ -889,11 +892,11 @@ __global__ void __launch_bounds__(kThreads, RES ? 2 : 1) sample_kernel(const Sam
             for (int e = tid * 4 - off; e < part; e += kThreads * 4) {
                 float f[4];
                 if (e + 3 < int(n)) {
-                    const float4 v = __ldg(reinterpret_cast<const float4*>(gx + e));
+                    const float4 v = *reinterpret_cast<const float4*>(gx + e);
                     f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) f[j] = e + j < int(n) && e + j >= 0 ? __ldg(gx + e + j) : -INFINITY;
+                    for (int j = 0; j < 4; ++j) f[j] = e + j < int(n) && e + j >= 0 ? gx[e + j] : -INFINITY;
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)

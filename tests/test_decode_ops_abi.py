@@ -1,6 +1,7 @@
 """Host-side checks of attn_decode, kv_evict and head_sample: what they refuse,
 before anything touches a GPU, and their workspaces' sizes."""
 import ctypes as C
+import os
 
 import pytest
 
@@ -157,6 +158,15 @@ def test_head_sample_refuses(lib, over, status):
 def test_head_sample_refuses_outputs_that_overlap(lib, over):
     """In place: one CTA of a row could read settings that another has written over."""
     assert sample(lib, **over) == 1
+
+
+@pytest.mark.parametrize("source", ["attn.cu", "attn.cuh", "attn_mma.cuh", "evict.cu", "sample.cu"])
+def test_no_read_only_loads(source):
+    """These grids begin while the one before may still write what they read (they wait for it on
+    the device), so nothing may go through the path for memory that is read-only while a grid runs."""
+    with open(os.path.join(build.CSRC, source)) as f:
+        text = f.read()
+    assert "__ldg(" not in text and ".nc" not in text
 
 
 def test_binding_refuses_host_tensors():
