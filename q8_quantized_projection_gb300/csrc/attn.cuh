@@ -33,10 +33,10 @@
 // warps an SM: one streams while the other ends a unit.
 //
 // Measured (32 query and 8 K/V heads of 128 values; device time): 64 rows of
-// 4100 to 8192 bf16 entries 241 us, 6.7 TB/s; 16 rows of up to 2052 visible
-// f32 entries 42 us, 5.5 TB/s; one row of 130001 bf16 entries 90 us, 5.9 TB/s,
-// and 104 us with the weights accumulated; one row of 613 f32 entries 8.5 us,
-// of one entry 3.8 us: there the launch, three dependent reads (positions, q
+// 4100 to 8192 bf16 entries 240 to 248 us (by the box), 6.5 to 6.7 TB/s; 16 rows
+// of up to 2052 visible f32 entries 42 us, 5.5 TB/s; one row of 130001 bf16
+// entries 90 us, 5.9 TB/s, and 103 us with the weights accumulated; one row of 613
+// f32 entries 8.1 us, of one entry 4.3 us: there the launch, three dependent reads (positions, q
 // and the entries, the partial states) and the ticket are the time.  A unit cut
 // between CTAs leaves partial states in the workspace; the CTA that finishes it
 // last (a ticket) joins them in CTA order, so results repeat bit for bit.

@@ -33,7 +33,8 @@
 // waves of clusters (64 rows of 128256, two CTAs an SM), then the instructions, 45
 // for an exact weight and about 170 a token in all against 4 bytes read, at 0.49
 // issued a clock and scheduler, and the histogram's shared atomics, 5 of the 39.
-// (An exponent of 5 instructions in place of 16 gained 0.2 us of the 84.)
+// (An exponent of 5 instructions in place of 16 gained 0.2 us of the 84.)  64
+// registers for two CTAs an SM: 48 bytes are spilled.
 //
 // Measured (device time): 3 rows of 1001 tokens 9 us, one of 128256 with every
 // filter 15 us, 64 of 128256 with top-p 85 us, 256 of 32003 with settings of
@@ -1125,7 +1126,9 @@ cudaError_t launch_sample(const SampleArgs& a, const LaunchCtx& ctx) {
     };
     // CTAs a row: parts of which an SM holds two where 8 CTAs reach that (248 rows
     // of 33098: 2 of 18 K 80 us, 4 of 10 K 101 us); more, down to parts of one tile
-    // a warp, while the GPU has SMs to spare
+    // a warp, while the GPU has SMs to spare.  Past 8 parts of 18 K an SM holds one
+    // CTA (64 rows, top-p: of 147456 92 us, of 147457 164), past 8 of 46 K none's part
+    // fits and every pass reads L2 (one row of 2^20, every filter: 58 us)
     int size = 1;
     while (size < kMaxCluster && (part_of(size) > kPairPart ||
                                   (a.rows * size * 2 <= ctx.num_sms && part_of(size) > kPart)))
