@@ -96,6 +96,12 @@ typedef enum {
     Q8_KV_BF16 = 2
 } q8_kv_type;
 
+/* Formats of the quantised K/V caches that the kvq_ calls take. */
+typedef enum {
+    Q8_KVQ_I8 = 0,   /* a signed byte a value, a binary32 scale a block of 32 */
+    Q8_KVQ_U4 = 1    /* four bits a value, a binary16 scale and minimum a block of 32 */
+} q8_kvq_type;
+
 /* Largest activation row count one call accepts (decode batch or prefill chunk). */
 #define Q8_MAX_ROWS 256
 
@@ -408,6 +414,90 @@ size_t kv_evict_workspace(int64_t rows, int64_t kv_heads, int64_t budget);
 q8_status head_sample(const float* logits, int64_t ldl, int64_t rows, int64_t N, const float* u,
                       const float* temperature, const int32_t* top_k, const float* top_p,
                       const float* min_p, int32_t* tok, float* prob, int32_t* kept, void* stream);
+
+/*
+ * Quantised K/V caches: kvq_store writes new tokens into them (beside
+ * q8_proj_fused_kv and its float caches), kvq_load reads entries back,
+ * kvq_attn_decode and kvq_evict are attn_decode and kv_evict over them.  The
+ * pages describe none; 36 or 20 bytes hold what 128 bytes of a float cache do.
+ *
+ * A cache is four planes, one of codes and one of words for K and for V, each
+ * head's entries one run:
+ *   k_codes, v_codes  Q8_KVQ_I8: int8 [rows][kv_heads][n_pos][head_dim];
+ *                     Q8_KVQ_U4: uint8 [rows][kv_heads][n_pos][head_dim / 2],
+ *                     value 2j in the low half of byte j, 2j + 1 in the high
+ *   k_words, v_words  [rows][kv_heads][n_pos][head_dim / 32] of 4 bytes, one a
+ *                     block of 32 values: float d, or binary16 s and m (s first)
+ * Numerics, by block (each operation one binary32 rounding):
+ *   I8: d = amax / 127, code = round_half_away(x / d) in [-127, 127] (0 where d
+ *       is 0): the one-word activation code; it stands for d * code;
+ *   U4: m = binary16(min), s = binary16((max - min) / 15), code =
+ *       round_half_away((x - m) / s) in [0, 15] (0 where s is 0); it stands for
+ *       m + s * code.
+ *   A block with an infinity or a NaN, or whose s or m overflows binary16, is
+ *   held as a word of NaN: all its values read back as NaN.
+ * head_dim a multiple of 32, up to 256; the other limits are attn_decode's.
+ * Two rows never share a cache; the planes overlap nothing else.
+ */
+
+/*
+ * Stores tokens: row m's token t becomes entry pos[m] + t of its cache, in K
+ * and in V (a decode step: T = 1; a prompt or a chunk of one: T tokens).
+ *   k, v     src_type (Q8_KV_F32, _F16 or _BF16), the token's kv_heads *
+ *            head_dim values at k + m * ld_row + t * ld_tok, likewise v (they
+ *            may be columns of the QKV projection's rows).  ld_row matters
+ *            where rows > 1, ld_tok where T > 1; then they are at least
+ *            kv_heads * head_dim (Q8_ERR_SHAPE) and whole 16 bytes (Q8_ERR_ALIGN)
+ *   pos      int32 [rows], device memory, read by the launch
+ *   lens     int32 [rows] or NULL: only row m's first lens[m] tokens are stored
+ *            (a padded batch; 0 and less: none, T and more: all)
+ * A token whose entry lies outside [0, n_pos) is not stored and sets device
+ * error 2.  1 <= T <= 2^31 - 1, rows and strides span at most 2^40 values.
+ */
+q8_status kvq_store(const void* k, const void* v, int src_type, int64_t ld_row, int64_t ld_tok,
+                    int64_t rows, int64_t T, int64_t kv_heads, int64_t head_dim, const int32_t* pos,
+                    const int32_t* lens, int kvq_type, void* k_codes, void* k_words, void* v_codes,
+                    void* v_words, int64_t n_pos, void* stream);
+
+/*
+ * Reads entries back: entry pos[m] + t of row m's cache into token t of k and v
+ * (dst_type, places and strides as kvq_store's k and v; the value in binary32,
+ * rounded once more where dst_type is 16 bits), for t < lens[m].  What lies
+ * behind lens[m] or outside the cache keeps what k and v held; the latter sets
+ * device error 2.
+ *   pos      int32 [rows] or NULL: 0
+ *   lens     int32 [rows] or NULL: T
+ * Rows and tokens of k and v must not overlap one another (Q8_ERR_SHAPE); k and
+ * v may be columns of the same rows.
+ */
+q8_status kvq_load(int kvq_type, const void* k_codes, const void* k_words, const void* v_codes,
+                   const void* v_words, int64_t rows, int64_t n_pos, int64_t kv_heads,
+                   int64_t head_dim, const int32_t* pos, int64_t T, const int32_t* lens, int dst_type,
+                   void* k, void* v, int64_t ld_row, int64_t ld_tok, void* stream);
+
+/*
+ * attn_decode over a quantised cache: the same arguments, results, limits and
+ * errors, with the cache's values as they stand for, and a workspace by the
+ * same rules (one may serve both in turn).
+ */
+q8_status kvq_attn_decode(const float* q, int64_t ldq, int kvq_type, const void* k_codes,
+                          const void* k_words, const void* v_codes, const void* v_words, int64_t rows,
+                          int64_t n_pos, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                          const int32_t* pos, int64_t window, int64_t sinks, float scale, float* out,
+                          int64_t ldo, float* acc, void* workspace, size_t ws_bytes, void* stream);
+size_t kvq_attn_decode_workspace(int64_t rows, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                 int64_t n_pos, int64_t window, int64_t sinks, int with_acc);
+
+/*
+ * kv_evict over a quantised cache: the same arguments, results, limits, errors
+ * and workspace; codes and words move, unchanged.
+ */
+q8_status kvq_evict(int kvq_type, void* k_codes, void* k_words, void* v_codes, void* v_words,
+                    int64_t rows, int64_t n_pos, int64_t kv_heads, int64_t head_dim,
+                    const int32_t* pos, const float* acc, int64_t budget, int64_t sinks,
+                    int64_t recent, int32_t* new_pos, float* new_acc, int32_t* kept, void* workspace,
+                    size_t ws_bytes, void* stream);
+size_t kvq_evict_workspace(int64_t rows, int64_t kv_heads, int64_t budget);
 
 /*
  * Debug: the per-block int32 dot products the projections fold with their

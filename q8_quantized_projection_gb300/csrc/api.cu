@@ -506,7 +506,7 @@ size_t attn_decode_workspace(int64_t rows, int64_t heads, int64_t kv_heads, int6
     size_t cache;
     if (check_attn(Q8_KV_F16, rows, n_pos, heads, kv_heads, head_dim, window, sinks, &cache) != Q8_OK)
         return 0;
-    return attn_workspace_bytes(rows, heads, kv_heads, head_dim, n_pos, window, sinks, with_acc != 0);
+    return attn_workspace_bytes(rows, heads, kv_heads, head_dim, n_pos, window, sinks, with_acc != 0, false);
 }
 
 q8_status attn_decode(const float* q, int64_t ldq, const void* k_cache, const void* v_cache,
@@ -532,7 +532,8 @@ q8_status attn_decode(const float* q, int64_t ldq, const void* k_cache, const vo
         overlaps2(acc, an, q, qn) || overlaps2(acc, an, k_cache, cache) ||
         overlaps2(acc, an, v_cache, cache) || overlaps2(acc, an, pos, pn))
         return Q8_ERR_ARG;
-    const size_t wn = attn_workspace_bytes(rows, heads, kv_heads, head_dim, n_pos, window, sinks, acc != nullptr);
+    const size_t wn =
+        attn_workspace_bytes(rows, heads, kv_heads, head_dim, n_pos, window, sinks, acc != nullptr, false);
     if (!workspace || ws_bytes < wn) return Q8_ERR_WORKSPACE;
     if (!aligned16(workspace)) return Q8_ERR_ALIGN;
     if (overlaps2(workspace, wn, q, qn) || overlaps2(workspace, wn, k_cache, cache) ||
@@ -613,6 +614,188 @@ q8_status head_sample(const float* logits, int64_t ldl, int64_t rows, int64_t N,
     if (st != Q8_OK) return st;
     const SampleArgs a{logits, ldl, rows, N, u, temperature, top_k, top_p, min_p, tok, prob, kept};
     return launched(launch_sample(a, ctx));
+}
+
+// ------------------------------------------------------------ quantised K/V caches
+
+namespace {
+
+// A buffer of a call and whether the call writes it.
+struct Span {
+    const void* p;
+    size_t n;
+    bool written;
+};
+
+// A written buffer among these overlaps another one.
+bool any_overlap(const Span* b, int n) {
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < i; ++j)
+            if ((b[i].written || b[j].written) && overlaps2(b[i].p, b[i].n, b[j].p, b[j].n)) return true;
+    return false;
+}
+
+// Sizes of a quantised cache; *codes and *words receive the bytes of one plane of each.
+q8_status check_kvq(int kind, int64_t rows, int64_t n_pos, int64_t kv_heads, int64_t dim, size_t* codes,
+                    size_t* words) {
+    if (kind != Q8_KVQ_I8 && kind != Q8_KVQ_U4) return Q8_ERR_MODE;
+    if (dim % Q8_QK) return Q8_ERR_SHAPE;
+    size_t n;
+    const q8_status st = check_cache(Q8_KV_F16, rows, n_pos, kv_heads, dim, &n);
+    if (st != Q8_OK) return st;
+    *codes = kind == Q8_KVQ_I8 ? n / 2 : n / 4;
+    *words = n / 16;
+    return Q8_OK;
+}
+
+// What kvq_store reads and kvq_load writes: one of K's and V's floats.
+q8_status check_floats(int type, int64_t rows, int64_t T, int64_t width, int64_t ld_row, int64_t ld_tok, bool written,
+                       size_t* bytes) {
+    if (type < Q8_KV_F32 || type > Q8_KV_BF16) return Q8_ERR_MODE;
+    const int64_t elt = type == Q8_KV_F32 ? 4 : 2, most = int64_t(1) << 40;
+    if (T < 1 || T > INT32_MAX) return Q8_ERR_SHAPE;
+    if ((T > 1 && (ld_tok < width || ld_tok > most / T)) || (rows > 1 && (ld_row < width || ld_row > most / rows)))
+        return Q8_ERR_SHAPE;
+    if ((T > 1 && ld_tok * elt % 16) || (rows > 1 && ld_row * elt % 16)) return Q8_ERR_ALIGN;
+    const int64_t tokens = T > 1 ? (T - 1) * ld_tok : 0, all = rows > 1 ? (rows - 1) * ld_row : 0;
+    // (rows that are written lie behind one another, or between one another's tokens)
+    if (written && T > 1 && rows > 1 && ld_row < tokens + width && ld_tok < all + width) return Q8_ERR_SHAPE;
+    *bytes = size_t(tokens + all + width) * size_t(elt);
+    return Q8_OK;
+}
+
+q8_status kvq_io(bool store, void* k, void* v, int type, int64_t ld_row, int64_t ld_tok, int64_t rows, int64_t T,
+                 int64_t kv_heads, int64_t dim, const int32_t* pos, const int32_t* lens, int kind, void* k_codes,
+                 void* k_words, void* v_codes, void* v_words, int64_t n_pos, void* stream) {
+    if (!k || !v || (store && !pos) || !k_codes || !k_words || !v_codes || !v_words) return Q8_ERR_ARG;
+    size_t codes, words, floats;
+    q8_status st = check_kvq(kind, rows, n_pos, kv_heads, dim, &codes, &words);
+    if (st != Q8_OK) return st;
+    if ((st = check_floats(type, rows, T, kv_heads * dim, ld_row, ld_tok, !store, &floats)) != Q8_OK) return st;
+    const void* all[] = {k, v, pos, lens, k_codes, k_words, v_codes, v_words};
+    for (const void* p : all)
+        if (!aligned16(p)) return Q8_ERR_ALIGN;
+    const size_t pn = size_t(rows) * 4;
+    Span b[] = {{k, floats, !store},     {v, floats, !store},     {pos, pn, false},        {lens, pn, false},
+                {k_codes, codes, store}, {k_words, words, store}, {v_codes, codes, store}, {v_words, words, store}};
+    // K and V that are written may be columns of the same rows: one span then, from the
+    // first's beginning to the second's end
+    const uintptr_t ka = reinterpret_cast<uintptr_t>(k), va = reinterpret_cast<uintptr_t>(v);
+    const uintptr_t apart = (ka < va ? va - ka : ka - va) / (type == Q8_KV_F32 ? 4 : 2);
+    const int64_t width = kv_heads * dim;
+    size_t both;
+    if (!store && apart >= uintptr_t(width) && apart < uintptr_t(1) << 40 &&
+        check_floats(type, rows, T, int64_t(apart) + width, ld_row, ld_tok, true, &both) == Q8_OK) {
+        b[0] = {ka < va ? k : v, both, true};
+        b[1] = {nullptr, 0, false};
+    }
+    if (any_overlap(b, sizeof(b) / sizeof(b[0]))) return Q8_ERR_ARG;
+    LaunchCtx ctx;
+    if ((st = make_ctx(stream, ctx)) != Q8_OK) return st;
+    const KvqIoArgs a{k,    v,    type, ld_row,  ld_tok,  rows,    T,       kv_heads, dim,
+                      pos,  lens, kind, k_codes, k_words, v_codes, v_words, n_pos};
+    return launched(store ? launch_kvq_store(a, ctx) : launch_kvq_load(a, ctx));
+}
+
+}  // namespace
+
+q8_status kvq_store(const void* k, const void* v, int src_type, int64_t ld_row, int64_t ld_tok, int64_t rows, int64_t T,
+                    int64_t kv_heads, int64_t head_dim, const int32_t* pos, const int32_t* lens, int kvq_type,
+                    void* k_codes, void* k_words, void* v_codes, void* v_words, int64_t n_pos, void* stream) {
+    return kvq_io(true, const_cast<void*>(k), const_cast<void*>(v), src_type, ld_row, ld_tok, rows, T, kv_heads, head_dim,
+                  pos, lens, kvq_type, k_codes, k_words, v_codes, v_words, n_pos, stream);
+}
+
+q8_status kvq_load(int kvq_type, const void* k_codes, const void* k_words, const void* v_codes, const void* v_words,
+                   int64_t rows, int64_t n_pos, int64_t kv_heads, int64_t head_dim, const int32_t* pos, int64_t T,
+                   const int32_t* lens, int dst_type, void* k, void* v, int64_t ld_row, int64_t ld_tok, void* stream) {
+    return kvq_io(false, k, v, dst_type, ld_row, ld_tok, rows, T, kv_heads, head_dim, pos, lens, kvq_type,
+                  const_cast<void*>(k_codes), const_cast<void*>(k_words), const_cast<void*>(v_codes),
+                  const_cast<void*>(v_words), n_pos, stream);
+}
+
+static q8_status check_kvq_attn(int kind, int64_t rows, int64_t n_pos, int64_t heads, int64_t kv_heads, int64_t dim,
+                                int64_t window, int64_t sinks, size_t* codes, size_t* words) {
+    const q8_status st = check_kvq(kind, rows, n_pos, kv_heads, dim, codes, words);
+    if (st != Q8_OK) return st;
+    size_t n;
+    return check_attn(Q8_KV_F16, rows, n_pos, heads, kv_heads, dim, window, sinks, &n);
+}
+
+size_t kvq_attn_decode_workspace(int64_t rows, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t n_pos,
+                                 int64_t window, int64_t sinks, int with_acc) {
+    size_t codes, words;
+    if (check_kvq_attn(Q8_KVQ_I8, rows, n_pos, heads, kv_heads, head_dim, window, sinks, &codes, &words) != Q8_OK)
+        return 0;
+    return attn_workspace_bytes(rows, heads, kv_heads, head_dim, n_pos, window, sinks, with_acc != 0, true);
+}
+
+q8_status kvq_attn_decode(const float* q, int64_t ldq, int kvq_type, const void* k_codes, const void* k_words,
+                          const void* v_codes, const void* v_words, int64_t rows, int64_t n_pos, int64_t heads,
+                          int64_t kv_heads, int64_t head_dim, const int32_t* pos, int64_t window, int64_t sinks,
+                          float scale, float* out, int64_t ldo, float* acc, void* workspace, size_t ws_bytes,
+                          void* stream) {
+    if (!q || !k_codes || !k_words || !v_codes || !v_words || !pos || !out) return Q8_ERR_ARG;
+    size_t codes, words;
+    q8_status st = check_kvq_attn(kvq_type, rows, n_pos, heads, kv_heads, head_dim, window, sinks, &codes, &words);
+    if (st != Q8_OK) return st;
+    const int64_t width = heads * head_dim, max_ld = int64_t(1) << 31;
+    if (ldq < width || ldo < width || ldq > max_ld || ldo > max_ld) return Q8_ERR_SHAPE;
+    if (scale != 0.0f && !(fabsf(scale) >= FLT_MIN && fabsf(scale) <= 0x1p127f)) return Q8_ERR_ARG;   // (as attn_decode)
+    const void* all[] = {q, k_codes, k_words, v_codes, v_words, pos, out, acc};
+    for (const void* p : all)
+        if (!aligned16(p)) return Q8_ERR_ALIGN;
+    const size_t wn =
+        attn_workspace_bytes(rows, heads, kv_heads, head_dim, n_pos, window, sinks, acc != nullptr, true);
+    const Span b[] = {{q, size_t((rows - 1) * ldq + width) * 4, false}, {out, size_t((rows - 1) * ldo + width) * 4, true},
+                      {acc, size_t(rows * kv_heads) * size_t(n_pos) * 4, true}, {pos, size_t(rows) * 4, false},
+                      {k_codes, codes, false}, {k_words, words, false}, {v_codes, codes, false}, {v_words, words, false}};
+    if (any_overlap(b, sizeof(b) / sizeof(b[0]))) return Q8_ERR_ARG;
+    if (!workspace || ws_bytes < wn) return Q8_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return Q8_ERR_ALIGN;
+    for (const Span& s : b)
+        if (overlaps2(workspace, wn, s.p, s.n)) return Q8_ERR_ARG;
+    LaunchCtx ctx;
+    if ((st = make_ctx(stream, ctx)) != Q8_OK) return st;
+    const AttnArgs a{q,      ldq,   k_codes, v_codes, kKvQuantised + kvq_type,
+                     rows,   n_pos, heads,   kv_heads, head_dim, pos, window, sinks, scale, out, ldo, acc, workspace,
+                     static_cast<const uint32_t*>(k_words), static_cast<const uint32_t*>(v_words)};
+    return launched(launch_attn(a, ctx));
+}
+
+size_t kvq_evict_workspace(int64_t rows, int64_t kv_heads, int64_t budget) {
+    return kv_evict_workspace(rows, kv_heads, budget);
+}
+
+q8_status kvq_evict(int kvq_type, void* k_codes, void* k_words, void* v_codes, void* v_words, int64_t rows,
+                    int64_t n_pos, int64_t kv_heads, int64_t head_dim, const int32_t* pos, const float* acc,
+                    int64_t budget, int64_t sinks, int64_t recent, int32_t* new_pos, float* new_acc, int32_t* kept,
+                    void* workspace, size_t ws_bytes, void* stream) {
+    if (!k_codes || !k_words || !v_codes || !v_words || !pos || !acc || !new_pos || !new_acc) return Q8_ERR_ARG;
+    size_t codes, words;
+    q8_status st = check_kvq(kvq_type, rows, n_pos, kv_heads, head_dim, &codes, &words);
+    if (st != Q8_OK) return st;
+    if (budget < 1 || budget > n_pos || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks)
+        return Q8_ERR_SHAPE;
+    const void* all[] = {k_codes, k_words, v_codes, v_words, pos, acc, new_pos, new_acc, kept};
+    for (const void* p : all)
+        if (!aligned16(p)) return Q8_ERR_ALIGN;
+    const size_t an = size_t(rows * kv_heads) * size_t(n_pos) * 4, pn = size_t(rows) * 4;
+    const size_t wn = evict_workspace_bytes(rows, kv_heads, budget);
+    if (!workspace || ws_bytes < wn) return Q8_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return Q8_ERR_ALIGN;
+    // (in place: the old one counts as the new)
+    const Span b[] = {{k_codes, codes, true}, {k_words, words, true}, {v_codes, codes, true}, {v_words, words, true},
+                      {new_pos == pos ? nullptr : pos, pn, false},    {new_acc == acc ? nullptr : acc, an, false},
+                      {new_pos, pn, true},    {new_acc, an, true},
+                      {kept, size_t(rows * kv_heads) * size_t(budget) * 4, true}, {workspace, wn, true}};
+    if (any_overlap(b, sizeof(b) / sizeof(b[0]))) return Q8_ERR_ARG;
+    LaunchCtx ctx;
+    if ((st = make_ctx(stream, ctx)) != Q8_OK) return st;
+    const EvictArgs a{k_codes, v_codes, kKvQuantised + kvq_type, rows,    n_pos,   kv_heads, head_dim, pos,
+                      acc,     budget,  sinks, recent, new_pos, new_acc, kept, workspace,
+                      static_cast<uint32_t*>(k_words), static_cast<uint32_t*>(v_words)};
+    return launched(launch_evict(a, ctx));
 }
 
 }  // extern "C"

@@ -7,6 +7,7 @@ namespace q8 {
 cudaError_t launch_attn_f32(const AttnParams& p, const LaunchCtx& ctx);
 cudaError_t launch_attn_f16(const AttnParams& p, const LaunchCtx& ctx);
 cudaError_t launch_attn_bf16(const AttnParams& p, const LaunchCtx& ctx);
+cudaError_t launch_attn_kvq(const AttnParams& p, const LaunchCtx& ctx);
 
 namespace {
 
@@ -72,17 +73,17 @@ int block_heads(int64_t group) {
     return int((group + nb - 1) / nb);
 }
 
-size_t part_bytes(int gsz, int64_t dim) {
-    const int ng = gsz <= 2 ? gsz : gsz <= 4 ? 4 : 8;
-    return round256(size_t(2) * kAttnMaxCtas * attn_slot(ng, dim) * 4);
+size_t part_bytes(int gsz, int64_t dim, bool quantised) {
+    const int ng = quantised ? kvq_block_heads(gsz) : gsz <= 2 ? gsz : gsz <= 4 ? 4 : 8;
+    return round256(size_t(2) * (quantised ? kKvqMaxCtas : kAttnMaxCtas) * attn_slot(ng, dim) * 4);
 }
 
 }  // namespace
 
 // [tickets][partial states][per query head: reference, 1 / sum][scores]
 size_t attn_workspace_bytes(int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim, int64_t n_pos,
-                            int64_t window, int64_t sinks, bool acc) {
-    size_t n = kCounterBytes + part_bytes(block_heads(heads / kv_heads), dim);
+                            int64_t window, int64_t sinks, bool acc, bool quantised) {
+    size_t n = kCounterBytes + part_bytes(block_heads(heads / kv_heads), dim, quantised);
     if (acc)
         n += round256(size_t(rows * heads) * 8) +
              round256(size_t(rows * heads) * size_t(visible_cap(n_pos, window, sinks)) * 4);
@@ -105,11 +106,12 @@ cudaError_t launch_attn(const AttnArgs& a, const LaunchCtx& ctx) {
     unsigned char* ws = static_cast<unsigned char*>(a.ws) + kCounterBytes;
     p.part = reinterpret_cast<float*>(ws);
     if (a.acc) {
-        ws += part_bytes(p.gsz, a.dim);
+        ws += part_bytes(p.gsz, a.dim, a.kv_type >= kKvQuantised);
         p.ml = reinterpret_cast<float2*>(ws);
         p.scores = reinterpret_cast<float*>(ws + round256(size_t(a.rows * a.heads) * 8));
     }
-    const cudaError_t e = a.kv_type == Q8_KV_F32   ? launch_attn_f32(p, ctx)
+    const cudaError_t e = a.kv_type >= kKvQuantised ? launch_attn_kvq(p, ctx)
+                          : a.kv_type == Q8_KV_F32 ? launch_attn_f32(p, ctx)
                           : a.kv_type == Q8_KV_F16 ? launch_attn_f16(p, ctx)
                                                    : launch_attn_bf16(p, ctx);
     if (e != cudaSuccess || !a.acc || p.cap == 0) return e;

@@ -61,6 +61,10 @@ constexpr int kAttnMaxCtas = 512;
 // and 100.)
 constexpr int kAttnLanesHeads = 4;
 static_assert(4 * kAttnMaxCtas <= kCounterBytes, "one ticket a CTA");
+// Quantised caches: CTAs of a call at most, and the query heads a kernel is built for.
+constexpr int kKvqMaxCtas = 640;
+static_assert(4 * kKvqMaxCtas <= kCounterBytes, "one ticket a CTA");
+constexpr int kvq_block_heads(int heads) { return heads <= 4 ? 4 : 8; }
 
 // Floats of a partial state, whole 16-byte words.
 __host__ __device__ constexpr size_t attn_slot(int ng, int64_t dim) {
@@ -158,7 +162,7 @@ struct Segment {
     int row, g0, ng;
     Visible vis;
     uint32_t pitch;          // bytes from one entry to the next
-    int64_t off;             // of the row and K/V head in the caches
+    int64_t off;             // of the row and K/V head in the caches (head-major ones: in entries)
     uint32_t v_end, v_begin;
     int its;                 // stages
     int half;                // of V's values, where two warps share them
@@ -405,6 +409,8 @@ struct AttnLanes {
     static constexpr int DUP = LPK > NV ? LPK / NV : 1;       // lanes holding the same scores
     static constexpr int LG = LPK / NG;                       // lanes a query head
     static constexpr int LEAST = NG == 8 ? 1 : 2;             // tiles a CTA, at least
+    static constexpr int CTAS = 2, RING = kAttnRing, MAX_CTAS = kAttnMaxCtas;
+    static constexpr bool HEAD_MAJOR = false;
     static_assert(S >= 2 && LG >= 1 && U % R == 0 && R * LPK >= NV, "attention tile");
     static_assert(NG * DMAX * 4 <= kAttnRing, "a warp's state fits its ring");
 
@@ -412,7 +418,7 @@ struct AttnLanes {
 };
 
 template <class T>
-__global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, T::CTAS) attn_kernel(const AttnParams p) {
     constexpr int NG = T::NG, WARPS = kAttnWarps / T::SPLIT;      // warps that share a stage's entries
     extern __shared__ __align__(256) unsigned char ring_raw[];
     unsigned char* const ring_all = ring_raw + (512 - (smem_u32(ring_raw) & 511) & 511);   // stages on whole rows
@@ -427,12 +433,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
     const int D = int(a.dim), rows = int(a.rows);
     const uint32_t per_row = uint32_t(a.kv_heads) * p.nb;
     const int TT = T::TK * p.tile_its;                     // entries a tile
-    unsigned char* ring = ring_all + warp * kAttnRing;
+    unsigned char* ring = ring_all + warp * T::RING;
     const uint32_t ring_s = smem_u32(ring);
 
     // values behind D are never copied; they stay zero
     if (D < T::DMAX) {
-        for (int i = lane; i < kAttnRing / 16; i += 32) reinterpret_cast<int4*>(ring)[i] = int4{0, 0, 0, 0};
+        for (int i = lane; i < T::RING / 16; i += 32) reinterpret_cast<int4*>(ring)[i] = int4{0, 0, 0, 0};
     }
     pdl_wait();
     pdl_launch_dependents();
@@ -514,8 +520,15 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
         const int g0 = h * group + b * p.gsz;                       // the block's first query head
         const int ng = min(p.gsz, group - b * p.gsz);
         const Visible vis = visible(s_pos[m], a.n_pos, a.window, a.sinks);
-        const uint32_t pitch = uint32_t(a.kv_heads) * D * T::ELT;      // (below 2^21)
-        const int64_t off = (int64_t(m) * a.n_pos * a.kv_heads + h) * D * T::ELT;
+        uint32_t pitch;
+        int64_t off;
+        if constexpr (T::HEAD_MAJOR) {
+            pitch = T::ROW;
+            off = (int64_t(m) * a.kv_heads + h) * a.n_pos;
+        } else {
+            pitch = uint32_t(a.kv_heads) * D * T::ELT;                 // (below 2^21)
+            off = (int64_t(m) * a.n_pos * a.kv_heads + h) * D * T::ELT;
+        }
         // this warp's entries: KT of every TK from v_begin on.  At most 2^31 - 1 are
         // visible, so 32 bits hold every index and a tile more.
         const uint64_t upto = uint64_t(t1 - unit0) * TT;
@@ -554,7 +567,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                 const int w = h0 + i;
                 const float f = s_m[w][g] == -INFINITY ? 1.0f : ex2(s_m[w][g] - top);   // l and o: 0 or NaN
                 const float4 o4 =
-                    *reinterpret_cast<const float4*>(ring_all + w * kAttnRing + (g * T::DV + d % T::DV) * 4);
+                    *reinterpret_cast<const float4*>(ring_all + w * T::RING + (g * T::DV + d % T::DV) * 4);
                 sum += s_l[w][g] * f;
                 v.x += o4.x * f, v.y += o4.y * f, v.z += o4.z * f, v.w += o4.w * f;
             }
@@ -591,8 +604,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                 // parts' o at a time as fit, copied by all threads: one CTA's plain
                 // loads in turn would be the time of a unit that many share
                 float* const s_f = reinterpret_cast<float*>(ring_all);
-                constexpr int FACTORS = kAttnMaxCtas * NG * 4;
-                constexpr int FIT = (kAttnWarps * kAttnRing - FACTORS) / (NG * T::DMAX * 4);
+                constexpr int FACTORS = T::MAX_CTAS * NG * 4;
+                constexpr int FIT = (kAttnWarps * T::RING - FACTORS) / (NG * T::DMAX * 4);
                 const float4* const s_x = reinterpret_cast<const float4*>(ring_all + FACTORS);
                 const int E = ng * D4;
                 const auto fetch = [&](int i0) {
@@ -670,7 +683,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_kernel(const AttnParams 
                 }
                 if (D < T::DMAX) {     // values behind D are zero again
                     __syncthreads();
-                    for (int i = tid; i < kAttnWarps * kAttnRing / 16; i += kAttnThreads)
+                    for (int i = tid; i < kAttnWarps * T::RING / 16; i += kAttnThreads)
                         reinterpret_cast<int4*>(ring_all)[i] = int4{0, 0, 0, 0};
                 }
             }
@@ -688,12 +701,12 @@ template <class T>
 cudaError_t launch_attn_kernel(const AttnParams& p, const LaunchCtx& ctx) {
     static std::atomic<bool> ready[kMaxDevices];
     const auto kern = attn_kernel<T>;
-    constexpr size_t smem = size_t(kAttnWarps) * kAttnRing + 512;
+    constexpr size_t smem = size_t(kAttnWarps) * T::RING + 512;
     const cudaError_t e = set_smem_once(kern, smem, ctx.dev, ready);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attrs[1];
-    cfg.gridDim = dim3(unsigned(2 * ctx.num_sms < kAttnMaxCtas ? 2 * ctx.num_sms : kAttnMaxCtas));
+    cfg.gridDim = dim3(unsigned(T::CTAS * ctx.num_sms < T::MAX_CTAS ? T::CTAS * ctx.num_sms : T::MAX_CTAS));
     cfg.blockDim = dim3(kAttnThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = ctx.stream;

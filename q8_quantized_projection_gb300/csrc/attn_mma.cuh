@@ -407,6 +407,8 @@ struct AttnMma {
     static constexpr int TK = kAttnWarps / SPLIT * KT;
     static constexpr int EXTRA = (128 * 1024 + TK * 2 * PITCH - 1) / (TK * 2 * PITCH);
     static constexpr int LEAST = 1;
+    static constexpr int CTAS = 2, RING = kAttnRing, MAX_CTAS = kAttnMaxCtas;
+    static constexpr bool HEAD_MAJOR = false;
     static_assert(S >= 2 && NG * DMAX * 4 <= kAttnRing && DV % 32 == 0, "attention tile");
 
     static constexpr int RPI = CPR == 8 ? 4 : CPR == 32 ? 1 : 2;       // rows a warp copies at a time

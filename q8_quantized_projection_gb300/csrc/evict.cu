@@ -306,6 +306,60 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
                         col < row_bytes, rank, size);
 }
 
+// The same over quantised caches, head-major: a CTA has acc of one row and K/V head, or
+// one of its four planes (codes and words of K and of V), whole entries of `bytes` in
+// pieces of V.
+template <typename V>
+__device__ __forceinline__ void move_plane(unsigned char* base, int bytes, const int32_t* idx, int64_t from, int64_t budget) {
+    const int lanes = bytes / int(sizeof(V)), rows = int(blockDim.x) / lanes;
+    const int mine = threadIdx.x / lanes, col = (threadIdx.x - mine * lanes) * int(sizeof(V));
+    move_items<false, V>(base + col, base + col, bytes, idx, from, budget, rows, mine, mine < rows, 0, 1);
+}
+
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_move_kvq_kernel(const EvictArgs a, int row) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t units = a.rows * a.kv_heads, unit = blockIdx.x % units, m = unit / a.kv_heads;
+    const int plane = int(blockIdx.x / units), tid = threadIdx.x;
+    const int from = first_moved(a)[unit];
+    if (plane == 0) {
+        if (unit == m * a.kv_heads && tid == 0) a.new_pos[m] = from < 0 ? a.pos[m] : int32_t(a.budget - 1);
+        const float* acc = a.acc + unit * a.n_pos;
+        float* new_acc = a.new_acc + unit * a.n_pos;
+        const int64_t as_is = from < 0 ? a.n_pos : from;
+        if (new_acc != acc)
+            for (int64_t i = tid; i < as_is; i += kThreads) new_acc[i] = acc[i];
+        if (from < 0) return;
+        move_items<false, float>(reinterpret_cast<const unsigned char*>(acc), reinterpret_cast<unsigned char*>(new_acc), 4,
+                                 kept_list(a, unit), from, a.budget, kThreads, tid, true, 0, 1);
+        for (int64_t i = a.budget + tid; i < a.n_pos; i += kThreads) new_acc[i] = 0.0f;
+        return;
+    }
+    if (from < 0) return;
+    if (plane <= 2) {
+        unsigned char* base = static_cast<unsigned char*>(plane == 1 ? a.k : a.v) + unit * a.n_pos * row;
+        move_plane<int4>(base, row, kept_list(a, unit), from, a.budget);
+    } else {
+        const int bytes = int(a.dim) / 8;
+        unsigned char* base = reinterpret_cast<unsigned char*>(plane == 3 ? a.k_words : a.v_words) + unit * a.n_pos * bytes;
+        if (bytes % 16 == 0) move_plane<int4>(base, bytes, kept_list(a, unit), from, a.budget);
+        else move_plane<int>(base, bytes, kept_list(a, unit), from, a.budget);
+    }
+}
+
+cudaError_t launch_move_kvq(const EvictArgs& a, const LaunchCtx& ctx) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attrs[1];
+    cfg.gridDim = dim3(unsigned(a.rows * a.kv_heads * 5));
+    cfg.blockDim = dim3(512);
+    cfg.stream = ctx.stream;
+    cfg.numAttrs = pdl_attrs(ctx, attrs);
+    cfg.attrs = attrs;
+    return cudaLaunchKernelEx(&cfg, evict_move_kvq_kernel<512>, a,
+                              int(a.kv_type == kKvQuantised + Q8_KVQ_U4 ? a.dim / 2 : a.dim));
+}
+
 template <int THREADS>
 cudaError_t launch_select(const EvictArgs& a, const LaunchCtx& ctx) {
     // CTAs a row and head: so many that lanes hold their keys, where 8 reach that
@@ -359,6 +413,7 @@ cudaError_t launch_evict(const EvictArgs& a, const LaunchCtx& ctx) {
                           : a.n_pos <= 512 * kHeld ? launch_select<512>(a, ctx)
                                                    : launch_select<1024>(a, ctx);
     if (e != cudaSuccess) return e;
+    if (a.kv_type >= kKvQuantised) return launch_move_kvq(a, ctx);
     // the widest slice that leaves a CTA an SM, 64 bytes at least
     const int elt = a.kv_type == Q8_KV_F32 ? 4 : 2, chunks = int(a.dim) * elt / 16;      // 16-byte pieces an entry
     int lanes_log = 5;

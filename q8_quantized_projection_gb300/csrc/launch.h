@@ -179,9 +179,13 @@ struct AttnArgs {
     int64_t ldo;
     float* acc;          // [rows][kv_heads][n_pos], or NULL
     void* ws;
+    // quantised caches (kvq.cuh): kv_type counts from kKvQuantised on, k and v are the codes
+    const uint32_t* k_words = nullptr;
+    const uint32_t* v_words = nullptr;
 };
+constexpr int kKvQuantised = 16;                    // kv_type of Q8_KVQ_I8; Q8_KVQ_U4 follows
 size_t attn_workspace_bytes(int64_t rows, int64_t heads, int64_t kv_heads, int64_t dim, int64_t n_pos,
-                            int64_t window, int64_t sinks, bool acc);
+                            int64_t window, int64_t sinks, bool acc, bool quantised);
 cudaError_t launch_attn(const AttnArgs& a, const LaunchCtx& ctx);
 
 // Eviction from the K/V caches by accumulated weight (evict.cu).
@@ -197,9 +201,31 @@ struct EvictArgs {
     float* new_acc;
     int32_t* kept;       // [rows][kv_heads][budget], or NULL
     void* ws;
+    // quantised caches, as AttnArgs
+    uint32_t* k_words = nullptr;
+    uint32_t* v_words = nullptr;
 };
 size_t evict_workspace_bytes(int64_t rows, int64_t kv_heads, int64_t budget);
 cudaError_t launch_evict(const EvictArgs& a, const LaunchCtx& ctx);
+
+// Tokens stored into quantised caches, and entries read back (kvq.cu).
+struct KvqIoArgs {
+    void* k;             // floats of `type`, read by a store and written by a load:
+    void* v;             // row m's token t at m * ld_row + t * ld_tok, [kv_heads][dim]
+    int type;
+    int64_t ld_row, ld_tok;
+    int64_t rows, T, kv_heads, dim;
+    const int32_t* pos;  // [rows], or NULL (0)
+    const int32_t* lens; // [rows], or NULL (T)
+    int kind;
+    void* k_codes;
+    void* k_words;
+    void* v_codes;
+    void* v_words;
+    int64_t n_pos;
+};
+cudaError_t launch_kvq_store(const KvqIoArgs& a, const LaunchCtx& ctx);
+cudaError_t launch_kvq_load(const KvqIoArgs& a, const LaunchCtx& ctx);
 
 // Sampling from the head's logits (sample.cu).
 struct SampleArgs {

@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(PKG, "libq8proj.so")
 Q8_ACT_F32, Q8_ACT_I8, Q8_ACT_I8X2 = 0, 1, 2
 MODES = {"f32": Q8_ACT_F32, "i8": Q8_ACT_I8, "i8x2": Q8_ACT_I8X2}
 Q8_KV_F32, Q8_KV_F16, Q8_KV_BF16 = 0, 1, 2
+Q8_KVQ_I8, Q8_KVQ_U4 = 0, 1
+KVQ_TYPES = {"i8": Q8_KVQ_I8, "u4": Q8_KVQ_U4}
 Q8_MAX_ROWS = 256
 
 _STATUS = ["Q8_OK", "Q8_ERR_ARG", "Q8_ERR_SHAPE", "Q8_ERR_ALIGN", "Q8_ERR_MODE",
@@ -55,6 +57,16 @@ SIGNATURES = {
                         _vp, _vp, _sz, _vp]),
     "kv_evict_workspace": (_sz, [_i64, _i64, _i64]),
     "head_sample": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "kvq_store": (_int, [_vp, _vp, _int, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _int, _vp, _vp, _vp, _vp,
+                         _i64, _vp]),
+    "kvq_load": (_int, [_int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _int, _vp, _vp, _i64,
+                        _i64, _vp]),
+    "kvq_attn_decode": (_int, [_vp, _i64, _int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64,
+                               C.c_float, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "kvq_attn_decode_workspace": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64, _i64, _int]),
+    "kvq_evict": (_int, [_int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _vp,
+                         _vp, _vp, _sz, _vp]),
+    "kvq_evict_workspace": (_sz, [_i64, _i64, _i64]),
     "q8_debug_block_dots": (_int, [_int, _vp, _vp, _i64, _i64, _i64, _vp, _int, _vp]),
     "q8_debug_row_geometry": (_int, [_int, _i64, _i64, _i64, _int, _int, _vp]),
     "q8_debug_row_geometry_fused": (_int, [_int, _int, _i64, _i64, _int, _int, _vp]),
@@ -366,6 +378,114 @@ def kv_evict(k_cache, v_cache, pos, acc, new_pos, new_acc, workspace, kv_heads, 
         _raw_stream(torch, device, stream)), "kv_evict")
 
 
+def _kvq_cache(cache):
+    """(torch, device, kvq type, the four planes' addresses, rows, kv_heads, n_pos, head_dim) of a
+    quantised cache (k_codes, k_words, v_codes, v_words), as kvq_cache allocates one."""
+    k_codes, k_words, v_codes, v_words = cache
+    torch, device = _current("k_codes", k_codes)
+    dtype, shape = k_codes.dtype, k_codes.shape
+    if dtype is not torch.int8 and dtype is not torch.uint8:
+        raise TypeError(f"k_codes must be int8 or uint8, not {dtype}")
+    if len(shape) != 4:
+        raise ValueError(f"k_codes must have shape (rows, kv_heads, n_pos, codes), not {tuple(shape)}")
+    rows, kv_heads, n_pos, row = shape
+    if dtype is torch.int8:
+        kind, dim, word, words = Q8_KVQ_I8, row, torch.float32, (rows, kv_heads, n_pos, row // 32)
+    else:
+        kind, dim, word, words = Q8_KVQ_U4, 2 * row, torch.float16, (rows, kv_heads, n_pos, row // 16, 2)
+    if not k_codes.is_contiguous():
+        raise ValueError("k_codes must be contiguous")
+    return (torch, device, kind, k_codes.data_ptr(), _need("k_words", k_words, word, words, device),
+            _need("v_codes", v_codes, dtype, shape, device), _need("v_words", v_words, word, words, device),
+            rows, kv_heads, n_pos, dim)
+
+
+def _tokens(torch, device, k, v, rows, width):
+    """(K and V addresses, kv type, row and token stride, tokens) of floats [rows, tokens, width]
+    whose last dimension is dense."""
+    dtype, shape = k.dtype, k.shape
+    kv = (Q8_KV_F32 if dtype is torch.float32 else Q8_KV_F16 if dtype is torch.float16
+          else Q8_KV_BF16 if dtype is torch.bfloat16 else None)
+    if kv is None:
+        raise TypeError(f"k must be float32, float16 or bfloat16, not {dtype}")
+    if len(shape) != 3 or shape[0] != rows or shape[2] != width:
+        raise ValueError(f"k must have shape ({rows}, tokens, {width}), not {tuple(shape)}")
+    if v.dtype is not dtype:
+        raise TypeError(f"v must be {dtype}, as k, not {v.dtype}")
+    if v.shape != shape:
+        raise ValueError(f"v must have shape {tuple(shape)}, as k, not {tuple(v.shape)}")
+    if k.get_device() != device or v.get_device() != device:
+        raise ValueError(f"k and v must be on cuda:{device}, not {k.device} and {v.device}")
+    row, tok, step = k.stride()
+    v_row, v_tok, v_step = v.stride()
+    # (the stride of a dimension of one says nothing)
+    if (step != 1 or v_step != 1 or (shape[0] > 1 and v_row != row) or (shape[1] > 1 and v_tok != tok)):
+        raise ValueError("k and v must have dense values and the same strides")
+    return k.data_ptr(), v.data_ptr(), kv, row, tok, shape[1]
+
+
+def kvq_store(k, v, pos, cache, lens=None, stream=None):
+    """k, v: [rows, tokens, kv_heads * head_dim] float32, float16 or bfloat16 with any row and
+    token strides of whole 16 bytes; pos int32 [rows]; cache as kvq_cache; lens int32 [rows] or None."""
+    torch, device, kind, kc, kw, vc, vw, rows, kv_heads, n_pos, dim = _kvq_cache(cache)
+    k_at, v_at, kv, ld_row, ld_tok, tokens = _tokens(torch, device, k, v, rows, kv_heads * dim)
+    per_row, i32 = (rows,), torch.int32
+    _check((_lib or load()).kvq_store(
+        k_at, v_at, kv, ld_row, ld_tok, rows, tokens, kv_heads, dim, _need("pos", pos, i32, per_row, device),
+        _maybe("lens", lens, i32, per_row, device), kind, kc, kw, vc, vw, n_pos,
+        _raw_stream(torch, device, stream)), "kvq_store")
+
+
+def kvq_load(cache, k, v, pos=None, lens=None, stream=None):
+    """Reads entries from pos (None: 0) on into k, v: [rows, tokens, kv_heads * head_dim], as kvq_store's."""
+    torch, device, kind, kc, kw, vc, vw, rows, kv_heads, n_pos, dim = _kvq_cache(cache)
+    k_at, v_at, kv, ld_row, ld_tok, tokens = _tokens(torch, device, k, v, rows, kv_heads * dim)
+    per_row, i32 = (rows,), torch.int32
+    _check((_lib or load()).kvq_load(
+        kind, kc, kw, vc, vw, rows, n_pos, kv_heads, dim, _maybe("pos", pos, i32, per_row, device), tokens,
+        _maybe("lens", lens, i32, per_row, device), kv, k_at, v_at, ld_row, ld_tok,
+        _raw_stream(torch, device, stream)), "kvq_load")
+
+
+def kvq_attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window=-1, sinks=0, acc=False) -> int:
+    return int((_lib or load()).kvq_attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window, sinks,
+                                                          1 if acc else 0))
+
+
+def kvq_attn_decode(q, cache, pos, out, workspace, heads, window=-1, sinks=0, scale=None, acc=None,
+                    stream=None):
+    """q, out, pos, acc and scale as attn_decode; cache as kvq_cache."""
+    torch, device, kind, kc, kw, vc, vw, rows, kv_heads, n_pos, dim = _kvq_cache(cache)
+    f32 = torch.float32
+    q_at, ldq = _need_rows("q", q, f32, rows, heads * dim, device)
+    out_at, ldo = _need_rows("out", out, f32, rows, heads * dim, device)
+    ws_at, ws_bytes = _workspace(workspace, device)
+    _check((_lib or load()).kvq_attn_decode(
+        q_at, ldq, kind, kc, kw, vc, vw, rows, n_pos, heads, kv_heads, dim,
+        _need("pos", pos, torch.int32, (rows,), device), window, sinks,
+        dim ** -0.5 if scale is None else scale, out_at, ldo,
+        _maybe("acc", acc, f32, (rows, kv_heads, n_pos), device), ws_at, ws_bytes,
+        _raw_stream(torch, device, stream)), "kvq_attn_decode")
+
+
+def kvq_evict_workspace(rows, kv_heads, budget) -> int:
+    return int((_lib or load()).kvq_evict_workspace(rows, kv_heads, budget))
+
+
+def kvq_evict(cache, pos, acc, new_pos, new_acc, workspace, budget, sinks=0, recent=0, kept=None,
+              stream=None):
+    """cache as kvq_cache; the others as kv_evict."""
+    torch, device, kind, kc, kw, vc, vw, rows, kv_heads, n_pos, dim = _kvq_cache(cache)
+    f32, i32, weights = torch.float32, torch.int32, (rows, kv_heads, n_pos)
+    ws_at, ws_bytes = _workspace(workspace, device)
+    _check((_lib or load()).kvq_evict(
+        kind, kc, kw, vc, vw, rows, n_pos, kv_heads, dim, _need("pos", pos, i32, (rows,), device),
+        _need("acc", acc, f32, weights, device), budget, sinks, recent,
+        _need("new_pos", new_pos, i32, (rows,), device), _need("new_acc", new_acc, f32, weights, device),
+        _maybe("kept", kept, i32, (rows, kv_heads, budget), device), ws_at, ws_bytes,
+        _raw_stream(torch, device, stream)), "kvq_evict")
+
+
 def head_sample(logits, u, tok, temperature=None, top_k=None, top_p=None, min_p=None, prob=None,
                 kept=None, stream=None):
     """logits float32 [rows, N] with any row pitch; u, temperature, top_p,
@@ -454,6 +574,28 @@ def attn_workspace(rows, heads, kv_heads, head_dim, n_pos, window=-1, sinks=0, a
     nbytes = attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window, sinks, acc)
     if nbytes == 0:
         raise Q8Error(2, "attn_decode_workspace")
+    return torch.zeros((nbytes + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def kvq_cache(kind, rows, n_pos, kv_heads, head_dim, device="cuda"):
+    """A zeroed quantised cache ("i8" or "u4"): (k_codes, k_words, v_codes, v_words)."""
+    import torch
+    if head_dim < 32 or head_dim > 256 or head_dim % 32:
+        raise ValueError(f"head_dim must be a multiple of 32 up to 256, not {head_dim}")
+    if KVQ_TYPES[kind] == Q8_KVQ_I8:
+        planes = (((head_dim,), torch.int8), ((head_dim // 32,), torch.float32))
+    else:
+        planes = (((head_dim // 2,), torch.uint8), ((head_dim // 32, 2), torch.float16))
+    return tuple(torch.zeros((rows, kv_heads, n_pos) + last, dtype=dtype, device=device)
+                 for last, dtype in planes * 2)
+
+
+def kvq_attn_workspace(rows, heads, kv_heads, head_dim, n_pos, window=-1, sinks=0, acc=False, device="cuda"):
+    """A zeroed kvq_attn_decode workspace (its counters must start at zero)."""
+    import torch
+    nbytes = kvq_attn_decode_workspace(rows, heads, kv_heads, head_dim, n_pos, window, sinks, acc)
+    if nbytes == 0:
+        raise Q8Error(2, "kvq_attn_decode_workspace")
     return torch.zeros((nbytes + 15) // 16 * 16, dtype=torch.uint8, device=device)
 
 
