@@ -7,7 +7,10 @@ namespace q8 {
 cudaError_t launch_attn_f32(const AttnParams& p, const LaunchCtx& ctx);
 cudaError_t launch_attn_f16(const AttnParams& p, const LaunchCtx& ctx);
 cudaError_t launch_attn_bf16(const AttnParams& p, const LaunchCtx& ctx);
-cudaError_t launch_attn_kvq(const AttnParams& p, const LaunchCtx& ctx);
+cudaError_t launch_attn_kvq_i8_4(const AttnParams& p, const LaunchCtx& ctx);
+cudaError_t launch_attn_kvq_i8_8(const AttnParams& p, const LaunchCtx& ctx);
+cudaError_t launch_attn_kvq_u4_4(const AttnParams& p, const LaunchCtx& ctx);
+cudaError_t launch_attn_kvq_u4_8(const AttnParams& p, const LaunchCtx& ctx);
 
 namespace {
 
@@ -76,6 +79,13 @@ int block_heads(int64_t group) {
 size_t part_bytes(int gsz, int64_t dim, bool quantised) {
     const int ng = quantised ? kvq_block_heads(gsz) : gsz <= 2 ? gsz : gsz <= 4 ? 4 : 8;
     return round256(size_t(2) * (quantised ? kKvqMaxCtas : kAttnMaxCtas) * attn_slot(ng, dim) * 4);
+}
+
+cudaError_t launch_attn_kvq(const AttnParams& p, const LaunchCtx& ctx) {
+    const bool four = kvq_block_heads(p.gsz) == 4;
+    if (p.a.kv_type == kKvQuantised + Q8_KVQ_I8)
+        return four ? launch_attn_kvq_i8_4(p, ctx) : launch_attn_kvq_i8_8(p, ctx);
+    return four ? launch_attn_kvq_u4_4(p, ctx) : launch_attn_kvq_u4_8(p, ctx);
 }
 
 }  // namespace

@@ -1,0 +1,10 @@
+// attn_kvq_i8_4.cu -- the attention kernels over Q8_KVQ_I8 caches, up to 4 query heads a block.
+#include "attn_kvq.cuh"
+
+namespace q8 {
+
+cudaError_t launch_attn_kvq_i8_4(const AttnParams& p, const LaunchCtx& ctx) {
+    return launch_attn_kvq_heads<Q8_KVQ_I8, 1>(p, ctx);
+}
+
+}  // namespace q8

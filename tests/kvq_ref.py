@@ -46,7 +46,9 @@ def unpack(codes, kind):
 
 
 def values(packed, words, kind, spread=False):
-    """The values [..., D] in 64 bits; spread: the sum of the magnitudes that they are made of."""
+    """The values [..., D] in 64 bits; spread: the sum of the magnitudes that they are made of, where
+    a u4 value may be m and s code, or m + 15 s and s (15 - code) (half of an output's entries are: codes
+    have no sign, and truncated sums of all would lean one way)."""
     q = unpack(packed, kind).astype(np.float64)
     q = q.reshape(q.shape[:-1] + (-1, 32))
     if kind == "i8":
@@ -54,7 +56,7 @@ def values(packed, words, kind, spread=False):
         v = np.abs(v) if spread else v
     else:
         s, m = words[..., 0:1].astype(np.float64), words[..., 1:2].astype(np.float64)
-        v = np.abs(s * q) + np.abs(m) if spread else m + s * q
+        v = np.maximum(np.abs(m) + s * q, np.abs(m + 15 * s) + s * (15 - q)) if spread else m + s * q
     return v.reshape(v.shape[:-2] + (-1,))
 
 

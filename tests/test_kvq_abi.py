@@ -159,7 +159,7 @@ def test_kvq_evict_workspace_sizes(lib):
     assert f(0, 2, 32) == 0 and f(2, 0, 32) == 0 and f(2, 2, 0) == 0
 
 
-@pytest.mark.parametrize("source", ["kvq.cu", "kvq.cuh", "attn_kvq.cu", "attn_kvq.cuh"])
+@pytest.mark.parametrize("source", ["kvq.cu", "kvq.cuh", "attn_kvq.cuh"])
 def test_no_read_only_loads(source):
     """These grids begin while the one before may still write what they read."""
     with open(os.path.join(build.CSRC, source)) as f:

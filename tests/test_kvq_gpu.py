@@ -491,9 +491,33 @@ def test_weights_that_cancel(kind, heads, dim, n):
     planes = planes_of(kind, *parts, n)
     assert np.array_equal(kr.values(planes[0], planes[1], kind)[:, 0], k)
     assert np.array_equal(kr.values(planes[2], planes[3], kind)[:, 0], v)
-    # (u4: the score is a difference of sums of q, 2^-10 at most; V's values a difference of halves)
-    more = 8 * ap.U if kind == "u4" else 0
+    # u4: the score is a difference of sums of q, 2^-10 at most (8u).  V is m + s code (at most 1 + 2) or
+    # m + 15 s less s (15 - code) (29 and at most 30): sums of weights times 30.  The first ones': one
+    # rounding a term, of 16 kinds of entries (by their place of 16) N = ceil(n / 16) terms each, so
+    # u 30 N (N + 1) / 2 a kind, 16 kinds over n weights: 30 u (N + 1) / 2.  The products': chains of 32
+    # entries, 16 of them negative, six additions truncated by 2u of at most 16 * 30, over 32 weights: 180u;
+    # the chains' sums, rounded, n / 32 of them, u 16 * 30 each, over n: 15u.
+    more = (8 + 15 * (n // 16 + 2) + 180 + 15) * ap.U if kind == "u4" else 0
     in_range(run_planes(kind, q, planes, ap.SCALE)[0], want, ap.cancelling_weights_bound(want, n) + more)
+
+
+@pytest.mark.parametrize("heads", [4, 8])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n", [64, 600])
+def test_weights_that_cancel_in_blocks_that_span_their_codes(heads, dim, n):
+    """As above in u4, with V of +-15/16 as codes 15 and 0 (what kvq_store makes of such a block)."""
+    q, k, v = ap.cancelling_weights(heads, dim, n)
+    v[:, :, 1::2] *= -1                              # (both codes in a block)
+    nb = dim // 32
+    kp = ((k > -1).astype(np.uint8), np.tile(np.array([1, -1], np.float16), (1, n, nb, 1)))
+    vp = ((v > 0).astype(np.uint8) * 15, np.tile(np.array([0.125, -0.9375], np.float16), (1, n, nb, 1)))
+    planes = planes_of("u4", kp, vp, n)
+    assert np.array_equal(kr.values(planes[2], planes[3], "u4")[:, 0], v * 0.9375)
+    want, _ = ap.exact(q, k, v * 0.9375)
+    # the score 8u as above; the terms are at most 15/16 and 15/8: additions of at most 16 entries' 15/8 in
+    # a chain, truncated six times by 2u, over 32 weights (12u), of 16 kinds of entries 15/16 (N + 1) / 2 u
+    in_range(run_planes("u4", q, planes, ap.SCALE)[0], want,
+             ap.cancelling_weights_bound(want, n) + (8 + 12 + (n // 16 + 2) / 2) * ap.U)
 
 
 @pytest.mark.parametrize("heads", [4, 7, 8])
