@@ -15,22 +15,34 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int64_t kSegment = 65536;   // tokens a grid plane
 
+// Eight floats as they lie in memory.
 template <typename F>
-__device__ __forceinline__ void load8(const F* p, float (&x)[8]) {
-    if constexpr (sizeof(F) == 4) {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        const int4 a = __ldcs(reinterpret_cast<const int4*>(p));
-        const int w[4] = {a.x, a.y, a.z, a.w};
+struct Eight {
+    int4 w[sizeof(F) / 2];
+};
+
+template <typename F>
+__device__ __forceinline__ void fetch8(const F* p, Eight<F>& e) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float2 f;
-            if constexpr (std::is_same<F, __half>::value)
-                f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            else
-                f = make_float2(__int_as_float(w[i] << 16), __int_as_float(w[i] & int(0xffff0000)));
-            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    for (int i = 0; i < int(sizeof(F) / 2); ++i) e.w[i] = __ldcs(reinterpret_cast<const int4*>(p) + i);
+}
+
+template <typename F>
+__device__ __forceinline__ void expand8(const Eight<F>& e, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(F) / 2); ++i) {
+        const int w[4] = {e.w[i].x, e.w[i].y, e.w[i].z, e.w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(F) == 4) {
+                x[4 * i + j] = __int_as_float(w[j]);
+            } else if constexpr (std::is_same<F, __half>::value) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                x[2 * j] = f.x, x[2 * j + 1] = f.y;
+            } else {
+                x[2 * j] = __int_as_float(w[j] << 16);
+                x[2 * j + 1] = __int_as_float(w[j] & int(0xffff0000));
+            }
         }
     }
 }
@@ -56,145 +68,268 @@ __device__ __forceinline__ void store8(F* p, const float (&x)[8]) {
     }
 }
 
-// What a thread has: its eight values' place in the floats and in a cache.
+// x[i] of a register array, by selection.
+__device__ __forceinline__ float pick(const float (&x)[8], int i) {
+    float y = x[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) y = i == j ? x[j] : y;
+    return y;
+}
+
+// Eight values' place: whose head and eight of it are the thread's own, tokens are not.
 struct Place {
-    bool in;             // there is such a token, and its entry lies in the cache
+    int64_t at;          // values from the floats' beginning, of token 0
+    int64_t entry;       // (row, head, entry) in one line, of token 0
+    int64_t first, end;  // the thread's first token, and the row's end of them
+    int64_t pos;
     bool v;              // of V
-    int64_t at;          // values from the floats' beginning
-    int64_t entry;       // (row, head, entry) in one line
     int c;               // which eight of the head
 };
 
-__device__ __forceinline__ Place place(const KvqIoArgs& a, int slots, int tb, int* err) {
+__device__ __forceinline__ Place place(const KvqIoArgs& a, int slots, int tb, int r) {
     const int c8 = int(a.dim) / 8, slot = threadIdx.x / c8, c = threadIdx.x - slot * c8;
     const int64_t m = blockIdx.z, t_first = int64_t(blockIdx.y) * kSegment;
     const int ub = slots / tb, units = int(a.kv_heads) * 2, ublocks = (units + ub - 1) / ub;
     const int uu = slot / tb, unit = int(blockIdx.x % ublocks) * ub + uu;
-    const int64_t t = t_first + int64_t(blockIdx.x / ublocks) * tb + (slot - uu * tb);
-    const int64_t t_end = a.T < t_first + kSegment ? a.T : t_first + kSegment;
     Place p;
-    const int64_t len = a.lens ? a.lens[m] : a.T, pos = a.pos ? a.pos[m] : 0;
-    p.in = slot < slots && uu < ub && unit < units && t < t_end && t < len;
-    const int64_t i = pos + t;
-    if (p.in && (i < 0 || i >= a.n_pos)) {
-        p.in = false;
-        if (c == 0) atomicExch(err, Q8_DEVERR_POSITION);
-    }
+    p.first = t_first + int64_t(blockIdx.x / ublocks) * (int64_t(tb) * r) + (slot - uu * tb);
+    p.end = a.T < t_first + kSegment ? a.T : t_first + kSegment;
+    const int64_t len = a.lens ? a.lens[m] : a.T;
+    p.pos = a.pos ? a.pos[m] : 0;
+    p.end = p.end < len ? p.end : len;
+    if (slot >= slots || uu >= ub || unit >= units) p.end = 0;
     p.v = unit >= a.kv_heads;
     const int64_t h = p.v ? unit - a.kv_heads : unit;
-    p.at = m * a.ld_row + t * a.ld_tok + h * a.dim + c * 8;
-    p.entry = (m * a.kv_heads + h) * a.n_pos + i;
+    p.at = m * a.ld_row + h * a.dim + c * 8;
+    p.entry = (m * a.kv_heads + h) * a.n_pos + p.pos;
     p.c = c;
     return p;
 }
 
-template <typename F, int KIND>
-__global__ void __launch_bounds__(kThreads) kvq_store_kernel(const KvqIoArgs a, int slots, int tb, int* err) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const Place p = place(a, slots, tb, err);
-    float x[8] = {};
-    if (p.in) load8(static_cast<const F*>(p.v ? a.v : a.k) + p.at, x);
-    // (magnitudes as integers: infinities and NaN are the largest)
-    uint32_t most = 0;
-    float lo = x[0], hi = x[0];
+// Whether token t is the row's, and its entry in the cache.
+__device__ __forceinline__ bool inside(const KvqIoArgs& a, const Place& p, int64_t t, int* err) {
+    if (t >= p.end) return false;
+    if (p.pos + t >= 0 && p.pos + t < a.n_pos) return true;
+    if (p.c == 0) atomicExch(err, Q8_DEVERR_POSITION);
+    return false;
+}
+
+// 2^23 plus byte j of w (a conversion instruction runs at a quarter of this one's rate).
+__device__ __forceinline__ float byte_above_2_23(uint32_t w, int j) {
+    return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 + j));
+}
+
+constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: a sum with it is an integer in its low bits
+
+// Codes of x / d (i8) by way of 1 / d.  The product is within 127 * 1.5 * 2^-23 of the quotient and
+// that within 127 * 2^-24 of its rounding, 3.1e-5 in all: where it lies 2^-14 or more from
+// every half, both round to the same integer.  False: some value lies nearer.
+__device__ __forceinline__ bool codes_i8(const float (&x)[8], float d, uint32_t (&w)[2]) {
+    const float inv = d == 0.0f ? 0.0f : __frcp_rn(d);
+    float far = 0.0f, n[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        most = max(most, __float_as_uint(x[i]) & 0x7fffffffu);
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
+        const float r = __fmul_rn(x[i], inv);
+        n[i] = __fadd_rn(r, kMagic);
+        far = fmaxf(far, fabsf(r - __fsub_rn(n[i], kMagic)));
     }
 #pragma unroll
-    for (int k = 1; k < 4; k *= 2) {
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, k));
-        if constexpr (KIND == Q8_KVQ_U4) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, k));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, k));
-        }
-    }
-    if (!p.in) return;
-    const int64_t row = p.entry * kvq_row(KIND, a.dim);
-    uint32_t* word = static_cast<uint32_t*>(p.v ? a.v_words : a.k_words) + p.entry * (a.dim / 32) + p.c / 4;
-    unsigned char* codes = static_cast<unsigned char*>(p.v ? a.v_codes : a.k_codes) + row;
-    bool bad = most >= 0x7f800000u;                    // the block reads back as NaN
-    if constexpr (KIND == Q8_KVQ_I8) {
-        const float d = bad ? __int_as_float(0x7fc00000) : __fdiv_rn(__uint_as_float(most), 127.0f);
-        uint32_t w[2] = {0u, 0u};
-        if (!bad) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i / 4] |= uint32_t(quantize_code(x[i], d, 127.0f) & 255) << (8 * (i & 3));
-        }
-        *reinterpret_cast<uint2*>(codes + p.c * 8) = make_uint2(w[0], w[1]);
-        if ((p.c & 3) == 0) *word = __float_as_uint(d);
-    } else {
-        const __half s = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)), m = __float2half_rn(lo);
-        const float sf = __half2float(s), mf = __half2float(m);
-        bad = bad || isinf(sf) || isinf(mf);
-        uint32_t w = 0;
-        if (!bad && sf != 0.0f) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float q = roundf(__fdiv_rn(__fsub_rn(x[i], mf), sf));
-                w |= uint32_t(fminf(fmaxf(q, 0.0f), 15.0f)) << (4 * i);
-            }
-        }
-        *reinterpret_cast<uint32_t*>(codes + p.c * 4) = w;
-        if ((p.c & 3) == 0)
-            *word = bad ? 0x7e007e00u : uint32_t(__half_as_ushort(s)) | uint32_t(__half_as_ushort(m)) << 16;
-    }
+    for (int i = 0; i < 2; ++i)
+        w[i] = __byte_perm(__byte_perm(__float_as_uint(n[4 * i]), __float_as_uint(n[4 * i + 1]), 0x0040),
+                           __byte_perm(__float_as_uint(n[4 * i + 2]), __float_as_uint(n[4 * i + 3]), 0x0040), 0x5410);
+    return far < 0.5f - 0x1p-14f && d < 0x1p126f && (d == 0.0f || d > 0x1p-100f);
 }
 
-template <typename F, int KIND>
-__global__ void __launch_bounds__(kThreads) kvq_load_kernel(const KvqIoArgs a, int slots, int tb, int* err) {
+// The same of (x - m) / s, which may lie outside [0, 15].
+__device__ __forceinline__ bool codes_u4(const float (&x)[8], float s, float m, uint32_t& w) {
+    const float inv = s == 0.0f ? 0.0f : __frcp_rn(s);
+    float far = 0.0f, n[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float r = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], m), inv), 0.0f), 15.0f);
+        n[i] = __fsub_rn(__fadd_rn(r, kMagic), kMagic);
+        far = fmaxf(far, fabsf(r - n[i]));
+    }
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(__fadd_rn(fmaf(n[2 * i + 1], 16.0f, n[2 * i]), kMagic));
+    w = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    return far < 0.5f - 0x1p-14f;
+}
+
+// R tokens at a time and thread, tb apart, whose reads go out together, `turns` times; a
+// turn's reads go out before the one before is worked on.
+template <typename F, int KIND, int R>
+__global__ void __launch_bounds__(kThreads) kvq_store_kernel(const KvqIoArgs a, int slots, int tb, int turns, int* err) {
     pdl_wait();
     pdl_launch_dependents();
-    const Place p = place(a, slots, tb, err);
-    if (!p.in) return;
-    const int64_t row = p.entry * kvq_row(KIND, a.dim);
-    const uint32_t word = static_cast<const uint32_t*>(p.v ? a.v_words : a.k_words)[p.entry * (a.dim / 32) + p.c / 4];
-    const unsigned char* codes = static_cast<const unsigned char*>(p.v ? a.v_codes : a.k_codes) + row;
-    float x[8];
-    if constexpr (KIND == Q8_KVQ_I8) {
-        const uint2 w = *reinterpret_cast<const uint2*>(codes + p.c * 8);
-        const float d = __uint_as_float(word);
+    const Place p = place(a, slots, tb, R * turns);
+    Eight<F> next[R], now[R];
+    bool in_next[R], in[R];
+    const F* const from = static_cast<const F*>(p.v ? a.v : a.k) + p.at;
+    const auto fetch = [&](int turn) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = byte_as_float(int(i < 4 ? w.x : w.y), i & 3) * d;
-    } else {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + p.c * 4);
-        const float2 sm = kvq_scale_min(word);
+        for (int r = 0; r < R; ++r) {
+            const int64_t t = p.first + int64_t(turn * R + r) * tb;
+            in_next[r] = inside(a, p, t, err);
+            if (in_next[r]) fetch8(from + t * a.ld_tok, next[r]);
+        }
+    };
+    fetch(0);
+    uint32_t* const words = static_cast<uint32_t*>(p.v ? a.v_words : a.k_words);
+    unsigned char* const codes = static_cast<unsigned char*>(p.v ? a.v_codes : a.k_codes);
+#pragma unroll 1
+    for (int turn = 0; turn < turns; ++turn) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fmaf(float(w >> (4 * i) & 15u), sm.x, sm.y);   // (the product is exact)
+        for (int r = 0; r < R; ++r) now[r] = next[r], in[r] = in_next[r];
+        if (turn + 1 < turns) fetch(turn + 1);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float x[8] = {};
+            if (in[r]) expand8(now[r], x);
+            // (magnitudes as integers: infinities and NaN are the largest)
+            uint32_t most = 0;
+            float lo = x[0], hi = x[0];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                most = max(most, __float_as_uint(x[i]) & 0x7fffffffu);
+                lo = fminf(lo, x[i]);
+                hi = fmaxf(hi, x[i]);
+            }
+#pragma unroll
+            for (int k = 1; k < 4; k *= 2) {
+                most = max(most, __shfl_xor_sync(0xffffffffu, most, k));
+                if constexpr (KIND == Q8_KVQ_U4) {
+                    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, k));
+                    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, k));
+                }
+            }
+            if (!in[r]) continue;
+            const int64_t entry = p.entry + p.first + int64_t(turn * R + r) * tb;
+            uint32_t* const word = words + entry * (a.dim / 32) + p.c / 4;
+            unsigned char* const to = codes + entry * kvq_row(KIND, a.dim);
+            bool bad = most >= 0x7f800000u;                    // the block reads back as NaN
+            if constexpr (KIND == Q8_KVQ_I8) {
+                const float d = bad ? __int_as_float(0x7fc00000) : __fdiv_rn(__uint_as_float(most), 127.0f);
+                uint32_t w[2] = {0u, 0u};
+                if (!bad && !codes_i8(x, d, w)) {
+                    w[0] = w[1] = 0u;
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) w[i / 4] |= uint32_t(quantize_code(pick(x, i), d, 127.0f) & 255) << (8 * (i & 3));
+                }
+                *reinterpret_cast<uint2*>(to + p.c * 8) = make_uint2(w[0], w[1]);
+                if ((p.c & 3) == 0) *word = __float_as_uint(d);
+            } else {
+                const __half s = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)), m = __float2half_rn(lo);
+                const float sf = __half2float(s), mf = __half2float(m);
+                bad = bad || isinf(sf) || isinf(mf);
+                uint32_t w = 0;
+                if (!bad && !codes_u4(x, sf, mf, w)) {
+                    w = 0;
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        const float q = roundf(__fdiv_rn(__fsub_rn(pick(x, i), mf), sf));
+                        w |= uint32_t(fminf(fmaxf(q, 0.0f), 15.0f)) << (4 * i);
+                    }
+                }
+                *reinterpret_cast<uint32_t*>(to + p.c * 4) = w;
+                if ((p.c & 3) == 0)
+                    *word = bad ? 0x7e007e00u : uint32_t(__half_as_ushort(s)) | uint32_t(__half_as_ushort(m)) << 16;
+            }
+        }
     }
-    store8(static_cast<F*>(p.v ? a.v : a.k) + p.at, x);
 }
 
-template <typename F, int KIND, bool STORE>
-cudaError_t launch_io_kernel(const KvqIoArgs& a, const LaunchCtx& ctx) {
+template <typename F, int KIND, int R>
+__global__ void __launch_bounds__(kThreads) kvq_load_kernel(const KvqIoArgs a, int slots, int tb, int turns, int* err) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const Place p = place(a, slots, tb, R * turns);
+    const uint32_t* const words = static_cast<const uint32_t*>(p.v ? a.v_words : a.k_words) + p.c / 4;
+    const unsigned char* const codes =
+        static_cast<const unsigned char*>(p.v ? a.v_codes : a.k_codes) + p.c * (KIND == Q8_KVQ_I8 ? 8 : 4);
+    F* const to = static_cast<F*>(p.v ? a.v : a.k) + p.at;
+    struct Held {
+        bool in;
+        uint32_t word;
+        uint2 w;
+    } next[R], now[R];
+    const auto fetch = [&](int turn) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t t = p.first + int64_t(turn * R + r) * tb, entry = p.entry + t;
+            next[r].in = inside(a, p, t, err);
+            if (!next[r].in) continue;
+            next[r].word = words[entry * (a.dim / 32)];
+            const unsigned char* from = codes + entry * kvq_row(KIND, a.dim);
+            if constexpr (KIND == Q8_KVQ_I8) next[r].w = *reinterpret_cast<const uint2*>(from);
+            else next[r].w.x = *reinterpret_cast<const uint32_t*>(from);
+        }
+    };
+    fetch(0);
+#pragma unroll 1
+    for (int turn = 0; turn < turns; ++turn) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) now[r] = next[r];
+        if (turn + 1 < turns) fetch(turn + 1);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (!now[r].in) continue;
+            const uint2 w = now[r].w;
+            float x[8];
+            if constexpr (KIND == Q8_KVQ_I8) {
+                const float d = __uint_as_float(now[r].word);
+                const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};     // (plus 128)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = (byte_above_2_23(u[i / 4], i & 3) - 8388736.0f) * d;
+            } else {
+                const float2 sm = kvq_scale_min(now[r].word);
+                const uint32_t u[2] = {w.x & 0x0f0f0f0fu, w.x >> 4 & 0x0f0f0f0fu};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)                                       // (the product is exact)
+                    x[i] = fmaf(byte_above_2_23(u[i & 1], i >> 1) - 8388608.0f, sm.x, sm.y);
+            }
+            store8(to + (p.first + int64_t(turn * R + r) * tb) * a.ld_tok, x);
+        }
+    }
+}
+
+template <typename F, int KIND, bool STORE, int R>
+cudaError_t launch_io_kernel(const KvqIoArgs& a, int turns, const LaunchCtx& ctx) {
     const int slots = kThreads / int(a.dim / 8);
     const int tb = a.T < slots ? int(a.T) : slots, ub = slots / tb;
-    const int64_t units = 2 * a.kv_heads, seg = a.T < kSegment ? a.T : kSegment;
+    const int64_t units = 2 * a.kv_heads, seg = a.T < kSegment ? a.T : kSegment, step = int64_t(tb) * R * turns;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attrs[1];
-    cfg.gridDim = dim3(unsigned((units + ub - 1) / ub * ((seg + tb - 1) / tb)), unsigned((a.T + kSegment - 1) / kSegment),
-                       unsigned(a.rows));
+    cfg.gridDim = dim3(unsigned((units + ub - 1) / ub * ((seg + step - 1) / step)),
+                       unsigned((a.T + kSegment - 1) / kSegment), unsigned(a.rows));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = ctx.stream;
     cfg.numAttrs = pdl_attrs(ctx, attrs);
     cfg.attrs = attrs;
-    if constexpr (STORE) return cudaLaunchKernelEx(&cfg, kvq_store_kernel<F, KIND>, a, slots, tb, ctx.dev_err);
-    return cudaLaunchKernelEx(&cfg, kvq_load_kernel<F, KIND>, a, slots, tb, ctx.dev_err);
+    if constexpr (STORE) return cudaLaunchKernelEx(&cfg, kvq_store_kernel<F, KIND, R>, a, slots, tb, turns, ctx.dev_err);
+    else return cudaLaunchKernelEx(&cfg, kvq_load_kernel<F, KIND, R>, a, slots, tb, turns, ctx.dev_err);
+}
+
+template <typename F, int KIND, bool STORE>
+cudaError_t launch_io_tokens(const KvqIoArgs& a, const LaunchCtx& ctx) {
+    const int64_t threads = a.rows * a.T * a.kv_heads * (a.dim / 4), all = int64_t(2048) * ctx.num_sms;
+    const int64_t tb = kThreads / (a.dim / 8);
+    if (a.T >= 16 * tb && threads >= 16 * all) return launch_io_kernel<F, KIND, STORE, 4>(a, 4, ctx);
+    if (a.T >= 4 * tb && threads >= 4 * all) return launch_io_kernel<F, KIND, STORE, 4>(a, 1, ctx);
+    return launch_io_kernel<F, KIND, STORE, 1>(a, 1, ctx);
 }
 
 template <bool STORE>
 cudaError_t launch_io(const KvqIoArgs& a, const LaunchCtx& ctx) {
     if (a.kind == Q8_KVQ_I8) {
-        if (a.type == Q8_KV_F32) return launch_io_kernel<float, Q8_KVQ_I8, STORE>(a, ctx);
-        if (a.type == Q8_KV_F16) return launch_io_kernel<__half, Q8_KVQ_I8, STORE>(a, ctx);
-        return launch_io_kernel<__nv_bfloat16, Q8_KVQ_I8, STORE>(a, ctx);
+        if (a.type == Q8_KV_F32) return launch_io_tokens<float, Q8_KVQ_I8, STORE>(a, ctx);
+        if (a.type == Q8_KV_F16) return launch_io_tokens<__half, Q8_KVQ_I8, STORE>(a, ctx);
+        return launch_io_tokens<__nv_bfloat16, Q8_KVQ_I8, STORE>(a, ctx);
     }
-    if (a.type == Q8_KV_F32) return launch_io_kernel<float, Q8_KVQ_U4, STORE>(a, ctx);
-    if (a.type == Q8_KV_F16) return launch_io_kernel<__half, Q8_KVQ_U4, STORE>(a, ctx);
-    return launch_io_kernel<__nv_bfloat16, Q8_KVQ_U4, STORE>(a, ctx);
+    if (a.type == Q8_KV_F32) return launch_io_tokens<float, Q8_KVQ_U4, STORE>(a, ctx);
+    if (a.type == Q8_KV_F16) return launch_io_tokens<__half, Q8_KVQ_U4, STORE>(a, ctx);
+    return launch_io_tokens<__nv_bfloat16, Q8_KVQ_U4, STORE>(a, ctx);
 }
 
 }  // namespace

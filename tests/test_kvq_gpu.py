@@ -121,6 +121,13 @@ def test_store_sizes(kind, rows, T, kv_heads):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,T,kv_heads,dim", [(1, 4001, 9, 160), (2, 9001, 5, 64), (3, 7000, 8, 128)])
+def test_store_long_prompts(kind, rows, T, kv_heads, dim):
+    """Several tokens a thread, in turns."""
+    store_and_check(kind, "bf16", rows, T, kv_heads, dim, T + 5, list(range(rows)), lens=[T, T - 700, 3][:rows], seed=T)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("src", FLOATS)
 def test_store_padded_batches(kind, src):
     store_and_check(kind, src, 6, 70, 2, 64, 90, [0, 1, 20, 5, 7, 3], lens=[70, 0, 1, -3, 1 << 30, 33], seed=5, pad=64)
