@@ -76,42 +76,58 @@ __device__ __forceinline__ float pick(const float (&x)[8], int i) {
     return y;
 }
 
-// Eight values' place: whose head and eight of it are the thread's own, tokens are not.
-struct Place {
-    int64_t at;          // values from the floats' beginning, of token 0
-    int64_t entry;       // (row, head, entry) in one line, of token 0
-    int64_t first, end;  // the thread's first token, and the row's end of them
-    int64_t pos;
-    bool v;              // of V
-    int c;               // which eight of the head
-};
-
-__device__ __forceinline__ Place place(const KvqIoArgs& a, int slots, int tb, int r) {
-    const int c8 = int(a.dim) / 8, slot = threadIdx.x / c8, c = threadIdx.x - slot * c8;
-    const int64_t m = blockIdx.z, t_first = int64_t(blockIdx.y) * kSegment;
-    const int ub = slots / tb, units = int(a.kv_heads) * 2, ublocks = (units + ub - 1) / ub;
-    const int uu = slot / tb, unit = int(blockIdx.x % ublocks) * ub + uu;
-    Place p;
-    p.first = t_first + int64_t(blockIdx.x / ublocks) * (int64_t(tb) * r) + (slot - uu * tb);
-    p.end = a.T < t_first + kSegment ? a.T : t_first + kSegment;
-    const int64_t len = a.lens ? a.lens[m] : a.T;
-    p.pos = a.pos ? a.pos[m] : 0;
-    p.end = p.end < len ? p.end : len;
-    if (slot >= slots || uu >= ub || unit >= units) p.end = 0;
-    p.v = unit >= a.kv_heads;
-    const int64_t h = p.v ? unit - a.kv_heads : unit;
-    p.at = m * a.ld_row + h * a.dim + c * 8;
-    p.entry = (m * a.kv_heads + h) * a.n_pos + p.pos;
-    p.c = c;
-    return p;
+// The smallest and the largest of eight and of the four neighbours' (a block); NaN if one is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
-// Whether token t is the row's, and its entry in the cache.
-__device__ __forceinline__ bool inside(const KvqIoArgs& a, const Place& p, int64_t t, int* err) {
-    if (t >= p.end) return false;
-    if (p.pos + t >= 0 && p.pos + t < a.n_pos) return true;
-    if (p.c == 0) atomicExch(err, Q8_DEVERR_POSITION);
-    return false;
+__device__ __forceinline__ float2 block_range(const Eight<float>& e) {
+    float x[8];
+    expand8(e, x);
+    float lo = min_nan(min_nan(min_nan(x[0], x[1], x[2]), x[3], x[4]), min_nan(x[5], x[6], x[7]));
+    float hi = max_nan(max_nan(max_nan(x[0], x[1], x[2]), x[3], x[4]), max_nan(x[5], x[6], x[7]));
+#pragma unroll
+    for (int k = 1; k < 4; k *= 2) {
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, k));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, k));
+    }
+    return make_float2(lo, hi);
+}
+
+// 16-bit types in their own, two at a time; then the smallest and the largest's negative as one word.
+template <typename F>
+__device__ __forceinline__ float2 block_range(const Eight<F>& e) {
+    using P = typename std::conditional<std::is_same<F, __half>::value, __half2, __nv_bfloat162>::type;
+    const int w[4] = {e.w[0].x, e.w[0].y, e.w[0].z, e.w[0].w};
+    const P a = *reinterpret_cast<const P*>(&w[0]), b = *reinterpret_cast<const P*>(&w[1]);
+    const P c = *reinterpret_cast<const P*>(&w[2]), d = *reinterpret_cast<const P*>(&w[3]);
+    const P lo = __hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d)), hi = __hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d));
+    const uint32_t l = *reinterpret_cast<const uint32_t*>(&lo), h = *reinterpret_cast<const uint32_t*>(&hi) ^ 0x80008000u;
+    const uint32_t first = __byte_perm(l, h, 0x5410), second = __byte_perm(l, h, 0x7632);
+    P m = __hmin2_nan(*reinterpret_cast<const P*>(&first), *reinterpret_cast<const P*>(&second));
+#pragma unroll
+    for (int k = 1; k < 4; k *= 2) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&m), k);
+        m = __hmin2_nan(m, *reinterpret_cast<const P*>(&other));
+    }
+    return make_float2(float(m.x), -float(m.y));
 }
 
 // 2^23 plus byte j of w (a conversion instruction runs at a quarter of this one's rate).
@@ -121,10 +137,23 @@ __device__ __forceinline__ float byte_above_2_23(uint32_t w, int j) {
 
 constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: a sum with it is an integer in its low bits
 
-// Codes of x / d (i8) by way of 1 / d.  The product is within 127 * 1.5 * 2^-23 of the quotient and
-// that within 127 * 2^-24 of its rounding, 3.1e-5 in all: where it lies 2^-14 or more from
-// every half, both round to the same integer.  False: some value lies nearer.
-__device__ __forceinline__ bool codes_i8(const float (&x)[8], float d, uint32_t (&w)[2]) {
+// round_half_away(x / d) as the formats define it, the quotient rounded to binary32 first, of
+// x >= 0 and 2^-100 < d < 2^126, from any r near enough that the answer is floor(r) or one
+// more.  With h = floor(r) + 1/2, the rounded quotient reaches h where x / d >= h - u, u half
+// a step of binary32 below h (h is even, so u itself rounds up): where x - h d, exact in one
+// multiply-add (its operands cancel but for some bits), is at least -u d.
+__device__ __forceinline__ float half_away(float x, float d, float r) {
+    const float n = __fsub_rn(__fadd_rd(r, 8388608.0f), 8388608.0f);
+    const float rest = fmaf(-(n + 0.5f), d, x);
+    const float u = __uint_as_float(__float_as_uint(r) & 0x7f800000u) * 0x1p-24f;
+    return rest >= -(u * d) ? n + 1.0f : n;
+}
+
+// Codes by way of 1 / d.  The product is within 127 * 1.5 * 2^-23 of the quotient and that
+// within 127 * 2^-24 of its rounding, 3.1e-5 in all: where it lies 2^-14 or more from every
+// half, both round to the same integer.  Elsewhere (of 16-bit values many quotients are halves)
+// half_away decides.
+__device__ __forceinline__ void codes_i8(const float (&x)[8], float d, uint32_t (&w)[2]) {
     const float inv = d == 0.0f ? 0.0f : __frcp_rn(d);
     float far = 0.0f, n[8];
 #pragma unroll
@@ -133,28 +162,86 @@ __device__ __forceinline__ bool codes_i8(const float (&x)[8], float d, uint32_t 
         n[i] = __fadd_rn(r, kMagic);
         far = fmaxf(far, fabsf(r - __fsub_rn(n[i], kMagic)));
     }
+    if (!(d > 0x1p-100f && d < 0x1p126f)) {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t code = uint32_t(quantize_code(pick(x, i), d, 127.0f) & 255) << (8 * (i & 3));
+            w[i / 4] = i & 3 ? w[i / 4] | code : code;
+        }
+        return;
+    }
+    if (far >= 0.5f - 0x1p-14f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            n[i] = __fadd_rn(copysignf(half_away(fabsf(x[i]), d, __fmul_rn(fabsf(x[i]), inv)), x[i]), kMagic);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         w[i] = __byte_perm(__byte_perm(__float_as_uint(n[4 * i]), __float_as_uint(n[4 * i + 1]), 0x0040),
                            __byte_perm(__float_as_uint(n[4 * i + 2]), __float_as_uint(n[4 * i + 3]), 0x0040), 0x5410);
-    return far < 0.5f - 0x1p-14f && d < 0x1p126f && (d == 0.0f || d > 0x1p-100f);
 }
 
-// The same of (x - m) / s, which may lie outside [0, 15].
-__device__ __forceinline__ bool codes_u4(const float (&x)[8], float s, float m, uint32_t& w) {
+// The same of (x - m) / s, which the rounding of m may push out of [0, 15] (lo, hi: the smallest
+// and largest x).
+__device__ __forceinline__ uint32_t codes_u4(const float (&x)[8], float s, float m, float lo, float hi) {
     const float inv = s == 0.0f ? 0.0f : __frcp_rn(s);
     float far = 0.0f, n[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float r = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], m), inv), 0.0f), 15.0f);
+        const float r = __fmul_rn(__fsub_rn(x[i], m), inv);
         n[i] = __fsub_rn(__fadd_rn(r, kMagic), kMagic);
         far = fmaxf(far, fabsf(r - n[i]));
+    }
+    if (far >= 0.5f - 0x1p-14f || (lo - m) * inv < -0.25f || (hi - m) * inv > 15.25f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float y = fminf(fmaxf(__fsub_rn(x[i], m), 0.0f), 15.0f * s);
+            n[i] = s == 0.0f ? 0.0f : half_away(y, s, __fmul_rn(y, inv));
+        }
     }
     uint32_t b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(__fadd_rn(fmaf(n[2 * i + 1], 16.0f, n[2 * i]), kMagic));
-    w = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    return far < 0.5f - 0x1p-14f;
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+
+// A thread's eight values of a head; its tokens are `first`, counted from the grid plane's
+// first one, and every tb-th behind.
+struct Place {
+    int first, end;      // the row's tokens end there
+    int lo, hi;          // those whose entries lie in the cache
+    int64_t at;          // the first token's floats
+    int64_t entry;       // and entry, (row, head, entry) in one line
+    bool v;              // of V
+    int c;               // which eight of the head
+};
+
+__device__ __forceinline__ Place place(const KvqIoArgs& a, int slots, int tb, int every) {
+    const int c8 = int(a.dim) / 8, slot = threadIdx.x / c8, c = threadIdx.x - slot * c8;
+    const int64_t m = blockIdx.z, plane = int64_t(blockIdx.y) * kSegment;
+    const int ub = slots / tb, units = int(a.kv_heads) * 2, ublocks = (units + ub - 1) / ub;
+    const int uu = slot / tb, block = int(blockIdx.x) / ublocks, unit = (int(blockIdx.x) - block * ublocks) * ub + uu;
+    Place p;
+    p.first = block * every + (slot - uu * tb);
+    const int64_t len = a.lens ? a.lens[m] : a.T, pos = a.pos ? a.pos[m] : 0;
+    const auto within = [&](int64_t t) { return int(t < plane ? 0 : t > plane + kSegment ? kSegment : t - plane); };
+    p.end = slot < slots && uu < ub && unit < units ? within(len < a.T ? len : a.T) : 0;
+    p.lo = within(-pos);
+    p.hi = within(a.n_pos - pos);
+    p.v = unit >= a.kv_heads;
+    const int64_t h = p.v ? unit - a.kv_heads : unit;
+    p.at = m * a.ld_row + (plane + p.first) * a.ld_tok + h * a.dim + c * 8;
+    p.entry = (m * a.kv_heads + h) * a.n_pos + pos + plane + p.first;
+    p.c = c;
+    return p;
+}
+
+// Whether token t is the row's, and its entry in the cache.
+__device__ __forceinline__ bool inside(const Place& p, int t, int* err) {
+    if (t >= p.end) return false;
+    if (t >= p.lo && t < p.hi) return true;
+    if (p.c == 0) atomicExch(err, Q8_DEVERR_POSITION);
+    return false;
 }
 
 // R tokens at a time and thread, tb apart, whose reads go out together, `turns` times; a
@@ -163,21 +250,26 @@ template <typename F, int KIND, int R>
 __global__ void __launch_bounds__(kThreads) kvq_store_kernel(const KvqIoArgs a, int slots, int tb, int turns, int* err) {
     pdl_wait();
     pdl_launch_dependents();
-    const Place p = place(a, slots, tb, R * turns);
+    const Place p = place(a, slots, tb, tb * R * turns);
     Eight<F> next[R], now[R];
     bool in_next[R], in[R];
-    const F* const from = static_cast<const F*>(p.v ? a.v : a.k) + p.at;
+    const F* from = static_cast<const F*>(p.v ? a.v : a.k) + p.at;
+    const int64_t step = tb * a.ld_tok;
     const auto fetch = [&](int turn) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t t = p.first + int64_t(turn * R + r) * tb;
-            in_next[r] = inside(a, p, t, err);
-            if (in_next[r]) fetch8(from + t * a.ld_tok, next[r]);
+            in_next[r] = inside(p, p.first + (turn * R + r) * tb, err);
+#pragma unroll
+            for (int i = 0; i < int(sizeof(F) / 2); ++i) next[r].w[i] = make_int4(0, 0, 0, 0);
+            if (in_next[r]) fetch8(from, next[r]);
+            from += step;
         }
     };
     fetch(0);
-    uint32_t* const words = static_cast<uint32_t*>(p.v ? a.v_words : a.k_words);
-    unsigned char* const codes = static_cast<unsigned char*>(p.v ? a.v_codes : a.k_codes);
+    const int words_row = int(a.dim) / 32, codes_row = int(kvq_row(KIND, a.dim));
+    uint32_t* const words = static_cast<uint32_t*>(p.v ? a.v_words : a.k_words) + p.entry * words_row + p.c / 4;
+    unsigned char* const codes = static_cast<unsigned char*>(p.v ? a.v_codes : a.k_codes) + p.entry * codes_row +
+                                 p.c * (KIND == Q8_KVQ_I8 ? 8 : 4);
 #pragma unroll 1
     for (int turn = 0; turn < turns; ++turn) {
 #pragma unroll
@@ -185,56 +277,29 @@ __global__ void __launch_bounds__(kThreads) kvq_store_kernel(const KvqIoArgs a, 
         if (turn + 1 < turns) fetch(turn + 1);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float x[8] = {};
-            if (in[r]) expand8(now[r], x);
-            // (magnitudes as integers: infinities and NaN are the largest)
-            uint32_t most = 0;
-            float lo = x[0], hi = x[0];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                most = max(most, __float_as_uint(x[i]) & 0x7fffffffu);
-                lo = fminf(lo, x[i]);
-                hi = fmaxf(hi, x[i]);
-            }
-#pragma unroll
-            for (int k = 1; k < 4; k *= 2) {
-                most = max(most, __shfl_xor_sync(0xffffffffu, most, k));
-                if constexpr (KIND == Q8_KVQ_U4) {
-                    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, k));
-                    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, k));
-                }
-            }
+            const float2 range = block_range(now[r]);
             if (!in[r]) continue;
-            const int64_t entry = p.entry + p.first + int64_t(turn * R + r) * tb;
-            uint32_t* const word = words + entry * (a.dim / 32) + p.c / 4;
-            unsigned char* const to = codes + entry * kvq_row(KIND, a.dim);
-            bool bad = most >= 0x7f800000u;                    // the block reads back as NaN
+            const float lo = range.x, hi = range.y;
+            float x[8];
+            expand8(now[r], x);
+            const int o = (turn * R + r) * tb;
+            uint32_t* const word = words + o * words_row;
+            unsigned char* const to = codes + o * codes_row;
             if constexpr (KIND == Q8_KVQ_I8) {
-                const float d = bad ? __int_as_float(0x7fc00000) : __fdiv_rn(__uint_as_float(most), 127.0f);
+                const float most = fmaxf(-lo, hi);
+                // (infinities and NaN: the block reads back as NaN)
+                const float d = lo - lo == 0.0f && hi - hi == 0.0f ? __fdiv_rn(most, 127.0f) : __int_as_float(0x7fc00000);
                 uint32_t w[2] = {0u, 0u};
-                if (!bad && !codes_i8(x, d, w)) {
-                    w[0] = w[1] = 0u;
-#pragma unroll 1
-                    for (int i = 0; i < 8; ++i) w[i / 4] |= uint32_t(quantize_code(pick(x, i), d, 127.0f) & 255) << (8 * (i & 3));
-                }
-                *reinterpret_cast<uint2*>(to + p.c * 8) = make_uint2(w[0], w[1]);
+                if (d > 0.0f) codes_i8(x, d, w);
+                *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
                 if ((p.c & 3) == 0) *word = __float_as_uint(d);
             } else {
                 const __half s = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)), m = __float2half_rn(lo);
                 const float sf = __half2float(s), mf = __half2float(m);
-                bad = bad || isinf(sf) || isinf(mf);
-                uint32_t w = 0;
-                if (!bad && !codes_u4(x, sf, mf, w)) {
-                    w = 0;
-#pragma unroll 1
-                    for (int i = 0; i < 8; ++i) {
-                        const float q = roundf(__fdiv_rn(__fsub_rn(pick(x, i), mf), sf));
-                        w |= uint32_t(fminf(fmaxf(q, 0.0f), 15.0f)) << (4 * i);
-                    }
-                }
-                *reinterpret_cast<uint32_t*>(to + p.c * 4) = w;
+                const bool fine = sf - sf == 0.0f && mf - mf == 0.0f;      // (s is NaN or infinite where lo or hi is)
+                *reinterpret_cast<uint32_t*>(to) = fine ? codes_u4(x, sf, mf, lo, hi) : 0u;
                 if ((p.c & 3) == 0)
-                    *word = bad ? 0x7e007e00u : uint32_t(__half_as_ushort(s)) | uint32_t(__half_as_ushort(m)) << 16;
+                    *word = fine ? uint32_t(__half_as_ushort(s)) | uint32_t(__half_as_ushort(m)) << 16 : 0x7e007e00u;
             }
         }
     }
@@ -244,11 +309,13 @@ template <typename F, int KIND, int R>
 __global__ void __launch_bounds__(kThreads) kvq_load_kernel(const KvqIoArgs a, int slots, int tb, int turns, int* err) {
     pdl_wait();
     pdl_launch_dependents();
-    const Place p = place(a, slots, tb, R * turns);
-    const uint32_t* const words = static_cast<const uint32_t*>(p.v ? a.v_words : a.k_words) + p.c / 4;
-    const unsigned char* const codes =
-        static_cast<const unsigned char*>(p.v ? a.v_codes : a.k_codes) + p.c * (KIND == Q8_KVQ_I8 ? 8 : 4);
-    F* const to = static_cast<F*>(p.v ? a.v : a.k) + p.at;
+    const Place p = place(a, slots, tb, tb * R * turns);
+    const int words_row = int(a.dim) / 32, codes_row = int(kvq_row(KIND, a.dim));
+    const uint32_t* const words = static_cast<const uint32_t*>(p.v ? a.v_words : a.k_words) + p.entry * words_row + p.c / 4;
+    const unsigned char* const codes = static_cast<const unsigned char*>(p.v ? a.v_codes : a.k_codes) +
+                                       p.entry * codes_row + p.c * (KIND == Q8_KVQ_I8 ? 8 : 4);
+    F* to = static_cast<F*>(p.v ? a.v : a.k) + p.at;
+    const int64_t step = tb * a.ld_tok;
     struct Held {
         bool in;
         uint32_t word;
@@ -257,13 +324,12 @@ __global__ void __launch_bounds__(kThreads) kvq_load_kernel(const KvqIoArgs a, i
     const auto fetch = [&](int turn) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t t = p.first + int64_t(turn * R + r) * tb, entry = p.entry + t;
-            next[r].in = inside(a, p, t, err);
+            const int o = (turn * R + r) * tb;
+            next[r].in = inside(p, p.first + o, err);
             if (!next[r].in) continue;
-            next[r].word = words[entry * (a.dim / 32)];
-            const unsigned char* from = codes + entry * kvq_row(KIND, a.dim);
-            if constexpr (KIND == Q8_KVQ_I8) next[r].w = *reinterpret_cast<const uint2*>(from);
-            else next[r].w.x = *reinterpret_cast<const uint32_t*>(from);
+            next[r].word = words[o * words_row];
+            if constexpr (KIND == Q8_KVQ_I8) next[r].w = *reinterpret_cast<const uint2*>(codes + o * codes_row);
+            else next[r].w.x = *reinterpret_cast<const uint32_t*>(codes + o * codes_row);
         }
     };
     fetch(0);
@@ -273,7 +339,7 @@ __global__ void __launch_bounds__(kThreads) kvq_load_kernel(const KvqIoArgs a, i
         for (int r = 0; r < R; ++r) now[r] = next[r];
         if (turn + 1 < turns) fetch(turn + 1);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+        for (int r = 0; r < R; ++r, to += step) {
             if (!now[r].in) continue;
             const uint2 w = now[r].w;
             float x[8];
@@ -289,7 +355,7 @@ __global__ void __launch_bounds__(kThreads) kvq_load_kernel(const KvqIoArgs a, i
                 for (int i = 0; i < 8; ++i)                                       // (the product is exact)
                     x[i] = fmaf(byte_above_2_23(u[i & 1], i >> 1) - 8388608.0f, sm.x, sm.y);
             }
-            store8(to + (p.first + int64_t(turn * R + r) * tb) * a.ld_tok, x);
+            store8(to, x);
         }
     }
 }
