@@ -1,9 +1,9 @@
 // kvq.cu -- tokens stored into quantised K/V caches, and entries read back as floats.
 //
-// A thread has eight values of one head of one token; four neighbours share a block and
-// exchange its extremes by two shuffles.  A CTA takes up to 256 / (head_dim / 8) tokens of
-// one head, whose codes and words are one run of the cache, or, where a row has fewer
-// tokens, those of several heads.
+// A thread has some values of one head of one token: 16 of a store, where two neighbours
+// share a block and exchange its extremes, and 8 of a load.  A CTA takes as many tokens of
+// one head as it has threads for, whose codes and words are one run of the cache, or, where
+// a row has fewer tokens, those of several heads.
 #include "kvq.cuh"
 
 #include <cuda_bf16.h>
@@ -15,22 +15,18 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int64_t kSegment = 65536;   // tokens a grid plane
 
-// Eight floats as they lie in memory.
+constexpr int kStored = 16, kLoaded = 8;   // values a thread
+
+// kStored floats as they lie in memory.
 template <typename F>
-struct Eight {
-    int4 w[sizeof(F) / 2];
+struct Floats {
+    int4 w[sizeof(F)];
 };
 
 template <typename F>
-__device__ __forceinline__ void fetch8(const F* p, Eight<F>& e) {
+__device__ __forceinline__ void expand(const Floats<F>& e, float (&x)[kStored]) {
 #pragma unroll
-    for (int i = 0; i < int(sizeof(F) / 2); ++i) e.w[i] = __ldcs(reinterpret_cast<const int4*>(p) + i);
-}
-
-template <typename F>
-__device__ __forceinline__ void expand8(const Eight<F>& e, float (&x)[8]) {
-#pragma unroll
-    for (int i = 0; i < int(sizeof(F) / 2); ++i) {
+    for (int i = 0; i < int(sizeof(F)); ++i) {
         const int w[4] = {e.w[i].x, e.w[i].y, e.w[i].z, e.w[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -38,10 +34,10 @@ __device__ __forceinline__ void expand8(const Eight<F>& e, float (&x)[8]) {
                 x[4 * i + j] = __int_as_float(w[j]);
             } else if constexpr (std::is_same<F, __half>::value) {
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-                x[2 * j] = f.x, x[2 * j + 1] = f.y;
+                x[8 * i + 2 * j] = f.x, x[8 * i + 2 * j + 1] = f.y;
             } else {
-                x[2 * j] = __int_as_float(w[j] << 16);
-                x[2 * j + 1] = __int_as_float(w[j] & int(0xffff0000));
+                x[8 * i + 2 * j] = __int_as_float(w[j] << 16);
+                x[8 * i + 2 * j + 1] = __int_as_float(w[j] & int(0xffff0000));
             }
         }
     }
@@ -69,14 +65,14 @@ __device__ __forceinline__ void store8(F* p, const float (&x)[8]) {
 }
 
 // x[i] of a register array, by selection.
-__device__ __forceinline__ float pick(const float (&x)[8], int i) {
+__device__ __forceinline__ float pick(const float (&x)[kStored], int i) {
     float y = x[0];
 #pragma unroll
-    for (int j = 1; j < 8; ++j) y = i == j ? x[j] : y;
+    for (int j = 1; j < kStored; ++j) y = i == j ? x[j] : y;
     return y;
 }
 
-// The smallest and the largest of eight and of the four neighbours' (a block); NaN if one is.
+// The smallest and the largest of a thread's values and its neighbour's (a block); NaN if one is.
 __device__ __forceinline__ float min_nan(float a, float b) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -98,35 +94,37 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
     return r;
 }
 
-__device__ __forceinline__ float2 block_range(const Eight<float>& e) {
-    float x[8];
-    expand8(e, x);
-    float lo = min_nan(min_nan(min_nan(x[0], x[1], x[2]), x[3], x[4]), min_nan(x[5], x[6], x[7]));
-    float hi = max_nan(max_nan(max_nan(x[0], x[1], x[2]), x[3], x[4]), max_nan(x[5], x[6], x[7]));
+__device__ __forceinline__ float2 block_range(const Floats<float>& e) {
+    float x[kStored];
+    expand(e, x);
+    float lo = x[0], hi = x[0];
 #pragma unroll
-    for (int k = 1; k < 4; k *= 2) {
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, k));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, k));
+    for (int i = 1; i + 1 < kStored; i += 2) {
+        lo = min_nan(lo, x[i], x[i + 1]);
+        hi = max_nan(hi, x[i], x[i + 1]);
     }
-    return make_float2(lo, hi);
+    lo = min_nan(lo, x[kStored - 1]);
+    hi = max_nan(hi, x[kStored - 1]);
+    return make_float2(min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 1)), max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 1)));
 }
 
 // 16-bit types in their own, two at a time; then the smallest and the largest's negative as one word.
 template <typename F>
-__device__ __forceinline__ float2 block_range(const Eight<F>& e) {
+__device__ __forceinline__ float2 block_range(const Floats<F>& e) {
     using P = typename std::conditional<std::is_same<F, __half>::value, __half2, __nv_bfloat162>::type;
-    const int w[4] = {e.w[0].x, e.w[0].y, e.w[0].z, e.w[0].w};
-    const P a = *reinterpret_cast<const P*>(&w[0]), b = *reinterpret_cast<const P*>(&w[1]);
-    const P c = *reinterpret_cast<const P*>(&w[2]), d = *reinterpret_cast<const P*>(&w[3]);
-    const P lo = __hmin2_nan(__hmin2_nan(a, b), __hmin2_nan(c, d)), hi = __hmax2_nan(__hmax2_nan(a, b), __hmax2_nan(c, d));
+    const int w[8] = {e.w[0].x, e.w[0].y, e.w[0].z, e.w[0].w, e.w[1].x, e.w[1].y, e.w[1].z, e.w[1].w};
+    P lo = *reinterpret_cast<const P*>(&w[0]), hi = lo;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        const P x = *reinterpret_cast<const P*>(&w[i]);
+        lo = __hmin2_nan(lo, x);
+        hi = __hmax2_nan(hi, x);
+    }
     const uint32_t l = *reinterpret_cast<const uint32_t*>(&lo), h = *reinterpret_cast<const uint32_t*>(&hi) ^ 0x80008000u;
     const uint32_t first = __byte_perm(l, h, 0x5410), second = __byte_perm(l, h, 0x7632);
     P m = __hmin2_nan(*reinterpret_cast<const P*>(&first), *reinterpret_cast<const P*>(&second));
-#pragma unroll
-    for (int k = 1; k < 4; k *= 2) {
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&m), k);
-        m = __hmin2_nan(m, *reinterpret_cast<const P*>(&other));
-    }
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&m), 1);
+    m = __hmin2_nan(m, *reinterpret_cast<const P*>(&other));
     return make_float2(float(m.x), -float(m.y));
 }
 
@@ -153,18 +151,18 @@ __device__ __forceinline__ float half_away(float x, float d, float r) {
 // within 127 * 2^-24 of its rounding, 3.1e-5 in all: where it lies 2^-14 or more from every
 // half, both round to the same integer.  Elsewhere (of 16-bit values many quotients are halves)
 // half_away decides.
-__device__ __forceinline__ void codes_i8(const float (&x)[8], float d, uint32_t (&w)[2]) {
-    const float inv = d == 0.0f ? 0.0f : __frcp_rn(d);
-    float far = 0.0f, n[8];
+__device__ __forceinline__ void codes_i8(const float (&x)[kStored], float d, uint32_t (&w)[4]) {
+    const float inv = __frcp_rn(d);
+    float far = 0.0f, n[kStored];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kStored; ++i) {
         const float r = __fmul_rn(x[i], inv);
         n[i] = __fadd_rn(r, kMagic);
         far = fmaxf(far, fabsf(r - __fsub_rn(n[i], kMagic)));
     }
     if (!(d > 0x1p-100f && d < 0x1p126f)) {
 #pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kStored; ++i) {
             const uint32_t code = uint32_t(quantize_code(pick(x, i), d, 127.0f) & 255) << (8 * (i & 3));
             w[i / 4] = i & 3 ? w[i / 4] | code : code;
         }
@@ -172,40 +170,42 @@ __device__ __forceinline__ void codes_i8(const float (&x)[8], float d, uint32_t 
     }
     if (far >= 0.5f - 0x1p-14f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < kStored; ++i)
             n[i] = __fadd_rn(copysignf(half_away(fabsf(x[i]), d, __fmul_rn(fabsf(x[i]), inv)), x[i]), kMagic);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < kStored / 4; ++i)
         w[i] = __byte_perm(__byte_perm(__float_as_uint(n[4 * i]), __float_as_uint(n[4 * i + 1]), 0x0040),
                            __byte_perm(__float_as_uint(n[4 * i + 2]), __float_as_uint(n[4 * i + 3]), 0x0040), 0x5410);
 }
 
 // The same of (x - m) / s, which the rounding of m may push out of [0, 15] (lo, hi: the smallest
 // and largest x).
-__device__ __forceinline__ uint32_t codes_u4(const float (&x)[8], float s, float m, float lo, float hi) {
+__device__ __forceinline__ uint2 codes_u4(const float (&x)[kStored], float s, float m, float lo, float hi) {
     const float inv = s == 0.0f ? 0.0f : __frcp_rn(s);
-    float far = 0.0f, n[8];
+    float far = 0.0f, n[kStored];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kStored; ++i) {
         const float r = __fmul_rn(__fsub_rn(x[i], m), inv);
         n[i] = __fsub_rn(__fadd_rn(r, kMagic), kMagic);
         far = fmaxf(far, fabsf(r - n[i]));
     }
+    // (never where s is 0: those products are)
     if (far >= 0.5f - 0x1p-14f || (lo - m) * inv < -0.25f || (hi - m) * inv > 15.25f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kStored; ++i) {
             const float y = fminf(fmaxf(__fsub_rn(x[i], m), 0.0f), 15.0f * s);
-            n[i] = s == 0.0f ? 0.0f : half_away(y, s, __fmul_rn(y, inv));
+            n[i] = half_away(y, s, __fmul_rn(y, inv));
         }
     }
-    uint32_t b[4];
+    uint32_t b[kStored / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(__fadd_rn(fmaf(n[2 * i + 1], 16.0f, n[2 * i]), kMagic));
-    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    for (int i = 0; i < kStored / 2; ++i) b[i] = __float_as_uint(__fadd_rn(fmaf(n[2 * i + 1], 16.0f, n[2 * i]), kMagic));
+    return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
 }
 
-// A thread's eight values of a head; its tokens are `first`, counted from the grid plane's
+// A thread's V values of a head; its tokens are `first`, counted from the grid plane's
 // first one, and every tb-th behind.
 struct Place {
     int first, end;      // the row's tokens end there
@@ -213,11 +213,12 @@ struct Place {
     int64_t at;          // the first token's floats
     int64_t entry;       // and entry, (row, head, entry) in one line
     bool v;              // of V
-    int c;               // which eight of the head
+    int c;               // which V of the head
 };
 
+template <int V>
 __device__ __forceinline__ Place place(const KvqIoArgs& a, int slots, int tb, int every) {
-    const int c8 = int(a.dim) / 8, slot = threadIdx.x / c8, c = threadIdx.x - slot * c8;
+    const int cv = int(a.dim) / V, slot = threadIdx.x / cv, c = threadIdx.x - slot * cv;
     const int64_t m = blockIdx.z, plane = int64_t(blockIdx.y) * kSegment;
     const int ub = slots / tb, units = int(a.kv_heads) * 2, ublocks = (units + ub - 1) / ub;
     const int uu = slot / tb, block = int(blockIdx.x) / ublocks, unit = (int(blockIdx.x) - block * ublocks) * ub + uu;
@@ -230,7 +231,7 @@ __device__ __forceinline__ Place place(const KvqIoArgs& a, int slots, int tb, in
     p.hi = within(a.n_pos - pos);
     p.v = unit >= a.kv_heads;
     const int64_t h = p.v ? unit - a.kv_heads : unit;
-    p.at = m * a.ld_row + (plane + p.first) * a.ld_tok + h * a.dim + c * 8;
+    p.at = m * a.ld_row + (plane + p.first) * a.ld_tok + h * a.dim + c * V;
     p.entry = (m * a.kv_heads + h) * a.n_pos + pos + plane + p.first;
     p.c = c;
     return p;
@@ -250,8 +251,8 @@ template <typename F, int KIND, int R>
 __global__ void __launch_bounds__(kThreads) kvq_store_kernel(const KvqIoArgs a, int slots, int tb, int turns, int* err) {
     pdl_wait();
     pdl_launch_dependents();
-    const Place p = place(a, slots, tb, tb * R * turns);
-    Eight<F> next[R], now[R];
+    const Place p = place<kStored>(a, slots, tb, tb * R * turns);
+    Floats<F> next[R] = {}, now[R];
     bool in_next[R], in[R];
     const F* from = static_cast<const F*>(p.v ? a.v : a.k) + p.at;
     const int64_t step = tb * a.ld_tok;
@@ -259,17 +260,18 @@ __global__ void __launch_bounds__(kThreads) kvq_store_kernel(const KvqIoArgs a, 
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             in_next[r] = inside(p, p.first + (turn * R + r) * tb, err);
+            if (in_next[r]) {
 #pragma unroll
-            for (int i = 0; i < int(sizeof(F) / 2); ++i) next[r].w[i] = make_int4(0, 0, 0, 0);
-            if (in_next[r]) fetch8(from, next[r]);
+                for (int i = 0; i < int(sizeof(F)); ++i) next[r].w[i] = __ldcs(reinterpret_cast<const int4*>(from) + i);
+            }
             from += step;
         }
     };
     fetch(0);
     const int words_row = int(a.dim) / 32, codes_row = int(kvq_row(KIND, a.dim));
-    uint32_t* const words = static_cast<uint32_t*>(p.v ? a.v_words : a.k_words) + p.entry * words_row + p.c / 4;
+    uint32_t* const words = static_cast<uint32_t*>(p.v ? a.v_words : a.k_words) + p.entry * words_row + p.c / 2;
     unsigned char* const codes = static_cast<unsigned char*>(p.v ? a.v_codes : a.k_codes) + p.entry * codes_row +
-                                 p.c * (KIND == Q8_KVQ_I8 ? 8 : 4);
+                                 p.c * (KIND == Q8_KVQ_I8 ? kStored : kStored / 2);
 #pragma unroll 1
     for (int turn = 0; turn < turns; ++turn) {
 #pragma unroll
@@ -280,8 +282,8 @@ __global__ void __launch_bounds__(kThreads) kvq_store_kernel(const KvqIoArgs a, 
             const float2 range = block_range(now[r]);
             if (!in[r]) continue;
             const float lo = range.x, hi = range.y;
-            float x[8];
-            expand8(now[r], x);
+            float x[kStored];
+            expand(now[r], x);
             const int o = (turn * R + r) * tb;
             uint32_t* const word = words + o * words_row;
             unsigned char* const to = codes + o * codes_row;
@@ -289,16 +291,16 @@ __global__ void __launch_bounds__(kThreads) kvq_store_kernel(const KvqIoArgs a, 
                 const float most = fmaxf(-lo, hi);
                 // (infinities and NaN: the block reads back as NaN)
                 const float d = lo - lo == 0.0f && hi - hi == 0.0f ? __fdiv_rn(most, 127.0f) : __int_as_float(0x7fc00000);
-                uint32_t w[2] = {0u, 0u};
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
                 if (d > 0.0f) codes_i8(x, d, w);
-                *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
-                if ((p.c & 3) == 0) *word = __float_as_uint(d);
+                *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                if ((p.c & 1) == 0) *word = __float_as_uint(d);
             } else {
                 const __half s = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)), m = __float2half_rn(lo);
                 const float sf = __half2float(s), mf = __half2float(m);
                 const bool fine = sf - sf == 0.0f && mf - mf == 0.0f;      // (s is NaN or infinite where lo or hi is)
-                *reinterpret_cast<uint32_t*>(to) = fine ? codes_u4(x, sf, mf, lo, hi) : 0u;
-                if ((p.c & 3) == 0)
+                *reinterpret_cast<uint2*>(to) = fine ? codes_u4(x, sf, mf, lo, hi) : make_uint2(0u, 0u);
+                if ((p.c & 1) == 0)
                     *word = fine ? uint32_t(__half_as_ushort(s)) | uint32_t(__half_as_ushort(m)) << 16 : 0x7e007e00u;
             }
         }
@@ -309,7 +311,7 @@ template <typename F, int KIND, int R>
 __global__ void __launch_bounds__(kThreads) kvq_load_kernel(const KvqIoArgs a, int slots, int tb, int turns, int* err) {
     pdl_wait();
     pdl_launch_dependents();
-    const Place p = place(a, slots, tb, tb * R * turns);
+    const Place p = place<kLoaded>(a, slots, tb, tb * R * turns);
     const int words_row = int(a.dim) / 32, codes_row = int(kvq_row(KIND, a.dim));
     const uint32_t* const words = static_cast<const uint32_t*>(p.v ? a.v_words : a.k_words) + p.entry * words_row + p.c / 4;
     const unsigned char* const codes = static_cast<const unsigned char*>(p.v ? a.v_codes : a.k_codes) +
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) kvq_load_kernel(const KvqIoArgs a, i
 
 template <typename F, int KIND, bool STORE, int R>
 cudaError_t launch_io_kernel(const KvqIoArgs& a, int turns, const LaunchCtx& ctx) {
-    const int slots = kThreads / int(a.dim / 8);
+    const int slots = kThreads / int(a.dim / (STORE ? kStored : kLoaded));
     const int tb = a.T < slots ? int(a.T) : slots, ub = slots / tb;
     const int64_t units = 2 * a.kv_heads, seg = a.T < kSegment ? a.T : kSegment, step = int64_t(tb) * R * turns;
     cudaLaunchConfig_t cfg{};
@@ -379,10 +381,12 @@ cudaError_t launch_io_kernel(const KvqIoArgs& a, int turns, const LaunchCtx& ctx
 
 template <typename F, int KIND, bool STORE>
 cudaError_t launch_io_tokens(const KvqIoArgs& a, const LaunchCtx& ctx) {
-    const int64_t threads = a.rows * a.T * a.kv_heads * (a.dim / 4), all = int64_t(2048) * ctx.num_sms;
-    const int64_t tb = kThreads / (a.dim / 8);
-    if (a.T >= 16 * tb && threads >= 16 * all) return launch_io_kernel<F, KIND, STORE, 4>(a, 4, ctx);
-    if (a.T >= 4 * tb && threads >= 4 * all) return launch_io_kernel<F, KIND, STORE, 4>(a, 1, ctx);
+    // several tokens a thread, and turns, where that leaves every SM its threads
+    constexpr int V = STORE ? kStored : kLoaded, R = STORE ? 2 : 4;
+    const int64_t threads = a.rows * a.T * a.kv_heads * (2 * a.dim / V), all = int64_t(1024) * ctx.num_sms;
+    const int64_t tb = kThreads / (a.dim / V);
+    if (a.T >= 4 * R * tb && threads >= 8 * R * all) return launch_io_kernel<F, KIND, STORE, R>(a, 4, ctx);
+    if (a.T >= R * tb && threads >= 2 * R * all) return launch_io_kernel<F, KIND, STORE, R>(a, 1, ctx);
     return launch_io_kernel<F, KIND, STORE, 1>(a, 1, ctx);
 }
 
