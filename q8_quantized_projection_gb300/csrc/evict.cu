@@ -264,6 +264,27 @@ __device__ __forceinline__ void move_items(const unsigned char* src, unsigned ch
     }
 }
 
+// acc of one row and K/V head, and the row's new position.
+template <bool CLUSTER, int kThreads>
+__device__ __forceinline__ void move_acc(const EvictArgs& a, int64_t unit, unsigned rank, unsigned size) {
+    const int64_t m = unit / a.kv_heads;
+    const int tid = threadIdx.x, from = first_moved(a)[unit];
+    if (unit == m * a.kv_heads && rank == 0 && tid == 0) {
+        // (pos may be new_pos: nobody else reads it in this kernel)
+        a.new_pos[m] = from < 0 ? a.pos[m] : int32_t(a.budget - 1);
+    }
+    const float* acc = a.acc + unit * a.n_pos;
+    float* new_acc = a.new_acc + unit * a.n_pos;
+    const int64_t as_is = from < 0 ? a.n_pos : from, me = int64_t(rank) * kThreads + tid, all = int64_t(size) * kThreads;
+    if (new_acc != acc)
+        for (int64_t i = me; i < as_is; i += all) new_acc[i] = acc[i];
+    if (from < 0) return;                                // (the whole cluster alike)
+    move_items<CLUSTER, float>(reinterpret_cast<const unsigned char*>(acc), reinterpret_cast<unsigned char*>(new_acc), 4,
+                         kept_list(a, unit), from, a.budget, kThreads, tid, true, rank, size);
+    // (every read ended before the last batch's barrier)
+    for (int64_t i = a.budget + me; i < a.n_pos; i += all) new_acc[i] = 0.0f;
+}
+
 // Cluster: acc of one row and K/V head (the first ones), or its K or V in one
 // column slice of 16 << lanes_log bytes.
 template <bool CLUSTER, int kThreads>
@@ -276,22 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
     const int64_t units = a.rows * a.kv_heads, cluster = blockIdx.x / size;
     const int tid = threadIdx.x;
     if (cluster < units) {
-        const int64_t unit = cluster, m = unit / a.kv_heads;
-        const int from = first_moved(a)[unit];
-        if (unit == m * a.kv_heads && rank == 0 && tid == 0) {
-            // (pos may be new_pos: nobody else reads it in this kernel)
-            a.new_pos[m] = from < 0 ? a.pos[m] : int32_t(a.budget - 1);
-        }
-        const float* acc = a.acc + unit * a.n_pos;
-        float* new_acc = a.new_acc + unit * a.n_pos;
-        const int64_t as_is = from < 0 ? a.n_pos : from, me = int64_t(rank) * kThreads + tid, all = int64_t(size) * kThreads;
-        if (new_acc != acc)
-            for (int64_t i = me; i < as_is; i += all) new_acc[i] = acc[i];
-        if (from < 0) return;                                // (the whole cluster alike)
-        move_items<CLUSTER, float>(reinterpret_cast<const unsigned char*>(acc), reinterpret_cast<unsigned char*>(new_acc), 4,
-                             kept_list(a, unit), from, a.budget, kThreads, tid, true, rank, size);
-        // (every read ended before the last batch's barrier)
-        for (int64_t i = a.budget + me; i < a.n_pos; i += all) new_acc[i] = 0.0f;
+        move_acc<CLUSTER, kThreads>(a, cluster, rank, size);
         return;
     }
     const int64_t id = cluster - units;
@@ -306,58 +312,86 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
                         col < row_bytes, rank, size);
 }
 
-// The same over quantised caches, head-major: a CTA has acc of one row and K/V head, or
-// one of its four planes (codes and words of K and of V), whole entries of `bytes` in
-// pieces of V.
-template <typename V>
-__device__ __forceinline__ void move_plane(unsigned char* base, int bytes, const int32_t* idx, int64_t from, int64_t budget) {
-    const int lanes = bytes / int(sizeof(V)), rows = int(blockDim.x) / lanes;
-    const int mine = threadIdx.x / lanes, col = (threadIdx.x - mine * lanes) * int(sizeof(V));
-    move_items<false, V>(base + col, base + col, bytes, idx, from, budget, rows, mine, mine < rows, 0, 1);
+// The same over quantised caches, head-major.  Cluster: the codes of one row, K/V head and
+// one of K and V, in one column slice of `lanes` pieces of 16 bytes; behind those, the words
+// of one; behind those, acc.
+template <bool CLUSTER, typename V>
+__device__ __forceinline__ void move_plane(unsigned char* base, int bytes, int lanes, int slice, const int32_t* idx,
+                                           int64_t from, int64_t budget, unsigned rank, unsigned size) {
+    const int rows = int(blockDim.x) / lanes, mine = threadIdx.x / lanes;
+    const int col = (slice * lanes + threadIdx.x - mine * lanes) * int(sizeof(V));
+    move_items<CLUSTER, V>(base + col, base + col, bytes, idx, from, budget, rows, mine, mine < rows && col < bytes, rank,
+                           size);
 }
 
-template <int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_move_kvq_kernel(const EvictArgs a, int row) {
+template <bool CLUSTER, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+    evict_move_kvq_kernel(const EvictArgs a, int row, int lanes, int slices) {
+    const unsigned rank = CLUSTER ? cg::this_cluster().block_rank() : 0;
+    const unsigned size = CLUSTER ? cg::this_cluster().num_blocks() : 1;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t units = a.rows * a.kv_heads, unit = blockIdx.x % units, m = unit / a.kv_heads;
-    const int plane = int(blockIdx.x / units), tid = threadIdx.x;
-    const int from = first_moved(a)[unit];
-    if (plane == 0) {
-        if (unit == m * a.kv_heads && tid == 0) a.new_pos[m] = from < 0 ? a.pos[m] : int32_t(a.budget - 1);
-        const float* acc = a.acc + unit * a.n_pos;
-        float* new_acc = a.new_acc + unit * a.n_pos;
-        const int64_t as_is = from < 0 ? a.n_pos : from;
-        if (new_acc != acc)
-            for (int64_t i = tid; i < as_is; i += kThreads) new_acc[i] = acc[i];
-        if (from < 0) return;
-        move_items<false, float>(reinterpret_cast<const unsigned char*>(acc), reinterpret_cast<unsigned char*>(new_acc), 4,
-                                 kept_list(a, unit), from, a.budget, kThreads, tid, true, 0, 1);
-        for (int64_t i = a.budget + tid; i < a.n_pos; i += kThreads) new_acc[i] = 0.0f;
+    const int64_t units = a.rows * a.kv_heads, moves = units * 2 * slices;
+    int64_t id = blockIdx.x / size;
+    if (id < moves) {
+        const int slice = int(id % slices), kv = int(id / slices % 2);
+        const int64_t unit = id / slices / 2;
+        const int from = first_moved(a)[unit];
+        if (from < 0) return;                                // (the whole cluster alike)
+        unsigned char* base = static_cast<unsigned char*>(kv ? a.v : a.k) + unit * a.n_pos * row;
+        move_plane<CLUSTER, int4>(base, row, lanes, slice, kept_list(a, unit), from, a.budget, rank, size);
         return;
     }
-    if (from < 0) return;
-    if (plane <= 2) {
-        unsigned char* base = static_cast<unsigned char*>(plane == 1 ? a.k : a.v) + unit * a.n_pos * row;
-        move_plane<int4>(base, row, kept_list(a, unit), from, a.budget);
-    } else {
-        const int bytes = int(a.dim) / 8;
-        unsigned char* base = reinterpret_cast<unsigned char*>(plane == 3 ? a.k_words : a.v_words) + unit * a.n_pos * bytes;
-        if (bytes % 16 == 0) move_plane<int4>(base, bytes, kept_list(a, unit), from, a.budget);
-        else move_plane<int>(base, bytes, kept_list(a, unit), from, a.budget);
+    id -= moves;
+    if (id < 2 * units) {
+        const int64_t unit = id / 2;
+        const int from = first_moved(a)[unit], bytes = int(a.dim) / 8;
+        if (from < 0) return;
+        unsigned char* base = reinterpret_cast<unsigned char*>(id % 2 ? a.v_words : a.k_words) + unit * a.n_pos * bytes;
+        if (bytes % 16 == 0)
+            move_plane<CLUSTER, int4>(base, bytes, bytes / 16, 0, kept_list(a, unit), from, a.budget, rank, size);
+        else
+            move_plane<CLUSTER, int>(base, bytes, bytes / 4, 0, kept_list(a, unit), from, a.budget, rank, size);
+        return;
     }
+    move_acc<CLUSTER, kThreads>(a, id - 2 * units, rank, size);
+}
+
+template <bool CLUSTER, int kThreads>
+cudaError_t launch_move_kvq_as(const EvictArgs& a, int size, int row, int lanes, int slices, const LaunchCtx& ctx) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attrs[2];
+    cfg.gridDim = dim3(unsigned(a.rows * a.kv_heads * (3 + 2 * slices) * size));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = ctx.stream;
+    cfg.numAttrs = pdl_attrs(ctx, attrs);
+    if (CLUSTER) {
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attrs[cfg.numAttrs].val.clusterDim.x = unsigned(size);
+        attrs[cfg.numAttrs].val.clusterDim.y = 1;
+        attrs[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    cfg.attrs = attrs;
+    return cudaLaunchKernelEx(&cfg, evict_move_kvq_kernel<CLUSTER, kThreads>, a, row, lanes, slices);
 }
 
 cudaError_t launch_move_kvq(const EvictArgs& a, const LaunchCtx& ctx) {
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attrs[1];
-    cfg.gridDim = dim3(unsigned(a.rows * a.kv_heads * 5));
-    cfg.blockDim = dim3(512);
-    cfg.stream = ctx.stream;
-    cfg.numAttrs = pdl_attrs(ctx, attrs);
-    cfg.attrs = attrs;
-    return cudaLaunchKernelEx(&cfg, evict_move_kvq_kernel<512>, a,
-                              int(a.kv_type == kKvQuantised + Q8_KVQ_U4 ? a.dim / 2 : a.dim));
+    const int row = int(a.kv_type == kKvQuantised + Q8_KVQ_U4 ? a.dim / 2 : a.dim), chunks = row / 16;
+    // Up to two CTAs an SM that walk codes, first by clusters of three batches a CTA and more
+    // (4 x 8 heads of 128 bytes, 24576 of 32768 entries: 171 us alone, 131 in pairs, 98 in
+    // fours, 107 in eights), then by slices of 64 bytes at least (1 x 8 heads, 40000 of 65536:
+    // eights 65 us, 54 in two slices, 62 in four); 256 threads where even single CTAs are more
+    // (64 x 8 heads of 32 bytes, 150 of 300: 24 and 17 us; of 128, 1000 of 2000: 68 and 62).
+    const int64_t ctas = a.rows * a.kv_heads * 2, most = 2 * int64_t(ctx.num_sms), batch = int64_t(512 / chunks) * kBatch;
+    int size = 1, slices = 1;
+    while (size < kMaxCluster && ctas * size * 2 <= most && a.budget >= 3 * batch * size * 2) size *= 2;
+    while (ctas * size * slices * 2 <= most && chunks >= 8 * slices) slices *= 2;
+    const int lanes = (chunks + slices - 1) / slices;
+    slices = (chunks + lanes - 1) / lanes;
+    if (size > 1) return launch_move_kvq_as<true, 512>(a, size, row, lanes, slices, ctx);
+    if (ctas > most) return launch_move_kvq_as<false, 256>(a, 1, row, lanes, slices, ctx);
+    return launch_move_kvq_as<false, 512>(a, 1, row, lanes, slices, ctx);
 }
 
 template <int THREADS>
