@@ -448,7 +448,7 @@ struct AttnKvq {
     static constexpr int SUB = CH <= 4 ? 2 : 1, KT = 16 * SUB;
     static constexpr int CODES = KT * PITCH, WORDS = KT * WB, STAGE = 2 * (CODES + WORDS);
     // CTAs an SM: by registers (of the sums of the output and of q), and stages by shared memory
-    static constexpr int CTAS = NH == 1 ? (CH <= 4 ? 4 : CH <= 12 ? 3 : 2) : NB <= 4 ? 3 : 2, MAX_CTAS = kKvqMaxCtas;
+    static constexpr int CTAS = NH == 1 ? (NB <= 2 && CH <= 4 ? 4 : CH <= 12 ? 3 : 2) : NB <= 2 ? 3 : 2, MAX_CTAS = kKvqMaxCtas;
     static constexpr int RING = (CTAS == 4 ? 12 : CTAS == 3 ? 16 : 24) * 1024;
     static constexpr int S0 = RING / STAGE, S = S0 > 6 ? 6 : S0;
     static constexpr int TK = kAttnWarps * KT;
