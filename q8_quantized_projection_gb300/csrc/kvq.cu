@@ -1,9 +1,18 @@
 // kvq.cu -- tokens stored into quantised K/V caches, and entries read back as floats.
 //
 // A thread has some values of one head of one token: 16 of a store, where two neighbours
-// share a block and exchange its extremes, and 8 of a load.  A CTA takes as many tokens of
+// share a block and exchange its extremes, and 16 bytes of them of a load.  A CTA takes as many tokens of
 // one head as it has threads for, whose codes and words are one run of the cache, or, where
 // a row has fewer tokens, those of several heads.
+//
+// What bounds them.  Long prompts: a store of 16-bit floats its instructions (some 22 a
+// value, of which 9 are the code and, where a quotient in the warp is near a half, 14 more to
+// decide it; 4 rows of 16384 tokens, 8 K/V heads of 128 values: bf16 102 us in 4 bits, 111 in
+// 8, 3.5 and 3.8 TB/s; binary32 109 and 115, 5.7 and 6.0 TB/s); a load HBM (60 and 67 us into
+// bf16, 98 and 106 into binary32, 5.9 to 6.5 TB/s).  Single tokens: the launch, 1.8 us each.
+// A reciprocal in place of divisions, three-operand extremes and 16 values a thread made the
+// first 102 us of 167; turns that read ahead took a load from 155 to 131 us (2 rows of 65536,
+// bf16), 32-bit places within a grid plane to 113.
 #include "kvq.cuh"
 
 #include <cuda_bf16.h>
@@ -15,7 +24,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int64_t kSegment = 65536;   // tokens a grid plane
 
-constexpr int kStored = 16, kLoaded = 8;   // values a thread
+// Values a thread: of a load, 16 bytes of floats (twice as many, and lanes that write every other
+// 16 bytes, read back 2 x 65536 bf16 entries in 130 us, not 113).
+constexpr int kStored = 16;
+template <typename F>
+constexpr int kLoaded = 16 / int(sizeof(F));
 
 // kStored floats as they lie in memory.
 template <typename F>
@@ -43,24 +56,26 @@ __device__ __forceinline__ void expand(const Floats<F>& e, float (&x)[kStored]) 
     }
 }
 
-template <typename F>
-__device__ __forceinline__ void store8(F* p, const float (&x)[8]) {
-    if constexpr (sizeof(F) == 4) {
-        __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
-        __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
-    } else {
-        int w[4];
+template <typename F, int V>
+__device__ __forceinline__ void put(F* p, const float (&x)[V]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (std::is_same<F, __half>::value) {
-                const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-                w[i] = *reinterpret_cast<const int*>(&h);
-            } else {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-                w[i] = *reinterpret_cast<const int*>(&h);
+    for (int i = 0; i < V; i += 16 / int(sizeof(F))) {
+        if constexpr (sizeof(F) == 4) {
+            __stcs(reinterpret_cast<float4*>(p + i), make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+        } else {
+            int w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (std::is_same<F, __half>::value) {
+                    const __half2 h = __floats2half2_rn(x[i + 2 * j], x[i + 2 * j + 1]);
+                    w[j] = *reinterpret_cast<const int*>(&h);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(x[i + 2 * j], x[i + 2 * j + 1]);
+                    w[j] = *reinterpret_cast<const int*>(&h);
+                }
             }
+            __stcs(reinterpret_cast<int4*>(p + i), make_int4(w[0], w[1], w[2], w[3]));
         }
-        __stcs(reinterpret_cast<int4*>(p), make_int4(w[0], w[1], w[2], w[3]));
     }
 }
 
@@ -147,12 +162,19 @@ __device__ __forceinline__ float half_away(float x, float d, float r) {
     return rest >= -(u * d) ? n + 1.0f : n;
 }
 
-// Codes by way of 1 / d.  The product is within 127 * 1.5 * 2^-23 of the quotient and that
-// within 127 * 2^-24 of its rounding, 3.1e-5 in all: where it lies 2^-14 or more from every
-// half, both round to the same integer.  Elsewhere (of 16-bit values many quotients are halves)
-// half_away decides.
+// 1 / x within 2^-23, of a normal x and result.
+__device__ __forceinline__ float reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Codes by way of 1 / d.  The product is within 127 * 1.5 * 2^-23 of the quotient (1 / d, and
+// its own rounding) and that within 127 * 2^-24 of its rounding, 3.1e-5 in all: where it lies
+// 2^-14 or more from every half, both round to the same integer.  Elsewhere (of 16-bit values
+// many quotients are halves) half_away decides.
 __device__ __forceinline__ void codes_i8(const float (&x)[kStored], float d, uint32_t (&w)[4]) {
-    const float inv = __frcp_rn(d);
+    const float inv = reciprocal(d);
     float far = 0.0f, n[kStored];
 #pragma unroll
     for (int i = 0; i < kStored; ++i) {
@@ -180,9 +202,9 @@ __device__ __forceinline__ void codes_i8(const float (&x)[kStored], float d, uin
 }
 
 // The same of (x - m) / s, which the rounding of m may push out of [0, 15] (lo, hi: the smallest
-// and largest x).
+// and largest x).  Of at most 15.25, the product is within 3.7e-6 of the rounded quotient.
 __device__ __forceinline__ uint2 codes_u4(const float (&x)[kStored], float s, float m, float lo, float hi) {
-    const float inv = s == 0.0f ? 0.0f : __frcp_rn(s);
+    const float inv = s == 0.0f ? 0.0f : reciprocal(s);
     float far = 0.0f, n[kStored];
 #pragma unroll
     for (int i = 0; i < kStored; ++i) {
@@ -191,7 +213,7 @@ __device__ __forceinline__ uint2 codes_u4(const float (&x)[kStored], float s, fl
         far = fmaxf(far, fabsf(r - n[i]));
     }
     // (never where s is 0: those products are)
-    if (far >= 0.5f - 0x1p-14f || (lo - m) * inv < -0.25f || (hi - m) * inv > 15.25f) {
+    if (far >= 0.5f - 0x1p-17f || (lo - m) * inv < -0.25f || (hi - m) * inv > 15.25f) {
 #pragma unroll
         for (int i = 0; i < kStored; ++i) {
             const float y = fminf(fmaxf(__fsub_rn(x[i], m), 0.0f), 15.0f * s);
@@ -309,19 +331,19 @@ __global__ void __launch_bounds__(kThreads) kvq_store_kernel(const KvqIoArgs a, 
 
 template <typename F, int KIND, int R>
 __global__ void __launch_bounds__(kThreads) kvq_load_kernel(const KvqIoArgs a, int slots, int tb, int turns, int* err) {
+    constexpr int V = kLoaded<F>, BYTES = KIND == Q8_KVQ_I8 ? V : V / 2, W = (BYTES + 3) / 4;   // values, bytes and words of codes
     pdl_wait();
     pdl_launch_dependents();
-    const Place p = place<kLoaded>(a, slots, tb, tb * R * turns);
+    const Place p = place<V>(a, slots, tb, tb * R * turns);
     const int words_row = int(a.dim) / 32, codes_row = int(kvq_row(KIND, a.dim));
-    const uint32_t* const words = static_cast<const uint32_t*>(p.v ? a.v_words : a.k_words) + p.entry * words_row + p.c / 4;
-    const unsigned char* const codes = static_cast<const unsigned char*>(p.v ? a.v_codes : a.k_codes) +
-                                       p.entry * codes_row + p.c * (KIND == Q8_KVQ_I8 ? 8 : 4);
+    const uint32_t* const words = static_cast<const uint32_t*>(p.v ? a.v_words : a.k_words) + p.entry * words_row + p.c / (32 / V);
+    const unsigned char* const codes =
+        static_cast<const unsigned char*>(p.v ? a.v_codes : a.k_codes) + p.entry * codes_row + p.c * BYTES;
     F* to = static_cast<F*>(p.v ? a.v : a.k) + p.at;
     const int64_t step = tb * a.ld_tok;
     struct Held {
         bool in;
-        uint32_t word;
-        uint2 w;
+        uint32_t word, w[W];
     } next[R], now[R];
     const auto fetch = [&](int turn) {
 #pragma unroll
@@ -330,8 +352,15 @@ __global__ void __launch_bounds__(kThreads) kvq_load_kernel(const KvqIoArgs a, i
             next[r].in = inside(p, p.first + o, err);
             if (!next[r].in) continue;
             next[r].word = words[o * words_row];
-            if constexpr (KIND == Q8_KVQ_I8) next[r].w = *reinterpret_cast<const uint2*>(codes + o * codes_row);
-            else next[r].w.x = *reinterpret_cast<const uint32_t*>(codes + o * codes_row);
+            const unsigned char* from = codes + o * codes_row;
+            if constexpr (BYTES == 8) {
+                const uint2 x = *reinterpret_cast<const uint2*>(from);
+                next[r].w[0] = x.x, next[r].w[W - 1] = x.y;
+            } else if constexpr (BYTES == 4) {
+                next[r].w[0] = *reinterpret_cast<const uint32_t*>(from);
+            } else {
+                next[r].w[0] = *reinterpret_cast<const uint16_t*>(from);
+            }
         }
     };
     fetch(0);
@@ -343,28 +372,30 @@ __global__ void __launch_bounds__(kThreads) kvq_load_kernel(const KvqIoArgs a, i
 #pragma unroll
         for (int r = 0; r < R; ++r, to += step) {
             if (!now[r].in) continue;
-            const uint2 w = now[r].w;
-            float x[8];
-            if constexpr (KIND == Q8_KVQ_I8) {
-                const float d = __uint_as_float(now[r].word);
-                const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};     // (plus 128)
+            float x[V];
+            const float2 sm = KIND == Q8_KVQ_U4 ? kvq_scale_min(now[r].word) : make_float2(__uint_as_float(now[r].word), 0.0f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = (byte_above_2_23(u[i / 4], i & 3) - 8388736.0f) * d;
-            } else {
-                const float2 sm = kvq_scale_min(now[r].word);
-                const uint32_t u[2] = {w.x & 0x0f0f0f0fu, w.x >> 4 & 0x0f0f0f0fu};
+            for (int k = 0; k < W; ++k) {
+                const uint32_t w = now[r].w[k];
+                if constexpr (KIND == Q8_KVQ_I8) {
+                    const uint32_t u = w ^ 0x80808080u;                           // (plus 128)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)                                       // (the product is exact)
-                    x[i] = fmaf(byte_above_2_23(u[i & 1], i >> 1) - 8388608.0f, sm.x, sm.y);
+                    for (int i = 0; i < 4; ++i) x[4 * k + i] = (byte_above_2_23(u, i) - 8388736.0f) * sm.x;
+                } else {
+                    const uint32_t u[2] = {w & 0x0f0f0f0fu, w >> 4 & 0x0f0f0f0fu};
+#pragma unroll
+                    for (int i = 0; i < (V < 8 ? V : 8); ++i)                     // (the product is exact)
+                        x[8 * k + i] = fmaf(byte_above_2_23(u[i & 1], i >> 1) - 8388608.0f, sm.x, sm.y);
+                }
             }
-            store8(to, x);
+            put(to, x);
         }
     }
 }
 
 template <typename F, int KIND, bool STORE, int R>
 cudaError_t launch_io_kernel(const KvqIoArgs& a, int turns, const LaunchCtx& ctx) {
-    const int slots = kThreads / int(a.dim / (STORE ? kStored : kLoaded));
+    const int slots = kThreads / int(a.dim / (STORE ? kStored : kLoaded<F>));
     const int tb = a.T < slots ? int(a.T) : slots, ub = slots / tb;
     const int64_t units = 2 * a.kv_heads, seg = a.T < kSegment ? a.T : kSegment, step = int64_t(tb) * R * turns;
     cudaLaunchConfig_t cfg{};
@@ -382,7 +413,7 @@ cudaError_t launch_io_kernel(const KvqIoArgs& a, int turns, const LaunchCtx& ctx
 template <typename F, int KIND, bool STORE>
 cudaError_t launch_io_tokens(const KvqIoArgs& a, const LaunchCtx& ctx) {
     // several tokens a thread, and turns, where that leaves every SM its threads
-    constexpr int V = STORE ? kStored : kLoaded, R = STORE ? 2 : 4;
+    constexpr int V = STORE ? kStored : kLoaded<F>, R = STORE ? 2 : 4;
     const int64_t threads = a.rows * a.T * a.kv_heads * (2 * a.dim / V), all = int64_t(1024) * ctx.num_sms;
     const int64_t tb = kThreads / (a.dim / V);
     if (a.T >= 4 * R * tb && threads >= 8 * R * all) return launch_io_kernel<F, KIND, STORE, R>(a, 4, ctx);
