@@ -478,7 +478,15 @@ q8_status kvq_load(int kvq_type, const void* k_codes, const void* k_words, const
 /*
  * attn_decode over a quantised cache: the same arguments, results, limits and
  * errors, with the cache's values as they stand for, and a workspace by the
- * same rules (one may serve both in turn).
+ * same rules (one may serve both in turn).  Scores, weights and sums are
+ * binary32; q enters the first product with 22 bits of values down to 2^-28
+ * (Q8_KVQ_U4: 2^-24) of its head's largest, weights times scales enter the
+ * second with 24, sums of up to 96 products are truncated where binary32 would
+ * round, and Q8_KVQ_U4's values enter as m + s code or (m + 15 s) - s (15 - code),
+ * so errors are relative to what a block's codes span; of Q8_KVQ_U4, what
+ * a weight times a scale adds below 2^-119 is lost.  A visible block of
+ * NaN makes its K/V head's outputs (in V: the block's own) NaN, and a query head
+ * with an infinity or a NaN is NaN.
  */
 q8_status kvq_attn_decode(const float* q, int64_t ldq, int kvq_type, const void* k_codes,
                           const void* k_words, const void* v_codes, const void* v_words, int64_t rows,

@@ -23,6 +23,24 @@
 // and one stage of the output, joined by rounded binary32 additions, and four-bit codes,
 // which have no sign, enter the output's with both signs (see `turned`).
 //
+// What bounds it.  Four bits: instructions.  16 entries of 128 values are 360 of them a warp
+// (four query heads: 24 products, 90 to unpack codes, 100 to scale and part the weights, 40 to
+// scale the scores), a product holds a scheduler's issue for some 5 clocks beside its 8 of the
+// tensor pipe, and together they take some 600 clocks where the bytes at HBM's rate take 430:
+// 0.58 issued a clock with two to four warps a scheduler alike.  Eight bits: HBM, with eight
+// query heads the instructions again.  And some 15 us a call to begin and to end: the launch,
+// positions, q as operands, the first stages, the join of parts.  tcgen05 would take the
+// products out of the way, but not what is around them, and V's scales, one a block of values
+// and not of entries, make the second product's other operand another one for every 32 values:
+// its smallest tile (64 or 128 values) would read all of V's 16-bit operand from shared memory
+// for every block of it, 128 KB for 128 entries of 128 values, more clocks than their bytes
+// take.
+//
+// Measured (16 rows of 16384 entries, 8 K/V heads of 128 values; device time): 4 bits, four query
+// heads 77 us, 4.4 TB/s (5.6 TB/s between 16384 and 32768 entries), eight 108 us; 8 bits 107 us,
+// 5.7 TB/s (6.5), and 123 us; 64 rows of 4100 to 8192 4-bit entries 110 us; one row of 130001
+// with the weights accumulated 52 us; one row of 613 9.6 us, of one entry 5.0 us.
+//
 // Layout.  Entries are the m of the first product, and its n = 8 columns the parts of q: four
 // query heads' first and second parts side by side, or eight heads' first parts and a second
 // product of their second ones.  So a lane ends with entries g and g + 8 of 16 for one head
@@ -447,7 +465,8 @@ struct AttnKvq {
     static constexpr int WB = 4 * NB, WC = NB % 4 == 0 ? 16 : NB % 2 == 0 ? 8 : 4, WN = WB / WC;
     static constexpr int SUB = CH <= 4 ? 2 : 1, KT = 16 * SUB;
     static constexpr int CODES = KT * PITCH, WORDS = KT * WB, STAGE = 2 * (CODES + WORDS);
-    // CTAs an SM: by registers (of the sums of the output and of q), and stages by shared memory
+    // CTAs an SM: what registers allow without spills of more than some words (of four heads of
+    // 128 4-bit values 112 us with 128 registers, 112 with 168; of eight 126 with 168, 108 with 255)
     static constexpr int CTAS = NH == 1 ? (NB <= 2 && CH <= 4 ? 4 : CH <= 12 ? 3 : 2) : NB <= 2 ? 3 : 2, MAX_CTAS = kKvqMaxCtas;
     static constexpr int RING = (CTAS == 4 ? 12 : CTAS == 3 ? 16 : 24) * 1024;
     static constexpr int S0 = RING / STAGE, S = S0 > 6 ? 6 : S0;
