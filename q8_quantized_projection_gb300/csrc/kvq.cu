@@ -414,12 +414,16 @@ cudaError_t launch_io_kernel(const KvqIoArgs& a, int turns, const LaunchCtx& ctx
 
 template <typename F, int KIND, bool STORE>
 cudaError_t launch_io_tokens(const KvqIoArgs& a, const LaunchCtx& ctx) {
-    // several tokens a thread, and turns, where that leaves every SM its threads
+    // Several tokens a thread, and turns of them, as soon as there are threads for it (us, by turns of
+    // none, 1 and 4: 1 row of 512 tokens of 8 heads of 128 values, bf16 in 4 bits, stored 3.5, 3.0, 6.2,
+    // read back 2.9, 2.3, 3.9; of 2048: 6.7, 6.3, 6.2 and 7.0, 5.0, 3.9; 8 rows of 2048: 45, 39, 28 and
+    // 46, 21, 14).  Eight turns of a store from some more on (2 rows of 65536: 197 and 182).
     constexpr int V = STORE ? kStored : kLoaded<F>, R = STORE ? 2 : 4;
-    const int64_t threads = a.rows * a.T * a.kv_heads * (2 * a.dim / V), all = int64_t(1024) * ctx.num_sms;
+    const int64_t threads = a.rows * a.T * a.kv_heads * (2 * a.dim / V), sms = ctx.num_sms;
     const int64_t tb = kThreads / (a.dim / V);
-    if (a.T >= 4 * R * tb && threads >= 8 * R * all) return launch_io_kernel<F, KIND, STORE, R>(a, 4, ctx);
-    if (a.T >= R * tb && threads >= 2 * R * all) return launch_io_kernel<F, KIND, STORE, R>(a, 1, ctx);
+    if (STORE && a.T >= 8 * R * tb && threads >= 25600 * sms) return launch_io_kernel<F, KIND, STORE, R>(a, 8, ctx);
+    if (a.T >= 4 * R * tb && threads >= (STORE ? 2048 : 3072) * sms) return launch_io_kernel<F, KIND, STORE, R>(a, 4, ctx);
+    if (a.T >= R * tb && threads >= (STORE ? 320 : 640) * sms) return launch_io_kernel<F, KIND, STORE, R>(a, 1, ctx);
     return launch_io_kernel<F, KIND, STORE, 1>(a, 1, ctx);
 }
 

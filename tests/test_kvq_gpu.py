@@ -129,6 +129,30 @@ def test_store_long_prompts(kind, rows, T, kv_heads, dim):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("src", FLOATS)
+def test_long_prompts_are_their_pieces(kind, src):
+    """The longest walks of a store and a load against calls of some tokens each."""
+    t = torch()
+    g = t.Generator(device="cuda").manual_seed(12)
+    qkv = t.randn(2, 17001, 6 * 1024, device="cuda", generator=g).to(dt(src))
+    k, v = qkv[..., 4096:5120], qkv[..., 5120:]
+    whole, pieces = (native.kvq_cache(kind, 2, 17010, 8, 128) for _ in range(2))
+    pos, lens = [3, 0], [17001, 16400]
+    native.kvq_store(k, v, i32(pos), whole, lens=i32(lens))
+    for a in range(0, 17001, 97):
+        native.kvq_store(k[:, a:a + 97], v[:, a:a + 97], i32([p + a for p in pos]), pieces, lens=i32([n - a for n in lens]))
+    for x, y in zip(whole, pieces):
+        assert t.equal(x.view(t.uint8), y.view(t.uint8))
+    outs = [t.zeros(2, 17001, 2048, device="cuda", dtype=dt(src)) for _ in range(2)]
+    native.kvq_load(whole, outs[0][..., :1024], outs[0][..., 1024:], pos=i32(pos), lens=i32(lens))
+    for a in range(0, 17001, 97):
+        part = outs[1][:, a:a + 97]
+        native.kvq_load(whole, part[..., :1024], part[..., 1024:], pos=i32([p + a for p in pos]), lens=i32([n - a for n in lens]))
+    assert t.equal(*outs)
+    no_error()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("src", FLOATS)
 def test_store_padded_batches(kind, src):
     store_and_check(kind, src, 6, 70, 2, 64, 90, [0, 1, 20, 5, 7, 3], lens=[70, 0, 1, -3, 1 << 30, 33], seed=5, pad=64)
 
