@@ -160,7 +160,8 @@ constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: a sum with it is an integ
 __device__ __forceinline__ float half_away(float x, float d, float r) {
     const float n = __fsub_rn(__fadd_rd(r, 8388608.0f), 8388608.0f);
     const float rest = fmaf(-(n + 0.5f), d, x);
-    const float u = __uint_as_float(__float_as_uint(r) & 0x7f800000u) * 0x1p-24f;
+    // (the binade below h: floor(r)'s, and that of 1/4 below 1/2, whatever r is rounded to)
+    const float u = __uint_as_float(__float_as_uint(fmaxf(n, 0.25f)) & 0x7f800000u) * 0x1p-24f;
     return rest >= -(u * d) ? n + 1.0f : n;
 }
 

@@ -211,6 +211,25 @@ def test_store_rounds_as_the_format_says_near_halves(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_store_rounds_next_to_exact_halves(kind):
+    """Steps that are powers of two: every half of them, and its neighbours on both sides."""
+    most = 15 if kind == "u4" else 127
+    half = (np.arange(most, dtype=np.float32) + np.float32(0.5))
+    near = np.concatenate([half, np.nextafter(half, np.float32(0)), np.nextafter(half, np.float32(999))])
+    near = np.concatenate([near, np.nextafter(near, np.float32(0)), -near if kind == "i8" else near])
+    n = (len(near) + 29) // 30
+    x = np.zeros((1, 12 * n, 6, 32), dtype=np.float32)
+    for i, k in enumerate((-20, -10, -3, -1, 0, 1, 2, 5, 9, 11, -14, 3)):
+        for b in range(n):
+            part = near[30 * b:30 * b + 30]
+            x[0, i * n + b, :, :len(part)] = part * np.float32(2.0 ** k)
+            x[0, i * n + b, :, 31] = most * np.float32(2.0 ** k)          # (and the least, 0, at 30)
+    store_and_check(kind, "f32", 1, 12 * n, 1, 32, 12 * n, [0], x=x.reshape(1, 12 * n, 192))
+    want = kr.quantise(x[0, 5 * n:6 * n, 0], kind)[0]
+    assert want.max() == most and len(np.unique(want)) > most
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_store_strides(kind):
     """Tokens before rows, rows of separate tensors, one row's columns."""
     t = torch()
