@@ -5,14 +5,15 @@
 // one head as it has threads for, whose codes and words are one run of the cache, or, where
 // a row has fewer tokens, those of several heads.
 //
-// What bounds them.  Long prompts: a store of 16-bit floats its instructions (some 22 a
-// value, of which 9 are the code and, where a quotient in the warp is near a half, 14 more to
-// decide it; 4 rows of 16384 tokens, 8 K/V heads of 128 values: bf16 102 us in 4 bits, 111 in
-// 8, 3.5 and 3.8 TB/s; binary32 109 and 115, 5.7 and 6.0 TB/s); a load HBM (60 and 67 us into
-// bf16, 98 and 106 into binary32, 5.9 to 6.5 TB/s).  Single tokens: the launch, 1.8 us each.
+// What bounds them.  Long prompts: a store of 16-bit floats its instructions (some 18 a
+// value, of which 9 are the code and, where a quotient near it is near a half, 13 more to
+// decide it; 4 rows of 16384 tokens, 8 K/V heads of 128 values: bf16 80 us in 4 bits, 85 in
+// 8, 4.4 and 4.9 TB/s; binary32 102 and 111, 6.1 and 6.2 TB/s); a load HBM (58 and 66 us into
+// bf16, 98 and 106 into binary32, 6.1 to 6.5 TB/s).  Single tokens: the launch, 1.8 us each.
 // A reciprocal in place of divisions, three-operand extremes and 16 values a thread made the
-// first 102 us of 167; turns that read ahead took a load from 155 to 131 us (2 rows of 65536,
-// bf16), 32-bit places within a grid plane to 113.
+// first 102 us of 167, eight turns 96, halves decided for a few values at a time 89 (8 bits: 108
+// to 96); turns that read ahead took a load from 155 to 131 us (2 rows of 65536, bf16), 32-bit
+// places within a grid plane to 113.
 #include "kvq.cuh"
 
 #include <cuda_bf16.h>
@@ -23,7 +24,9 @@ namespace q8 {
 
 namespace {
 
-constexpr int kThreads = 256;
+// (Of 256, whose registers fit twice an SM and leave a quarter of them idle, the stores above took
+// 89 and 96, 105 and 113 us; of 64 the same as here.)
+constexpr int kThreads = 128;
 constexpr int64_t kSegment = 65536;   // tokens a grid plane
 
 // Values a thread: of a load, 16 bytes of floats (twice as many, and lanes that write every other
@@ -157,12 +160,13 @@ constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: a sum with it is an integ
 // more.  With h = floor(r) + 1/2, the rounded quotient reaches h where x / d >= h - u, u half
 // a step of binary32 below h (h is even, so u itself rounds up): where x - h d, exact in one
 // multiply-add (its operands cancel but for some bits), is at least -u d.
-__device__ __forceinline__ float half_away(float x, float d, float r) {
+// `tiny` is d * 2^-24.
+__device__ __forceinline__ float half_away(float x, float d, float tiny, float r) {
     const float n = __fsub_rn(__fadd_rd(r, 8388608.0f), 8388608.0f);
     const float rest = fmaf(-(n + 0.5f), d, x);
     // (the binade below h: floor(r)'s, and that of 1/4 below 1/2, whatever r is rounded to)
-    const float u = __uint_as_float(__float_as_uint(fmaxf(n, 0.25f)) & 0x7f800000u) * 0x1p-24f;
-    return rest >= -(u * d) ? n + 1.0f : n;
+    const float binade = __uint_as_float(__float_as_uint(fmaxf(n, 0.25f)) & 0x7f800000u);
+    return rest >= -(binade * tiny) ? n + 1.0f : n;
 }
 
 // 1 / x within 2^-23, of a normal x and result.
@@ -176,14 +180,15 @@ __device__ __forceinline__ float reciprocal(float x) {
 // its own rounding) and that within 127 * 2^-24 of its rounding, 3.1e-5 in all: where it lies
 // 2^-14 or more from every half, both round to the same integer.  Elsewhere (of 16-bit values
 // many quotients are halves) half_away decides.
+template <int G>
 __device__ __forceinline__ void codes_i8(const float (&x)[kStored], float d, uint32_t (&w)[4]) {
     const float inv = reciprocal(d);
-    float far = 0.0f, n[kStored];
+    float far[kStored / G] = {}, n[kStored];
 #pragma unroll
     for (int i = 0; i < kStored; ++i) {
         const float r = __fmul_rn(x[i], inv);
         n[i] = __fadd_rn(r, kMagic);
-        far = fmaxf(far, fabsf(r - __fsub_rn(n[i], kMagic)));
+        far[i / G] = fmaxf(far[i / G], fabsf(r - __fsub_rn(n[i], kMagic)));
     }
     if (!(d > 0x1p-100f && d < 0x1p126f)) {
 #pragma unroll 1
@@ -193,10 +198,13 @@ __device__ __forceinline__ void codes_i8(const float (&x)[kStored], float d, uin
         }
         return;
     }
-    if (far >= 0.5f - 0x1p-14f) {
+    const float tiny = d * 0x1p-24f;
 #pragma unroll
-        for (int i = 0; i < kStored; ++i)
-            n[i] = __fadd_rn(copysignf(half_away(fabsf(x[i]), d, __fmul_rn(fabsf(x[i]), inv)), x[i]), kMagic);
+    for (int g = 0; g < kStored; g += G) {
+        if (far[g / G] < 0.5f - 0x1p-14f) continue;
+#pragma unroll
+        for (int i = g; i < g + G; ++i)
+            n[i] = __fadd_rn(copysignf(half_away(fabsf(x[i]), d, tiny, __fmul_rn(fabsf(x[i]), inv)), x[i]), kMagic);
     }
 #pragma unroll
     for (int i = 0; i < kStored / 4; ++i)
@@ -206,21 +214,26 @@ __device__ __forceinline__ void codes_i8(const float (&x)[kStored], float d, uin
 
 // The same of (x - m) / s, which the rounding of m may push out of [0, 15] (lo, hi: the smallest
 // and largest x).  Of at most 15.25, the product is within 3.7e-6 of the rounded quotient.
+template <int G>
 __device__ __forceinline__ uint2 codes_u4(const float (&x)[kStored], float s, float m, float lo, float hi) {
     const float inv = s == 0.0f ? 0.0f : reciprocal(s);
-    float far = 0.0f, n[kStored];
+    float far[kStored / G] = {}, n[kStored];
 #pragma unroll
     for (int i = 0; i < kStored; ++i) {
         const float r = __fmul_rn(__fsub_rn(x[i], m), inv);
         n[i] = __fsub_rn(__fadd_rn(r, kMagic), kMagic);
-        far = fmaxf(far, fabsf(r - n[i]));
+        far[i / G] = fmaxf(far[i / G], fabsf(r - n[i]));
     }
-    // (never where s is 0: those products are)
-    if (far >= 0.5f - 0x1p-17f || (lo - m) * inv < -0.25f || (hi - m) * inv > 15.25f) {
+    // (neither where s is 0: those products are)
+    const bool outside = (lo - m) * inv < -0.25f || (hi - m) * inv > 15.25f;
+    const float tiny = s * 0x1p-24f;
 #pragma unroll
-        for (int i = 0; i < kStored; ++i) {
+    for (int g = 0; g < kStored; g += G) {
+        if (far[g / G] < 0.5f - 0x1p-17f && !outside) continue;
+#pragma unroll
+        for (int i = g; i < g + G; ++i) {
             const float y = fminf(fmaxf(__fsub_rn(x[i], m), 0.0f), 15.0f * s);
-            n[i] = half_away(y, s, __fmul_rn(y, inv));
+            n[i] = half_away(y, s, tiny, __fmul_rn(y, inv));
         }
     }
     uint32_t b[kStored / 2];
@@ -317,14 +330,14 @@ __global__ void __launch_bounds__(kThreads) kvq_store_kernel(const KvqIoArgs a, 
                 // (infinities and NaN: the block reads back as NaN)
                 const float d = lo - lo == 0.0f && hi - hi == 0.0f ? __fdiv_rn(most, 127.0f) : __int_as_float(0x7fc00000);
                 uint32_t w[4] = {0u, 0u, 0u, 0u};
-                if (d > 0.0f) codes_i8(x, d, w);
+                if (d > 0.0f) codes_i8<kStored / (sizeof(F) == 4 ? 2 : 4)>(x, d, w);
                 *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
                 if ((p.c & 1) == 0) *word = __float_as_uint(d);
             } else {
                 const __half s = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)), m = __float2half_rn(lo);
                 const float sf = __half2float(s), mf = __half2float(m);
                 const bool fine = sf - sf == 0.0f && mf - mf == 0.0f;      // (s is NaN or infinite where lo or hi is)
-                *reinterpret_cast<uint2*>(to) = fine ? codes_u4(x, sf, mf, lo, hi) : make_uint2(0u, 0u);
+                *reinterpret_cast<uint2*>(to) = fine ? codes_u4<8>(x, sf, mf, lo, hi) : make_uint2(0u, 0u);
                 if ((p.c & 1) == 0)
                     *word = fine ? uint32_t(__half_as_ushort(s)) | uint32_t(__half_as_ushort(m)) << 16 : 0x7e007e00u;
             }
@@ -416,14 +429,16 @@ cudaError_t launch_io_kernel(const KvqIoArgs& a, int turns, const LaunchCtx& ctx
 template <typename F, int KIND, bool STORE>
 cudaError_t launch_io_tokens(const KvqIoArgs& a, const LaunchCtx& ctx) {
     // Several tokens a thread, and turns of them, as soon as there are threads for it (us, by turns of
-    // none, 1 and 4: 1 row of 512 tokens of 8 heads of 128 values, bf16 in 4 bits, stored 3.5, 3.0, 6.2,
-    // read back 2.9, 2.3, 3.9; of 2048: 6.7, 6.3, 6.2 and 7.0, 5.0, 3.9; 8 rows of 2048: 45, 39, 28 and
-    // 46, 21, 14).  Eight turns of a store from some more on (2 rows of 65536: 197 and 182).
+    // none, 1 and 4: 1 row of 512 tokens of 8 heads of 128 values, bf16 in 4 bits, stored 2.6, 2.6, 4.5,
+    // read back 3.5, 2.2, 3.2; of 2048: 6.0, 5.4, 5.6 and 6.8, 4.7, 3.8; 8 rows of 2048: 38, 32, 24 and
+    // 45, 21, 14).  Two turns of a load just below (3 rows of 1001, 5 heads of 96: one 4.7, two 3.3, four
+    // 4.0), eight of a store from some more on (4 rows of 8192: 43.6 and 42.3).
     constexpr int V = STORE ? kStored : kLoaded<F>, R = STORE ? 2 : 4;
     const int64_t threads = a.rows * a.T * a.kv_heads * (2 * a.dim / V), sms = ctx.num_sms;
     const int64_t tb = kThreads / (a.dim / V);
     if (STORE && a.T >= 8 * R * tb && threads >= 25600 * sms) return launch_io_kernel<F, KIND, STORE, R>(a, 8, ctx);
     if (a.T >= 4 * R * tb && threads >= (STORE ? 2048 : 3072) * sms) return launch_io_kernel<F, KIND, STORE, R>(a, 4, ctx);
+    if (!STORE && a.T >= 2 * R * tb && threads >= 2048 * sms) return launch_io_kernel<F, KIND, STORE, R>(a, 2, ctx);
     if (a.T >= R * tb && threads >= (STORE ? 320 : 640) * sms) return launch_io_kernel<F, KIND, STORE, R>(a, 1, ctx);
     return launch_io_kernel<F, KIND, STORE, 1>(a, 1, ctx);
 }
