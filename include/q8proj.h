@@ -117,8 +117,9 @@ int q8_last_cuda_error(void);
 /*
  * Synchronises `stream`, then reads and clears the device error word of the
  * current device: 0 = none, 1 = a bounded wait ran out, 2 = a KV-cache
- * position outside its cache (q8_proj_fused_kv, attn_decode, kv_evict), 3 = a
- * sampling parameter outside its range (head_sample).  *code receives it.
+ * position outside its cache (q8_proj_fused_kv, attn_decode, kv_evict, the
+ * kvq_ calls), 3 = a sampling parameter outside its range (head_sample).
+ * *code receives it.
  */
 q8_status q8_device_error(int32_t* code /* host */, void* stream);
 
