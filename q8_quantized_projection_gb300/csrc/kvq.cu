@@ -432,12 +432,12 @@ cudaError_t launch_io_tokens(const KvqIoArgs& a, const LaunchCtx& ctx) {
     // none, 1 and 4: 1 row of 512 tokens of 8 heads of 128 values, bf16 in 4 bits, stored 2.6, 2.6, 4.5,
     // read back 3.5, 2.2, 3.2; of 2048: 6.0, 5.4, 5.6 and 6.8, 4.7, 3.8; 8 rows of 2048: 38, 32, 24 and
     // 45, 21, 14).  Two turns of a load just below (3 rows of 1001, 5 heads of 96: one 4.7, two 3.3, four
-    // 4.0), eight of a store from some more on (4 rows of 8192: 43.6 and 42.3).
+    // 4.0; that row of 2048: 3.6), eight of a store from some more on (4 rows of 8192: 43.6 and 42.3).
     constexpr int V = STORE ? kStored : kLoaded<F>, R = STORE ? 2 : 4;
     const int64_t threads = a.rows * a.T * a.kv_heads * (2 * a.dim / V), sms = ctx.num_sms;
     const int64_t tb = kThreads / (a.dim / V);
     if (STORE && a.T >= 8 * R * tb && threads >= 25600 * sms) return launch_io_kernel<F, KIND, STORE, R>(a, 8, ctx);
-    if (a.T >= 4 * R * tb && threads >= (STORE ? 2048 : 3072) * sms) return launch_io_kernel<F, KIND, STORE, R>(a, 4, ctx);
+    if (a.T >= 4 * R * tb && threads >= (STORE ? 2048 : 4096) * sms) return launch_io_kernel<F, KIND, STORE, R>(a, 4, ctx);
     if (!STORE && a.T >= 2 * R * tb && threads >= 2048 * sms) return launch_io_kernel<F, KIND, STORE, R>(a, 2, ctx);
     if (a.T >= R * tb && threads >= (STORE ? 320 : 640) * sms) return launch_io_kernel<F, KIND, STORE, R>(a, 1, ctx);
     return launch_io_kernel<F, KIND, STORE, 1>(a, 1, ctx);
