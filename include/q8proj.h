@@ -468,8 +468,10 @@ q8_status kvq_store(const void* k, const void* v, int src_type, int64_t ld_row, 
  * device error 2.
  *   pos      int32 [rows] or NULL: 0
  *   lens     int32 [rows] or NULL: T
- * Rows and tokens of k and v must not overlap one another (Q8_ERR_SHAPE); k and
- * v may be columns of the same rows.
+ * Rows and tokens of k and v must not overlap one another (Q8_ERR_SHAPE), nor
+ * may a value written lie in the other one's values, in the cache, pos or lens
+ * (Q8_ERR_ARG).  What lies between the values does not count: k and v may be
+ * columns of the same rows.
  */
 q8_status kvq_load(int kvq_type, const void* k_codes, const void* k_words, const void* v_codes,
                    const void* v_words, int64_t rows, int64_t n_pos, int64_t kv_heads,

@@ -664,6 +664,33 @@ q8_status check_floats(int type, int64_t rows, int64_t T, int64_t width, int64_t
     return Q8_OK;
 }
 
+// What kvq_load writes of K, and again of V: runs of n bytes, an inner line of them, those lines one
+// behind another (check_floats' two orders of rows and tokens).
+struct Runs {
+    int64_t n, inner, inners, outer, outers;
+};
+
+Runs float_runs(int64_t elt, int64_t rows, int64_t T, int64_t width, int64_t ld_row, int64_t ld_tok) {
+    const int64_t row = rows > 1 ? ld_row * elt : 1, tok = T > 1 ? ld_tok * elt : 1;   // (a stride of one says nothing)
+    return row < tok ? Runs{width * elt, row, rows, tok, T} : Runs{width * elt, tok, T, row, rows};
+}
+
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }
+
+// Whether one of the runs from a on overlaps [b, b + nb), or, with again, one of the same runs from b on:
+// whether some o * outer + i * inner lies in [lo, hi].  Lines have gaps, so a line may reach over
+// that interval and miss it, but only the few at its ends do.
+bool runs_overlap(const Runs& r, const void* a, const void* b, int64_t nb, bool again) {
+    const int64_t d = int64_t(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+    const int64_t lo = d - r.n + 1, hi = d + nb - 1, i0 = again ? 1 - r.inners : 0, o0 = again ? 1 - r.outers : 0;
+    const int64_t first = -floor_div((r.inners - 1) * r.inner - lo, r.outer), last = floor_div(hi - i0 * r.inner, r.outer);
+    for (int64_t o = first < o0 ? o0 : first; o <= last && o < r.outers; ++o) {
+        const int64_t from = -floor_div(o * r.outer - lo, r.inner), to = floor_div(hi - o * r.outer, r.inner);
+        if ((from < i0 ? i0 : from) <= (to < r.inners ? to : r.inners - 1)) return true;
+    }
+    return false;
+}
+
 q8_status kvq_io(bool store, void* k, void* v, int type, int64_t ld_row, int64_t ld_tok, int64_t rows, int64_t T,
                  int64_t kv_heads, int64_t dim, const int32_t* pos, const int32_t* lens, int kind, void* k_codes,
                  void* k_words, void* v_codes, void* v_words, int64_t n_pos, void* stream) {
@@ -676,20 +703,18 @@ q8_status kvq_io(bool store, void* k, void* v, int type, int64_t ld_row, int64_t
     for (const void* p : all)
         if (!aligned16(p)) return Q8_ERR_ALIGN;
     const size_t pn = size_t(rows) * 4;
-    Span b[] = {{k, floats, !store},     {v, floats, !store},     {pos, pn, false},        {lens, pn, false},
-                {k_codes, codes, store}, {k_words, words, store}, {v_codes, codes, store}, {v_words, words, store}};
-    // K and V that are written may be columns of the same rows: one span then, from the
-    // first's beginning to the second's end
-    const uintptr_t ka = reinterpret_cast<uintptr_t>(k), va = reinterpret_cast<uintptr_t>(v);
-    const uintptr_t apart = (ka < va ? va - ka : ka - va) / (type == Q8_KV_F32 ? 4 : 2);
-    const int64_t width = kv_heads * dim;
-    size_t both;
-    if (!store && apart >= uintptr_t(width) && apart < uintptr_t(1) << 40 &&
-        check_floats(type, rows, T, int64_t(apart) + width, ld_row, ld_tok, true, &both) == Q8_OK) {
-        b[0] = {ka < va ? k : v, both, true};
-        b[1] = {nullptr, 0, false};
+    const Span b[] = {{k, floats, !store},     {v, floats, !store},     {pos, pn, false},        {lens, pn, false},
+                      {k_codes, codes, store}, {k_words, words, store}, {v_codes, codes, store}, {v_words, words, store}};
+    if (store) {
+        if (any_overlap(b, sizeof(b) / sizeof(b[0]))) return Q8_ERR_ARG;
+    } else {
+        // K and V that are written may be columns of the same rows, and anything may lie between their runs
+        const Runs r = float_runs(type == Q8_KV_F32 ? 4 : 2, rows, T, kv_heads * dim, ld_row, ld_tok);
+        if (runs_overlap(r, k, v, r.n, true)) return Q8_ERR_ARG;
+        for (const Span& x : b)
+            if (x.p && !x.written && (runs_overlap(r, k, x.p, int64_t(x.n), false) || runs_overlap(r, v, x.p, int64_t(x.n), false)))
+                return Q8_ERR_ARG;
     }
-    if (any_overlap(b, sizeof(b) / sizeof(b[0]))) return Q8_ERR_ARG;
     LaunchCtx ctx;
     if ((st = make_ctx(stream, ctx)) != Q8_OK) return st;
     const KvqIoArgs a{k,    v,    type, ld_row,  ld_tok,  rows,    T,       kv_heads, dim,

@@ -2,6 +2,8 @@
 touches a GPU, and their workspaces' sizes."""
 import ctypes as C
 import os
+import subprocess
+import sys
 
 import pytest
 
@@ -176,3 +178,74 @@ def test_binding_refuses_host_tensors_and_odd_heads():
     for dim in (0, 16, 40, 288):
         with pytest.raises(ValueError):
             native.kvq_cache("i8", 1, 8, 1, dim, device="cpu")
+
+
+# kvq_load's buffers, by enumeration.  Accepted calls have placeholder pointers, so they run in a process
+# that sees no GPU: it ends them with Q8_ERR_CUDA before any launch.
+_PLACES = r"""
+import ctypes as C, random, sys
+from q8_quantized_projection_gb300 import native
+lib = native.load()
+assert lib.q8_last_cuda_error() == 0
+W = 32                                        # values of a run: one head of 32, in f32 or 16 bits
+
+def load(k, v, pos, lens, planes, rows, T, ld_row, ld_tok, dst, n_pos, kind=1):
+    P = lambda x: C.c_void_p(x) if x else None
+    return lib.kvq_load(kind, *map(P, planes), rows, n_pos, 1, W, P(pos), T, P(lens), dst, P(k), P(v), ld_row, ld_tok, None)
+
+def runs(p, rows, T, ld_row, ld_tok, elt):
+    return [(p + (m * ld_row + t * ld_tok) * elt, p + (m * ld_row + t * ld_tok + W) * elt)
+            for m in range(rows) for t in range(T)]
+
+def meet(a, b):
+    return any(x < w and u < y for x, y in a for u, w in b)
+
+M = 1 << 20
+far = [100 * M, 104 * M, 108 * M, 112 * M]
+OPEN = 5
+assert load(M, 2 * M, 3 * M, 0, far, 2, 3, 96, 32, 0, 16) == OPEN
+# one token of one row, whatever lies between its K and its V, and whatever its strides say
+for ld_row, ld_tok in ((32, 32), (0, 0), (-7, 1), (1 << 62, -1 << 62)):
+    for dst in (0, 1, 2):
+        assert load(M, 9 * M, 6 * M, 7 * M, far, 1, 1, ld_row, ld_tok, dst, 16) == OPEN
+        assert load(200 * M, M, 50 * M, 60 * M, far, 1, 1, ld_row, ld_tok, dst, 16) == OPEN
+# K and V as halves of [rows][2][T][W]
+assert load(M, M + 4 * W * 4, 2 * M, 0, far, 3, 4, 8 * W, W, 0, 16) == OPEN
+# one token a row, a pitch longer than from K to V
+assert load(M, 9 * M, 6 * M, 0, far, 2, 1, 4 * M, 0, 0, 16) == OPEN
+rng = random.Random(1)
+seen = {1: 0, OPEN: 0}
+for i in range(20000):
+    dst, rows, T = rng.choice((0, 1, 2)), rng.choice((1, 1, 2, 3, 5)), rng.choice((1, 1, 2, 3, 4))
+    elt = 2 if dst else 4
+    step = 16 // elt
+    if rng.random() < 0.5:
+        ld_tok = W + step * rng.choice((0, 0, 1, 4, rng.randrange(40)))
+        ld_row = (T - 1) * ld_tok + W + step * rng.choice((0, 0, 3, rng.randrange(60)))
+    else:
+        ld_row = W + step * rng.choice((0, 0, 1, 4, rng.randrange(40)))
+        ld_tok = (rows - 1) * ld_row + W + step * rng.choice((0, 0, 3, rng.randrange(60)))
+    if rows == 1: ld_row = rng.choice((ld_row, 0, 3))
+    if T == 1: ld_tok = rng.choice((ld_tok, 0, 3))
+    span = 16 * rng.choice((8, 64, 160, 400))
+    n_pos = rng.choice((1, 2, 5))
+    at = lambda: M + 16 * rng.randrange(span // 16) if rng.random() < 0.4 else M * rng.randrange(2, 90)
+    k, v = M, M + 16 * rng.randrange(-span // 16, span // 16)
+    pos, lens, planes = at(), at() if rng.random() < 0.5 else 0, [at() for _ in range(4)]
+    both = runs(k, rows, T, ld_row, ld_tok, elt), runs(v, rows, T, ld_row, ld_tok, elt)
+    others = [(pos, pos + 4 * rows)] + [(lens, lens + 4 * rows)] * (lens > 0)
+    others += [(p, p + rows * n_pos * (W // 2, 4)[j % 2]) for j, p in enumerate(planes)]
+    want = 1 if meet(*both) or meet(both[0] + both[1], others) else OPEN
+    got = load(k, v, pos, lens, planes, rows, T, ld_row, ld_tok, dst, n_pos)
+    assert got == want, (i, got, want, dst, rows, T, ld_row, ld_tok, v - k, pos - k, lens and lens - k, [p - k for p in planes], n_pos)
+    seen[got] += 1
+assert min(seen.values()) > 2000, seen
+print("checked", seen)
+"""
+
+
+def test_kvq_load_refuses_what_overlaps_and_nothing_else(lib):
+    """Among strided runs of K and V, whatever lies between them untouched."""
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="", PYTHONPATH=build.ROOT)
+    r = subprocess.run([sys.executable, "-c", _PLACES], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "checked" in r.stdout, r.stdout + r.stderr

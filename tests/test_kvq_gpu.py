@@ -839,3 +839,46 @@ def test_binding_refuses_what_does_not_fit():
         with pytest.raises((ValueError, TypeError, native.Q8Error)):
             call(**bad)
     no_error()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dst", FLOATS)
+@pytest.mark.parametrize("rows,T,place", [(1, 1, "apart"), (1, 1, "turned"), (4, 1, "rows"), (3, 4, "halves"), (1, 4, "rows")])
+def test_load_with_buffers_between(kind, dst, rows, T, place):
+    """K and V in one line of memory with pos, lens and the cache between them, whatever order they have."""
+    t = torch()
+    kv_heads, dim, n_pos, width = 2, 96, 9, 192
+    planes, _ = filled(kind, rows, n_pos, kv_heads, dim, seed=rows + T)
+    elt = t.empty((), dtype=dt(dst)).element_size()
+    pos, lens = [(3 * m + 2) % (n_pos - T + 1) for m in range(rows)], [T] * rows
+    line = t.full((1 << 20,), 85, dtype=t.uint8, device="cuda")
+
+    def at(begin, x):
+        """x's copy at byte `begin` of the line."""
+        y = line[begin:begin + x.numel() * x.element_size()].view(x.dtype).view(x.shape)
+        y.copy_(x)
+        return y
+
+    # (the row pitch of "rows": from a row's K over 64 KB and its V on to the next)
+    pitch = {"apart": 0, "turned": 0, "rows": 1 << 17, "halves": 2 * T * width * elt}[place]
+    k0, v0 = (1 << 17, 0) if place == "turned" else (0, T * width * elt) if place == "halves" else (0, 1 << 16)
+    tok = 2 * width if place == "rows" else width
+    ko, vo = (line[b:].view(dt(dst)).as_strided((rows, T, width), (pitch // elt, tok, 1)) for b in (k0, v0))
+    mid = (1 << 19) if place == "halves" else (1 << 14)
+    cache = tuple(at(mid + 8192 * i, dev(p)) for i, p in enumerate(planes))
+    pos_d, lens_d = at(mid + 40960, i32(pos)), at(mid + 40960 + 1024, i32(lens))
+    want = line.clone()
+    exp = kr.values(planes[0], planes[1], kind).astype(np.float32), kr.values(planes[2], planes[3], kind).astype(np.float32)
+    for begin, f in zip((k0, v0), exp):
+        w = want[begin:].view(dt(dst)).as_strided((rows, T, width), (pitch // elt, tok, 1))
+        for m in range(rows):
+            x = f[m, :, pos[m]:pos[m] + T].transpose(1, 0, 2).reshape(T, width)
+            w[m].copy_(dev(x, dt(dst)))
+    native.kvq_load(cache, ko, vo, pos=pos_d, lens=lens_d)
+    assert t.equal(line, want)
+    no_error()
+    if T > 1:                                       # K's second token is V's first
+        with pytest.raises(native.Q8Error):
+            native.kvq_load(cache, ko[:, :T - 1], ko[:, 1:], pos=pos_d)
+    with pytest.raises(native.Q8Error):
+        native.kvq_load(cache, ko, ko, pos=pos_d)
