@@ -107,10 +107,11 @@ cudaError_t launch_attn(const AttnArgs& a, const LaunchCtx& ctx) {
     p.gsz = block_heads(group);
     p.nb = int((group + p.gsz - 1) / p.gsz);
     p.cap = visible_cap(a.n_pos, a.window, a.sinks);
-    // all tiles of all units number below 2^31: a stage of all warps holds 8
-    // entries at least, and a unit counts at most 16 tiles more
+    // all tiles of all units number below 2^31, with the last one of each, which need not
+    // be whole, and those it counts more
     p.tile_its = 1;
-    while (a.rows * a.kv_heads * p.nb * (p.cap / (8 * p.tile_its) + 17) > INT32_MAX) p.tile_its *= 2;
+    while (a.rows * a.kv_heads * p.nb * (p.cap / (kAttnLeastStage * p.tile_its) + 1 + kAttnMostExtra) > INT32_MAX)
+        p.tile_its *= 2;
     p.qscale = float(double(a.scale) * 1.4426950408889634);
     p.err = ctx.dev_err;
     unsigned char* ws = static_cast<unsigned char*>(a.ws) + kCounterBytes;

@@ -66,6 +66,10 @@ constexpr int kKvqMaxCtas = 640;
 static_assert(4 * kKvqMaxCtas <= kCounterBytes, "one ticket a CTA");
 constexpr int kvq_block_heads(int heads) { return heads <= 4 ? 4 : 8; }
 
+// What bounds the number of tiles of a call: the entries of a stage of all warps at least, and
+// the tiles that a unit counts for its begin and end at most (4-bit heads of 32 values).
+constexpr int kAttnLeastStage = 8, kAttnMostExtra = 26;
+
 // Floats of a partial state, whole 16-byte words.
 __host__ __device__ constexpr size_t attn_slot(int ng, int64_t dim) {
     return size_t(ng) * size_t(dim) + size_t(ng == 1 ? 4 : 2 * ng);
@@ -420,6 +424,7 @@ struct AttnLanes {
 template <class T>
 __global__ void __launch_bounds__(kAttnThreads, T::CTAS) attn_kernel(const AttnParams p) {
     constexpr int NG = T::NG, WARPS = kAttnWarps / T::SPLIT;      // warps that share a stage's entries
+    static_assert(T::TK >= kAttnLeastStage && T::EXTRA <= kAttnMostExtra, "launch_attn's bound on the tiles of a call");
     extern __shared__ __align__(256) unsigned char ring_raw[];
     unsigned char* const ring_all = ring_raw + (512 - (smem_u32(ring_raw) & 511) & 511);   // stages on whole rows
     __shared__ uint32_t s_pre[Q8_MAX_ROWS + 1];   // tiles before each row
