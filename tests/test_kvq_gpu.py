@@ -128,6 +128,17 @@ def test_store_long_prompts(kind, rows, T, kv_heads, dim):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("src", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,T,kv_heads,dim", [(1, 401, 8, 128), (1, 701, 8, 128), (1, 2051, 8, 128), (3, 1003, 5, 96)])
+def test_store_prompts_between_short_and_long(kind, src, rows, T, kv_heads, dim):
+    """Several tokens a thread: stores in one turn, loads in one and two (on 148 to 160 SMs; four in f32), none of
+    whose shares T is a multiple of."""
+    lens = [T - 13, T, 517][:rows]
+    store_and_check(kind, src, rows, T, kv_heads, dim, T + 3, [2, 0, 3][:rows], lens=lens, seed=T)
+    store_and_check(kind, src, rows, T, kv_heads, dim, T - 5, [0, -3, 2][:rows], seed=T + 1, error=2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("src", FLOATS)
 def test_long_prompts_are_their_pieces(kind, src):
     """The longest walks of a store and a load against calls of some tokens each."""
