@@ -468,10 +468,10 @@ q8_status kvq_store(const void* k, const void* v, int src_type, int64_t ld_row, 
  * device error 2.
  *   pos      int32 [rows] or NULL: 0
  *   lens     int32 [rows] or NULL: T
- * Rows and tokens of k and v must not overlap one another (Q8_ERR_SHAPE), nor
- * may a value written lie in the other one's values, in the cache, pos or lens
- * (Q8_ERR_ARG).  What lies between the values does not count: k and v may be
- * columns of the same rows.
+ * Rows of k and of v lie behind one another, or all rows' token t before any
+ * row's t + 1, and overlap nowhere (Q8_ERR_SHAPE); no value written may lie in
+ * the other one's values, in the cache, pos or lens (Q8_ERR_ARG).  What lies
+ * between the values does not count: k and v may be columns of the same rows.
  */
 q8_status kvq_load(int kvq_type, const void* k_codes, const void* k_words, const void* v_codes,
                    const void* v_words, int64_t rows, int64_t n_pos, int64_t kv_heads,

@@ -30,7 +30,7 @@
 // cut evenly over the CTAs, so ragged batches balance and one long sequence fills
 // the GPU (few units, fewer CTAs: the join of many parts would be the time);
 // lengths are read on the device, so one captured graph serves every step.  Two CTAs of four
-// warps an SM: one streams while the other ends a unit.
+// warps an SM (quantised caches: T::CTAS): one streams while the other ends a unit.
 //
 // Measured (32 query and 8 K/V heads of 128 values; device time): 64 rows of
 // 4100 to 8192 bf16 entries 240 to 248 us (by the box), 6.5 to 6.7 TB/s; 16 rows
@@ -51,7 +51,7 @@
 
 namespace q8 {
 
-constexpr int kAttnWarps = 4;                         // two CTAs an SM
+constexpr int kAttnWarps = 4;                         // T::CTAS CTAs an SM
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnRing = 24 * 1024;                  // bytes a warp
 constexpr int kAttnMaxCtas = 512;

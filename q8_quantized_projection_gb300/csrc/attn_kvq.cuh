@@ -28,13 +28,17 @@
 // scale the scores), a product holds a scheduler's issue for some 5 clocks beside its 8 of the
 // tensor pipe, and together they take some 600 clocks where the bytes at HBM's rate take 430:
 // 0.58 issued a clock with two to four warps a scheduler alike.  Eight bits: HBM, with eight
-// query heads the instructions again.  And some 15 us a call to begin and to end: the launch,
-// positions, q as operands, the first stages, the join of parts.  tcgen05 would take the
-// products out of the way, but not what is around them, and V's scales, one a block of values
-// and not of entries, make the second product's other operand another one for every 32 values:
-// its smallest tile (64 or 128 values) would read all of V's 16-bit operand from shared memory
-// for every block of it, 128 KB for 128 entries of 128 values, more clocks than their bytes
-// take.
+// query heads the instructions again.  Beside its bytes, a call that fills the GPU has some us
+// that do not grow with the entries (a line through 16 rows of 2048 to 49152: 4 bits 13 us with
+// four query heads, 17 with eight, 8 bits 10 and 15): the launch, positions, q as operands, the
+// first stages, the join of parts.  tcgen05 would take the products out of the way, but not
+// what is around them.  V's scales, one a block of values and not of entries, make the second
+// product's other operand another one for every 32 values: its smallest tile (64 or 128
+// values) would read all of V's 16-bit operand from shared memory for every block of it, 128
+// KB for 128 entries of 128 values, more clocks than their bytes take.  The first product,
+// whose scales are factors of its results, was not tried there: it wants K's codes unpacked in
+// shared memory, 8 stores of 16 bytes a lane for 16 entries of 128 values, as many as its
+// matrix instructions are now with four heads.
 //
 // Measured (16 rows of 16384 entries, 8 K/V heads of 128 values; device time): 4 bits, four query
 // heads 77 us, 4.4 TB/s (5.6 TB/s between 16384 and 32768 entries), eight 108 us; 8 bits 107 us,

@@ -5,8 +5,8 @@
 // one head as it has threads for, whose codes and words are one run of the cache, or, where
 // a row has fewer tokens, those of several heads.
 //
-// What bounds them.  Long prompts: a store of 16-bit floats its instructions (some 18 a
-// value, of which 9 are the code and, where a quotient near it is near a half, 13 more to
+// What bounds them.  Long prompts: a store of 16-bit floats its instructions (0.8 issued a clock; some
+// 18 a value, of which 9 are the code and, where a quotient near it is near a half, 13 more to
 // decide it; 4 rows of 16384 tokens, 8 K/V heads of 128 values: bf16 80 us in 4 bits, 85 in
 // 8, 4.4 and 4.9 TB/s; binary32 102 and 111, 6.1 and 6.2 TB/s); a load HBM (58 and 66 us into
 // bf16, 98 and 106 into binary32, 6.1 to 6.5 TB/s).  Single tokens: the launch, 1.8 us each.
@@ -431,8 +431,10 @@ cudaError_t launch_io_tokens(const KvqIoArgs& a, const LaunchCtx& ctx) {
     // Several tokens a thread, and turns of them, as soon as there are threads for it (us, by turns of
     // none, 1 and 4: 1 row of 512 tokens of 8 heads of 128 values, bf16 in 4 bits, stored 2.6, 2.6, 4.5,
     // read back 3.5, 2.2, 3.2; of 2048: 6.0, 5.4, 5.6 and 6.8, 4.7, 3.8; 8 rows of 2048: 38, 32, 24 and
-    // 45, 21, 14).  Two turns of a load just below (3 rows of 1001, 5 heads of 96: one 4.7, two 3.3, four
-    // 4.0; that row of 2048: 3.6), eight of a store from some more on (4 rows of 8192: 43.6 and 42.3).
+    // 45, 21, 14).  Two turns of a load just below (one, two and four, 4 bits into bf16: 3 rows of 1001 tokens
+    // of 5 heads of 96, 2371 threads an SM, 4.6, 3.2, 4.0, that row of 2048, 3449 threads, 4.6, 3.5, 3.8;
+    // above, 3 x 1001 into f32, 4742 threads, 4.5, 5.7, 4.3, from 8 bits 4.8, 4.1, 4.1), eight of a store
+    // from some more on (4 rows of 8192: 43.6 and 42.3).
     constexpr int V = STORE ? kStored : kLoaded<F>, R = STORE ? 2 : 4;
     const int64_t threads = a.rows * a.T * a.kv_heads * (2 * a.dim / V), sms = ctx.num_sms;
     const int64_t tb = kThreads / (a.dim / V);
